@@ -202,7 +202,7 @@ def _gate(st):
     g = st["gate"]
     if g is None:
         return 1.0
-    return g.float()[:, None] if st["case"]["gate"] == "token" else g.float()
+    return g.float()
 
 
 def _plain_norm_fwd(st):
@@ -242,7 +242,7 @@ def _plain_norm_bwd(st):
          "dw_post": (dp * yh).sum(0), "dw_pre": (dn * th).sum(0)}
     if c["gate"] != "none":
         dg = ALPHA * yh * st["w_post"] * grad
-        o["dgate"] = {"channel": lambda: dg.sum(0), "token": lambda: dg.sum(1),
+        o["dgate"] = {"channel": lambda: dg.sum(0), "token": lambda: dg.sum(1, keepdim=True),
                       "full": lambda: dg.to(torch.bfloat16)}[c["gate"]]()
     return o
 
@@ -387,7 +387,7 @@ def prepare(case, seed):
         st["gate"] = {
             "none": lambda: None,
             "channel": lambda: 0.5 + 0.1 * torch.randn((cols,), generator=gen, device=DEV),
-            "token": lambda: torch.sigmoid(torch.randn((rows,), generator=gen, device=DEV)),
+            "token": lambda: torch.sigmoid(torch.randn((rows, 1), generator=gen, device=DEV)),
             "full": lambda: torch.sigmoid(torch.randn((rows, cols), generator=gen,
                                                       device=DEV)).to(bf16)}[c["gate"]]()
         if op == "norm_fwd":
@@ -409,7 +409,7 @@ def prepare(case, seed):
         st["dn"] = _acts(gen, rows, cols, 1e-3).to(bf16)
         st["dr_out"] = _acts(gen, rows, cols, 1e-3).to(res)
         dgate = {"none": lambda: None, "channel": lambda: _empty((cols,), torch.float32),
-                 "token": lambda: _empty((rows,), torch.float32),
+                 "token": lambda: _empty((rows, 1), torch.float32),
                  "full": lambda: _empty((rows, cols), bf16)}[c["gate"]]()
         st["out"] = (_empty((rows, cols), res), _empty((rows, cols), bf16),
                      _empty((cols,), torch.float32), _empty((cols,), torch.float32), dgate)
@@ -498,8 +498,6 @@ def exact(case, seed):
         gate = torch.ones((1, 1), dtype=torch.float64, device=DEV)
         if st["gate"] is not None:
             gate = st["gate"].double()
-            gate = {"channel": gate.view(1, -1), "token": gate.view(-1, 1),
-                    "full": gate}[c["gate"]]
     if op == "norm_fwd":
         y, r = st["y"].double(), st["r"].double()
         iy = (y.square().sum(1) / c["cols"] + EPS) ** -0.5
@@ -531,7 +529,8 @@ def exact(case, seed):
         if c["gate"] != "none":
             dg = ALPHA * total * y * iy * wp
             o["dgate"] = (dg if c["gate"] == "full" else
-                          dg.sum(0) if c["gate"] == "channel" else dg.sum(1))
+                          dg.sum(0) if c["gate"] == "channel" else
+                          dg.sum(1, keepdim=True))
     elif op == "swiglu_fwd":
         f = c["f"]
         g, u = st["gu"][:, :f].double(), st["gu"][:, f:].double()
