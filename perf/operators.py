@@ -180,7 +180,7 @@ def _encode(x, pow2):
         s = torch.where(e > -127, _power(e), torch.full_like(a, 2.0 ** -127))
         r = _power(-e)
     else:
-        s, r = a / 448.0, 448.0 / a
+        s, r = a / 448.0, torch.full_like(a, 448.0) / a     # each one rounding
     one = torch.ones_like(a)
     s, r = torch.where(amax == 0, one, s), torch.where(amax == 0, one, r)
     q = torch.clamp(v * r, -448.0, 448.0).to(FP8)
