@@ -24,6 +24,14 @@ __all__ = [
     "puro_fp8_gemm_fwd_pow2",
     "puro_fp8_gemm_dgrad_pow2",
     "puro_fp8_gemm_wgrad_pow2",
+    "puro_ckpt_pack",
+    "puro_ckpt_unpack",
+    "puro_ckpt_transpose",
+    "puro_block_norm_fwd",
+    "puro_block_norm_bwd",
+    "puro_swiglu_fwd",
+    "puro_swiglu_bwd",
+    "puro_swiglu_bwd_fp8",
 ]
 
 

@@ -29,6 +29,30 @@ class PuroAdamWParams(ctypes.Structure):
                 ("step", ctypes.c_int64)]
 
 
+class PuroBlockNorm(ctypes.Structure):
+    """puro_block_norm: one forward block norm."""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("rows", "cols")]
+                + [(k, ctypes.c_int) for k in ("residual_type", "gate_kind", "pow2")]
+                + [(k, ctypes.c_float) for k in ("alpha", "beta", "eps")]
+                + [(k, ctypes.c_void_p) for k in
+                   ("y", "r", "w_post", "w_pre", "gate", "r_out", "n", "nq", "ns", "rstd_y",
+                    "rstd_r", "yq", "ys", "rq", "rs")])
+
+
+class PuroBlockNormGrad(ctypes.Structure):
+    """puro_block_norm_grad: one backward block norm."""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("rows", "cols")]
+                + [(k, ctypes.c_int) for k in ("residual_type", "gate_kind", "accumulate")]
+                + [(k, ctypes.c_float) for k in ("alpha", "beta")]
+                + [(k, ctypes.c_void_p) for k in
+                   ("dr_out", "dn", "y", "yq", "ys", "r", "rq", "rs", "rstd_y", "rstd_r",
+                    "w_post", "w_pre", "gate", "dr", "dy", "dw_post", "dw_pre", "dgate")])
+
+
+TYPE_BF16, TYPE_FP32 = 0, 1                                     # PURO_TYPE_*
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3     # PURO_GATE_*
+NORM_MAX_COLS = 16384                                           # PURO_NORM_MAX_COLS
+
 OPT_MAX_BLOCKS = 2048  # PURO_OPT_MAX_BLOCKS
 OPT_WORKSPACE_BYTES = 8 * OPT_MAX_BLOCKS + 256  # PURO_OPT_WORKSPACE_BYTES
 
@@ -54,6 +78,18 @@ SIGNATURES.update({
     "puro_hyperball_step_noalloc": ([_P, _P, _I64, ctypes.c_float, _P, _P, _P], ctypes.c_int),
     "puro_adamw_step": ([_P, _P, _P, _P, _I64, ctypes.POINTER(PuroAdamWParams), _P, _P],
                         ctypes.c_int),
+})
+_INT = ctypes.c_int
+SIGNATURES.update({
+    "puro_ckpt_pack": ([_P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P], _INT),
+    "puro_ckpt_unpack": ([_P, _P, _I64, _I64, _P, _INT, _I64, _P], _INT),
+    "puro_ckpt_transpose": ([_P, _P, _I64, _I64, _INT, _P, _P, _P], _INT),
+    "puro_block_norm_fwd": ([ctypes.POINTER(PuroBlockNorm), _P], _INT),
+    "puro_block_norm_workspace": ([_I64, _I64], _I64),
+    "puro_block_norm_bwd": ([ctypes.POINTER(PuroBlockNormGrad), _P, _P], _INT),
+    "puro_swiglu_fwd": ([_P, _I64, _I64, _P, _P, _P, _P, _P, _INT, _P], _INT),
+    "puro_swiglu_bwd": ([_P, _P, _P, _P, _I64, _I64, _P, _P], _INT),
+    "puro_swiglu_bwd_fp8": ([_P, _P, _P, _P, _I64, _I64, _INT] + [_P] * 7, _INT),
 })
 # The power-of-two-scale variants take the same arguments as their standard counterparts.
 POW2_BASES = ("puro_quant_act_1x128", "puro_quant_w_128x128", "puro_quant_w_128x128_group",

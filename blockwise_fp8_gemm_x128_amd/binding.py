@@ -8,11 +8,13 @@ computation runs in libpuro's HIP kernels; there is no other code path.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple, Optional
 
 import torch
 
-from ._lib import (OPT_WORKSPACE_BYTES, W_GROUP_MAX, PuroAdamWParams, PuroError, PuroWItem,
-                   check, lib)
+from ._lib import (GATE_CHANNEL, GATE_FULL, GATE_NONE, GATE_TOKEN, OPT_WORKSPACE_BYTES, TYPE_BF16,
+                   TYPE_FP32, W_GROUP_MAX, PuroAdamWParams, PuroBlockNorm, PuroBlockNormGrad,
+                   PuroError, PuroWItem, check, lib)
 
 FP8 = torch.uint8  # E4M3 codes travel as raw bytes
 
@@ -245,6 +247,351 @@ def puro_adamw_step(p, g, m, v, lr, beta1, beta2, eps, weight_decay, step, p_bf1
                                 p.numel(), ctypes.byref(hp),
                                 None if p_bf16 is None else p_bf16.data_ptr(), _stream(dev)))
     return p_bf16
+
+
+# ---------------------------------------------------------------- between the GEMMs
+# 8-bit checkpoints are pairs (codes uint8 [rows, cols], scales fp32 [ceil(cols/128), rows]).
+_TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_FP32}
+
+
+def _groups(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _new_codes(rows, cols, dev):
+    return (torch.empty((rows, cols), dtype=FP8, device=dev),
+            torch.empty((_groups(cols), rows), dtype=torch.float32, device=dev))
+
+
+def _need_codes(q, s, name, rows, cols, dev, groups=None) -> None:
+    _need(q, name + " codes", FP8, (rows, cols), dev)
+    _need(s, name + " scales", torch.float32, (groups or _groups(cols), rows), dev)
+
+
+def _need_rows(x, name, dev):
+    """A 2-D bf16 or fp32 matrix with unit column stride; returns (type, row stride)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _TYPES:
+        raise PuroError(f"{name}: expected a bf16 or fp32 matrix")
+    if x.device != dev:
+        raise PuroError(f"{name}: on {x.device}, expected {dev}")
+    rows, cols = x.shape
+    ld = x.stride(0) if rows > 1 else cols
+    if (cols > 1 and x.stride(1) != 1) or ld < cols:
+        raise PuroError(f"{name}: columns must be adjacent and rows must not overlap")
+    return _TYPES[x.dtype], ld
+
+
+def puro_ckpt_pack(x: torch.Tensor, q=None, s=None, pow2: bool = False):
+    """8-bit checkpoint of x, bf16 or fp32 [rows, cols] (any sizes, rows may be strided) ->
+    (q uint8 E4M3 [rows, cols], s fp32 [ceil(cols/128), rows])."""
+    dev = _dev(x)
+    kind, ld = _need_rows(x, "x", dev)
+    rows, cols = x.shape
+    q = _out(q, "q", FP8, (rows, cols), dev)
+    s = _out(s, "s", torch.float32, (_groups(cols), rows), dev)
+    check(lib().puro_ckpt_pack(x.data_ptr(), kind, rows, cols, ld, bool(pow2), q.data_ptr(),
+                               s.data_ptr(), _stream(dev)))
+    return q, s
+
+
+def puro_ckpt_unpack(q, s, x=None, dtype=torch.bfloat16):
+    """The values a checkpoint stands for, as `dtype` (bf16 or fp32) or into x (rows may be
+    strided)."""
+    dev = _dev(q)
+    rows, cols = q.shape
+    _need_codes(q, s, "checkpoint", rows, cols, dev)
+    if x is None:
+        x = torch.empty((rows, cols), dtype=dtype, device=dev)
+    kind, ld = _need_rows(x, "x", dev)
+    if tuple(x.shape) != (rows, cols):
+        raise PuroError(f"x: shape {tuple(x.shape)}, expected {(rows, cols)}")
+    check(lib().puro_ckpt_unpack(q.data_ptr(), s.data_ptr(), rows, cols, x.data_ptr(), kind, ld,
+                                 _stream(dev)))
+    return x
+
+
+def puro_ckpt_transpose(q, s, qt=None, st=None, pow2: bool = False):
+    """Checkpoint [rows, cols] -> checkpoint of its transpose (qt uint8 [cols, rows], st fp32
+    [ceil(rows/128), cols]): a forward GEMM operand becomes the weight gradient's."""
+    dev = _dev(q)
+    rows, cols = q.shape
+    _need_codes(q, s, "checkpoint", rows, cols, dev)
+    qt = _out(qt, "qt", FP8, (cols, rows), dev)
+    st = _out(st, "st", torch.float32, (_groups(rows), cols), dev)
+    check(lib().puro_ckpt_transpose(q.data_ptr(), s.data_ptr(), rows, cols, bool(pow2),
+                                    qt.data_ptr(), st.data_ptr(), _stream(dev)))
+    return qt, st
+
+
+class BlockNorm(NamedTuple):
+    """Outputs of puro_block_norm_fwd; None where left out."""
+    r_out: Optional[torch.Tensor]    # residual type [rows, cols]
+    n: Optional[torch.Tensor]        # bf16 [rows, cols]
+    nq: Optional[torch.Tensor]       # n as an FP8 operand
+    ns: Optional[torch.Tensor]
+    rstd_y: Optional[torch.Tensor]   # fp32 [rows]
+    rstd_r: Optional[torch.Tensor]
+    yq: Optional[torch.Tensor]       # checkpoint of y
+    ys: Optional[torch.Tensor]
+    rq: Optional[torch.Tensor]       # checkpoint of r_out
+    rs: Optional[torch.Tensor]
+
+
+class BlockNormGrads(NamedTuple):
+    """Outputs of puro_block_norm_bwd; None where left out."""
+    dr: Optional[torch.Tensor]
+    dy: Optional[torch.Tensor]
+    dw_post: Optional[torch.Tensor]
+    dw_pre: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+
+
+def _gate(gate, rows, cols, dev, name="gate"):
+    """fp32 [cols] is a gate per channel, fp32 [rows, 1] one per token, bf16 [rows, cols] one per
+    element. Returns (kind, pointer)."""
+    if gate is None:
+        return GATE_NONE, None
+    if gate.dim() == 1:
+        kind, dtype, shape = GATE_CHANNEL, torch.float32, (cols,)
+    elif gate.dtype == torch.float32:
+        kind, dtype, shape = GATE_TOKEN, torch.float32, (rows, 1)
+    else:
+        kind, dtype, shape = GATE_FULL, torch.bfloat16, (rows, cols)
+    _need(gate, name, dtype, shape, dev)
+    return kind, gate.data_ptr()
+
+
+def puro_block_norm_fwd(y, r, w_post, w_pre, gate=None, alpha: float = 1.0, beta: float = 1.0,
+                        eps: float = 1e-6, n: str = "fp8", ckpt: bool = True,
+                        pow2: bool = False, out=None) -> BlockNorm:
+    """r_out = beta r + alpha gate * rmsnorm(y) w_post; n = rmsnorm(r_out) w_pre, in one pass.
+
+    y bf16 [rows, cols] (None: only the norm before a block, r_out = beta r), r bf16 or fp32
+    [rows, cols], w_post / w_pre fp32 [cols] (w_pre None: only the norm after a block), gate None,
+    fp32 [cols], fp32 [rows, 1] or bf16 [rows, cols]. `n`: "fp8" (codes and scales, the next
+    GEMM's operand), "bf16" or "both"; `ckpt`: also 8-bit checkpoints of y and r_out. `out`: the
+    ten outputs to write (a BlockNorm or a tuple in its order, None to leave one out) instead of
+    new ones; out.r_out may be r."""
+    dev = _dev(r)
+    if r.dim() != 2 or r.dtype not in _TYPES:
+        raise PuroError("r: expected a bf16 or fp32 matrix")
+    rows, cols = shape = tuple(r.shape)
+    f32, bf16 = torch.float32, torch.bfloat16
+    _need(r, "r", r.dtype, shape, dev)
+    post, pre = y is not None, w_pre is not None
+    if post:
+        _need(y, "y", bf16, shape, dev)
+        _need(w_post, "w_post", f32, (cols,), dev)
+    if pre:
+        _need(w_pre, "w_pre", f32, (cols,), dev)
+    kind, gp = _gate(gate, rows, cols, dev)
+    if out is None:
+        if n not in ("fp8", "bf16", "both"):
+            raise PuroError("n: expected 'fp8', 'bf16' or 'both'")
+        none = (None, None)
+        out = BlockNorm(
+            torch.empty_like(r) if post or beta != 1.0 else None,
+            torch.empty(shape, dtype=bf16, device=dev) if pre and n != "fp8" else None,
+            *(_new_codes(rows, cols, dev) if pre and n != "bf16" else none),
+            torch.empty((rows,), dtype=f32, device=dev) if post else None,
+            torch.empty((rows,), dtype=f32, device=dev) if pre else None,
+            *(_new_codes(rows, cols, dev) if post and ckpt else none),
+            *(_new_codes(rows, cols, dev) if ckpt else none))
+    else:
+        out = BlockNorm(*out)
+        for t, name, dtype, want in ((out.r_out, "r_out", r.dtype, shape),
+                                     (out.n, "n", bf16, shape),
+                                     (out.rstd_y, "rstd_y", f32, (rows,)),
+                                     (out.rstd_r, "rstd_r", f32, (rows,))):
+            if t is not None:
+                _need(t, name, dtype, want, dev)
+        for q, s, name in ((out.nq, out.ns, "n"), (out.yq, out.ys, "y"), (out.rq, out.rs, "r")):
+            if q is not None or s is not None:
+                _need_codes(q, s, name, rows, cols, dev)
+    d = PuroBlockNorm(rows, cols, _TYPES[r.dtype], kind, bool(pow2), alpha, beta, eps, _ptr(y),
+                      r.data_ptr(), _ptr(w_post) if post else None, _ptr(w_pre), gp,
+                      *map(_ptr, out))
+    check(lib().puro_block_norm_fwd(ctypes.byref(d), _stream(dev)))
+    return out
+
+
+def _saved(x, name, dtype, shape, dev, where):
+    """A saved activation, as it was or as its checkpoint (codes, scales): (x, q, s) pointers."""
+    if x is None:
+        if where:
+            raise PuroError(f"{name}: required")
+        return None, None, None
+    if isinstance(x, (tuple, list)):
+        q, s = x
+        _need_codes(q, s, name, *shape, dev)
+        return None, q.data_ptr(), s.data_ptr()
+    _need(x, name, dtype, shape, dev)
+    return x.data_ptr(), None, None
+
+
+def block_norm_workspace(rows: int, cols: int, dev) -> torch.Tensor:
+    """Device workspace of puro_block_norm_bwd for these sizes."""
+    size = lib().puro_block_norm_workspace(rows, cols)
+    return torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+
+
+def puro_block_norm_bwd(dr_out, dn, y, r_out, rstd_y, rstd_r, w_post, w_pre, gate=None,
+                        alpha: float = 1.0, beta: float = 1.0, accumulate: bool = False,
+                        workspace=None, out=None) -> BlockNormGrads:
+    """Gradients of puro_block_norm_fwd from those of r_out (dr_out, None for zero) and n (dn
+    bf16, None if w_pre was). y and r_out: the saved tensors, or their checkpoints as (codes,
+    scales) pairs; rstd_y None: the norm after the block was left out. accumulate adds dw_post,
+    dw_pre and a channel gate's gradient to `out`'s. `out`: the five outputs to write (None to
+    skip; out.dr may be dr_out)."""
+    f32, bf16 = torch.float32, torch.bfloat16
+    post, pre = rstd_y is not None, dn is not None
+    lead = dr_out if dr_out is not None else dn
+    if lead is None:
+        raise PuroError("dr_out and dn: at least one is required")
+    dev = _dev(lead)
+    rows, cols = shape = tuple(lead.shape)
+    res = (dr_out.dtype if dr_out is not None else
+           r_out.dtype if isinstance(r_out, torch.Tensor) else
+           out[0].dtype if out is not None and out[0] is not None else bf16)
+    if res not in _TYPES:
+        raise PuroError("dr_out: expected bf16 or fp32")
+    if dr_out is not None:
+        _need(dr_out, "dr_out", res, shape, dev)
+    if post:
+        _need(rstd_y, "rstd_y", f32, (rows,), dev)
+        _need(w_post, "w_post", f32, (cols,), dev)
+    if pre:
+        _need(dn, "dn", bf16, shape, dev)
+        _need(rstd_r, "rstd_r", f32, (rows,), dev)
+        _need(w_pre, "w_pre", f32, (cols,), dev)
+    ys = _saved(y if post else None, "y", bf16, shape, dev, post)
+    rs = _saved(r_out if pre else None, "r_out", res, shape, dev, pre)
+    kind, gp = _gate(gate, rows, cols, dev)
+    if out is None:
+        if accumulate:
+            raise PuroError("accumulate=True needs existing gradients in out")
+        vec = lambda: torch.empty((cols,), dtype=f32, device=dev)  # noqa: E731
+        out = BlockNormGrads(torch.empty(shape, dtype=res, device=dev),
+                             torch.empty(shape, dtype=bf16, device=dev) if post else None,
+                             vec() if post else None, vec() if pre else None,
+                             torch.empty_like(gate) if gate is not None else None)
+    else:
+        out = BlockNormGrads(*out)
+        for t, name, dtype, want in ((out.dr, "dr", res, shape), (out.dy, "dy", bf16, shape),
+                                     (out.dw_post, "dw_post", f32, (cols,)),
+                                     (out.dw_pre, "dw_pre", f32, (cols,))):
+            if t is not None:
+                _need(t, name, dtype, want, dev)
+        if gate is not None:
+            _need(out.dgate, "dgate", gate.dtype, tuple(gate.shape), dev)
+    need = lib().puro_block_norm_workspace(rows, cols)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or workspace.numel() * workspace.element_size() < need:
+        raise PuroError(f"workspace: {need} bytes on {dev} needed")
+    d = PuroBlockNormGrad(rows, cols, _TYPES[res], kind, bool(accumulate), alpha, beta,
+                          _ptr(dr_out), _ptr(dn), *ys, *rs, _ptr(rstd_y),
+                          rstd_r.data_ptr() if pre else None, w_post.data_ptr() if post else None,
+                          w_pre.data_ptr() if pre else None, gp, *map(_ptr, out))
+    check(lib().puro_block_norm_bwd(ctypes.byref(d), workspace.data_ptr(), _stream(dev)))
+    return out
+
+
+class SwiGLU(NamedTuple):
+    """Outputs of puro_swiglu_fwd; None where left out."""
+    h: Optional[torch.Tensor]        # bf16 [rows, f]
+    hq: Optional[torch.Tensor]       # h as an FP8 operand
+    hs: Optional[torch.Tensor]
+    guq: Optional[torch.Tensor]      # checkpoint of gu: codes [rows, 2f]
+    gus: Optional[torch.Tensor]      # scales [2 ceil(f/128), rows], g's groups first
+
+
+class SwiGLUOperands(NamedTuple):
+    """Outputs of puro_swiglu_bwd_fp8: the FP8 operands of the GEMMs that follow."""
+    dguq: torch.Tensor               # dgu [rows, 2f]: gate_up's data gradient
+    dgus: torch.Tensor
+    dgutq: torch.Tensor              # dgu transposed [2f, rows]: gate_up's weight gradient
+    dguts: torch.Tensor
+    htq: torch.Tensor                # h transposed [f, rows]: down's weight gradient
+    hts: torch.Tensor
+
+
+def _half(cols, name):
+    if cols % 2:
+        raise PuroError(f"{name}: {cols} columns, expected an even number (g and u)")
+    return cols // 2
+
+
+def puro_swiglu_fwd(gu, h: bool = False, fp8: bool = True, ckpt: bool = True, pow2: bool = False,
+                    out=None) -> SwiGLU:
+    """h = u g sigmoid(g) from gu = [g | u], bf16 [rows, 2f]. `h`: h in bf16; `fp8`: h as the down
+    projection's operand; `ckpt`: an 8-bit checkpoint of gu. `out`: the five outputs to write
+    (None to leave one out) instead of new ones."""
+    dev = _dev(gu)
+    rows, cols = gu.shape
+    f = _half(cols, "gu")
+    _need(gu, "gu", torch.bfloat16, (rows, cols), dev)
+    if out is None:
+        none = (None, None)
+        out = SwiGLU(torch.empty((rows, f), dtype=torch.bfloat16, device=dev) if h else None,
+                     *(_new_codes(rows, f, dev) if fp8 else none),
+                     *((torch.empty((rows, cols), dtype=FP8, device=dev),
+                        torch.empty((2 * _groups(f), rows), dtype=torch.float32, device=dev))
+                       if ckpt else none))
+    else:
+        out = SwiGLU(*out)
+        if out.h is not None:
+            _need(out.h, "h", torch.bfloat16, (rows, f), dev)
+        if out.hq is not None or out.hs is not None:
+            _need_codes(out.hq, out.hs, "h", rows, f, dev)
+        if out.guq is not None or out.gus is not None:
+            _need_codes(out.guq, out.gus, "gu", rows, cols, dev, 2 * _groups(f))
+    check(lib().puro_swiglu_fwd(gu.data_ptr(), rows, f, *map(_ptr, out), bool(pow2),
+                                _stream(dev)))
+    return out
+
+
+def _swiglu_saved(dh, gu):
+    dev = _dev(dh)
+    rows, f = dh.shape
+    _need(dh, "dh", torch.bfloat16, (rows, f), dev)
+    if isinstance(gu, (tuple, list)):
+        q, s = gu
+        _need_codes(q, s, "gu", rows, 2 * f, dev, 2 * _groups(f))
+        return dev, rows, f, (None, q.data_ptr(), s.data_ptr())
+    _need(gu, "gu", torch.bfloat16, (rows, 2 * f), dev)
+    return dev, rows, f, (gu.data_ptr(), None, None)
+
+
+def puro_swiglu_bwd(dh, gu, dgu=None):
+    """dgu bf16 [rows, 2f] from dh bf16 [rows, f] and gu: bf16 [rows, 2f], or its checkpoint as a
+    (codes, scales) pair."""
+    dev, rows, f, src = _swiglu_saved(dh, gu)
+    dgu = _out(dgu, "dgu", torch.bfloat16, (rows, 2 * f), dev)
+    check(lib().puro_swiglu_bwd(dh.data_ptr(), *src, rows, f, dgu.data_ptr(), _stream(dev)))
+    return dgu
+
+
+def puro_swiglu_bwd_fp8(dh, gu, pow2: bool = False, out=None) -> SwiGLUOperands:
+    """puro_swiglu_bwd straight to the FP8 operands of gate_up's data and weight gradients, and
+    h's transposed copy for down's weight gradient. rows and f: multiples of 128. `out`: the six
+    outputs to write instead of new ones."""
+    dev, rows, f, src = _swiglu_saved(dh, gu)
+    if out is None:
+        out = SwiGLUOperands(*_new_codes(rows, 2 * f, dev), *_new_codes(2 * f, rows, dev),
+                             *_new_codes(f, rows, dev))
+    else:
+        out = SwiGLUOperands(*out)
+        _need_codes(out.dguq, out.dgus, "dgu", rows, 2 * f, dev)
+        _need_codes(out.dgutq, out.dguts, "dgut", 2 * f, rows, dev)
+        _need_codes(out.htq, out.hts, "ht", f, rows, dev)
+    check(lib().puro_swiglu_bwd_fp8(dh.data_ptr(), *src, rows, f, bool(pow2), *map(_ptr, out),
+                                    _stream(dev)))
+    return out
 
 
 def _pow2_variant(base):

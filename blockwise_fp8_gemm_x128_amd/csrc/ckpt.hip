@@ -1,0 +1,187 @@
+// 8-bit activation checkpoints for gfx950: a bf16 or fp32 matrix of any size stored as E4M3 codes
+// with one fp32 scale per 128 columns of a row, read back, and requantised along its rows for the
+// weight-gradient GEMM.
+//
+// For a group x_1..x_128 with amax = max |x_i| over its finite elements: s = amax/448,
+// r = 448/amax, q_i = E4M3(x_i r), and what the checkpoint stands for is value(q_i) s. For sizes
+// that are multiples of 128 the bytes are those of the 1x128 quantiser, so an FP8 GEMM operand
+// kept from the forward pass is a checkpoint, and a checkpoint is an operand.
+//
+// All of it is bound by HBM: 3 B per element (bf16) or 5 B (fp32) packed or unpacked, 2 B
+// requantised, and 4 B of scale per group.
+#include "coltile.hpp"
+
+namespace puro {
+namespace {
+
+// ------------------------------------------------------------------ row groups
+// A 256-thread block covers 64 rows of one 128-column chunk: 16 lanes x 8 elements per row, 16
+// rows at a time, every load issued before the first group is scaled. The scales of a chunk are
+// contiguous over rows, so lane k of a 16-lane row stores those of its k-th row.
+constexpr int kPasses = 4;
+constexpr int kRowsPerBlock = 16 * kPasses;
+
+template <typename T>
+__global__ __launch_bounds__(256) void ckpt_pack_kernel(const T* __restrict__ x, int64_t rows,
+                                                        int64_t cols, int64_t ldx, int pow2,
+                                                        uint8_t* __restrict__ q,
+                                                        float* __restrict__ s) {
+  const int64_t chunks = (cols + 127) >> 7;
+  const int64_t c = blockIdx.x % chunks;
+  const int64_t r0 = blockIdx.x / chunks * kRowsPerBlock + (threadIdx.x >> 4);
+  const int l16 = threadIdx.x & 15;
+  const int64_t col = c * 128 + l16 * kVec;
+  const int n = static_cast<int>(min(cols - col, int64_t(kVec)));
+  F8 v[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int64_t row = r0 + 16 * p;
+    v[p] = load8<true>(x + row * ldx + col, row < rows ? n : 0);
+  }
+  const RowGroups<kPasses> g = row_groups<kPasses>(&v[0].f, pow2 != 0);
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int64_t row = r0 + 16 * p;
+    if (row < rows) store8(q + row * cols + col, n, encode8(g, p, v[p].f));
+  }
+  if (l16 < kPasses && r0 + 16 * l16 < rows) s[c * rows + r0 + 16 * l16] = g.s;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void ckpt_unpack_kernel(const uint8_t* __restrict__ q,
+                                                          const float* __restrict__ s,
+                                                          int64_t rows, int64_t cols, int64_t ldx,
+                                                          T* __restrict__ x) {
+  const int64_t chunks = (cols + 127) >> 7;
+  const int64_t c = blockIdx.x % chunks;
+  const int64_t r0 = blockIdx.x / chunks * kRowsPerBlock + (threadIdx.x >> 4);
+  const int64_t col = c * 128 + (threadIdx.x & 15) * kVec;
+  const int n = static_cast<int>(min(cols - col, int64_t(kVec)));
+  u32x2_el v[kPasses];
+  float sc[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int64_t row = r0 + 16 * p;
+    v[p] = load_raw<true>(q + row * cols + col, row < rows ? n : 0);
+    sc[p] = row < rows ? s[c * rows + row] : 0.0f;
+  }
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int64_t row = r0 + 16 * p;
+    float f[kVec];
+    decode8(v[p], sc[p], f);
+    if (row < rows) store8(x + row * ldx + col, n, f);
+  }
+}
+
+// ------------------------------------------------------------------ along the rows
+// Requantisation for the weight gradient: a 512-thread block decodes a 128 x 128 tile into
+// registers (4 consecutive rows x 8 columns a thread) and encodes its column groups.
+__global__ __launch_bounds__(kTileThreads) void ckpt_transpose_kernel(
+    const uint8_t* __restrict__ q, const float* __restrict__ s, int64_t rows, int64_t cols,
+    int pow2, uint8_t* __restrict__ qt, float* __restrict__ st) {
+  __shared__ ColTile<1> sh;
+  const int64_t chunks = (cols + 127) >> 7;
+  const int64_t cb = blockIdx.x % chunks, mb = blockIdx.x / chunks;
+  const int64_t col = cb * 128 + (threadIdx.x & 15) * kVec;
+  const int64_t r0 = mb * 128 + (threadIdx.x >> 4) * kTileRows;
+  const int n = static_cast<int>(min(cols - col, int64_t(kVec)));
+  u32x2_el raw[kTileRows];
+  float sc[kTileRows];
+#pragma unroll
+  for (int p = 0; p < kTileRows; ++p) {
+    raw[p] = load_raw<false>(q + (r0 + p) * cols + col, r0 + p < rows ? n : 0);
+    sc[p] = r0 + p < rows ? s[cb * rows + r0 + p] : 0.0f;
+  }
+  float v[1][kTileRows][kVec];
+#pragma unroll
+  for (int p = 0; p < kTileRows; ++p) decode8(raw[p], sc[p], v[0][p]);
+  const ColOut out[1] = {{qt, st, cols, cb * 128}};
+  col_codes<1>(sh, v, out, rows, mb, pow2 != 0);
+}
+
+puro_status check_rows(int64_t rows, int64_t cols, int64_t* blocks) {
+  *blocks = ceil_div(rows, kRowsPerBlock) * ceil_div(cols, 128);
+  return *blocks > INT32_MAX ? PURO_ERR_SHAPE : PURO_OK;
+}
+
+// The 16- or 32-bit side of a checkpoint: any row stride from cols up, element-aligned.
+puro_status check_wide(const void* x, int type, int64_t cols, int64_t ldx, bool empty) {
+  if (type != PURO_TYPE_BF16 && type != PURO_TYPE_FP32) return PURO_ERR_ARG;
+  if (ldx < cols || ldx > (int64_t(1) << 40)) return PURO_ERR_ARG;
+  if (empty) return PURO_OK;
+  if (x == nullptr) return PURO_ERR_NULL;
+  return aligned_to(x, type == PURO_TYPE_BF16 ? 2 : 4) ? PURO_OK : PURO_ERR_ALIGN;
+}
+
+}  // namespace
+}  // namespace puro
+
+using namespace puro;
+
+extern "C" puro_status puro_ckpt_pack(const void* x, int x_type, int64_t rows, int64_t cols,
+                                      int64_t ldx, int pow2, void* q, float* s, void* stream) {
+  if (!any_dim_ok(rows) || !any_dim_ok(cols)) return PURO_ERR_SHAPE;
+  const bool empty = rows == 0 || cols == 0;
+  if (pow2 != 0 && pow2 != 1) return PURO_ERR_ARG;
+  PURO_TRY(check_wide(x, x_type, cols, ldx, empty));
+  PURO_TRY(check_ptr(q, empty));
+  PURO_TRY(check_ptr(s, empty));
+  if (empty) return PURO_OK;
+  int64_t blocks;
+  PURO_TRY(check_rows(rows, cols, &blocks));
+  const dim3 grid(static_cast<uint32_t>(blocks));
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (x_type == PURO_TYPE_BF16)
+    hipLaunchKernelGGL(ckpt_pack_kernel<uint16_t>, grid, dim3(256), 0, st,
+                       static_cast<const uint16_t*>(x), rows, cols, ldx, pow2,
+                       static_cast<uint8_t*>(q), s);
+  else
+    hipLaunchKernelGGL(ckpt_pack_kernel<float>, grid, dim3(256), 0, st,
+                       static_cast<const float*>(x), rows, cols, ldx, pow2,
+                       static_cast<uint8_t*>(q), s);
+  return launch_status();
+}
+
+extern "C" puro_status puro_ckpt_unpack(const void* q, const float* s, int64_t rows, int64_t cols,
+                                        void* x, int x_type, int64_t ldx, void* stream) {
+  if (!any_dim_ok(rows) || !any_dim_ok(cols)) return PURO_ERR_SHAPE;
+  const bool empty = rows == 0 || cols == 0;
+  PURO_TRY(check_ptr(q, empty));
+  PURO_TRY(check_ptr(s, empty));
+  PURO_TRY(check_wide(x, x_type, cols, ldx, empty));
+  if (empty) return PURO_OK;
+  int64_t blocks;
+  PURO_TRY(check_rows(rows, cols, &blocks));
+  const dim3 grid(static_cast<uint32_t>(blocks));
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (x_type == PURO_TYPE_BF16)
+    hipLaunchKernelGGL(ckpt_unpack_kernel<uint16_t>, grid, dim3(256), 0, st,
+                       static_cast<const uint8_t*>(q), s, rows, cols, ldx,
+                       static_cast<uint16_t*>(x));
+  else
+    hipLaunchKernelGGL(ckpt_unpack_kernel<float>, grid, dim3(256), 0, st,
+                       static_cast<const uint8_t*>(q), s, rows, cols, ldx,
+                       static_cast<float*>(x));
+  return launch_status();
+}
+
+extern "C" puro_status puro_ckpt_transpose(const void* q, const float* s, int64_t rows,
+                                           int64_t cols, int pow2, void* qt, float* st,
+                                           void* stream) {
+  if (!any_dim_ok(rows) || !any_dim_ok(cols)) return PURO_ERR_SHAPE;
+  const bool empty = rows == 0 || cols == 0;
+  if (pow2 != 0 && pow2 != 1) return PURO_ERR_ARG;
+  PURO_TRY(check_ptr(q, empty));
+  PURO_TRY(check_ptr(s, empty));
+  PURO_TRY(check_ptr(qt, empty));
+  PURO_TRY(check_ptr(st, empty));
+  if (empty) return PURO_OK;
+  const int64_t blocks = ceil_div(rows, 128) * ceil_div(cols, 128);
+  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  hipLaunchKernelGGL(ckpt_transpose_kernel, dim3(static_cast<uint32_t>(blocks)),
+                     dim3(kTileThreads), 0, static_cast<hipStream_t>(stream),
+                     static_cast<const uint8_t*>(q), s, rows, cols, pow2,
+                     static_cast<uint8_t*>(qt), st);
+  return launch_status();
+}

@@ -1,0 +1,140 @@
+// Column groups of a 128 x 128 tile held in registers: the transposed codes and scales that the
+// weight-gradient GEMM reads (groups along the tokens), from fp32 values, for kN tensors at once.
+//
+// A 512-thread block holds the tile as 4 consecutive rows x 8 consecutive columns per thread
+// (16 lanes cover a row, each wave 16 rows). A column's largest magnitude is a register maximum
+// over 4 rows, two lane swaps over the wave's 16 and eight words of LDS over the block; one
+// thread per column then does the two divisions. Only codes are transposed through LDS, one byte
+// per element: four rows of a column are one dword, and a column's 128 bytes leave as one line.
+//
+// Dword of column 8 l + i, rows 4 g .. 4 g + 3: codes[(16 i + l) * kPitch + g]. With a pitch of 36
+// dwords the 16 lanes of a row start 16 different multiples of 4 banks and the wave's four row
+// groups fill the banks between, so the writes are free of conflicts and the reads are 16 B.
+#pragma once
+#include "block.hpp"
+
+namespace puro {
+
+typedef uint32_t u32x4_by __attribute__((ext_vector_type(4), aligned(1)));
+
+constexpr int kTileThreads = 512;
+constexpr int kTileRows = 4;   // rows per thread
+
+template <int kN>
+struct ColTile {
+  static constexpr int kPitch = 36;
+  union {  // the maxima are read for the last time a barrier before the first code is written
+    uint32_t codes[kN][128 * kPitch];
+    uint32_t wmax[kN][8][128];
+  };
+  float r[kN][128];
+  int odd;
+};
+
+// Where one tensor's transposed codes go: qt [cols][rows], st [ceil(rows/128)][cols].
+struct ColOut {
+  uint8_t* qt;
+  float* st;
+  int64_t cols;   // columns of the tensor
+  int64_t c0;     // first column of this tile
+};
+
+template <int kN, bool kFinite>
+__device__ __forceinline__ void col_maxima(ColTile<kN>& sh, const float (&v)[kN][kTileRows][kVec]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int t = 0; t < kN; ++t) {
+    uint32_t m[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      m[i] = 0;
+#pragma unroll
+      for (int p = 0; p < kTileRows; ++p)
+        m[i] = umax32(m[i], kFinite ? finite_mag(v[t][p][i]) : mag(v[t][p][i]));
+      m[i] = __float_as_uint(across_rows_max(__uint_as_float(m[i])));
+    }
+    if (lane < 16) {
+      uint4* dst = reinterpret_cast<uint4*>(&sh.wmax[t][wave][8 * lane]);
+      dst[0] = make_uint4(m[0], m[1], m[2], m[3]);
+      dst[1] = make_uint4(m[4], m[5], m[6], m[7]);
+    }
+  }
+}
+
+template <int kN, bool kMark>
+__device__ __forceinline__ void col_scales(ColTile<kN>& sh, const ColOut (&out)[kN], int64_t mb,
+                                           bool pow2) {
+  const int t = threadIdx.x;
+  if (t < kN * 128) {
+    const int k = t >> 7, c = t & 127;
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = umax32(m, sh.wmax[k][w][c]);
+    if (kMark && m >= kInfBits) sh.odd = 1;  // every writer writes the same value
+    float s, r;
+    ckpt_scale(m, pow2, s, r);
+    sh.r[k][c] = r;
+    ColOut o = out[0];
+#pragma unroll
+    for (int j = 1; j < kN; ++j)
+      if (k == j) o = out[j];
+    if (o.c0 + c < o.cols) o.st[mb * o.cols + o.c0 + c] = s;
+  }
+}
+
+// All 512 threads call it once; v[t][p][i] is element (row m0 + 4 (thread/16) + p, column
+// c0 + 8 (thread mod 16) + i) of tensor t, zero outside it.
+template <int kN>
+__device__ __forceinline__ void col_codes(ColTile<kN>& sh, const float (&v)[kN][kTileRows][kVec],
+                                          const ColOut (&out)[kN], int64_t rows, int64_t mb,
+                                          bool pow2) {
+  static_assert(kN * 128 <= kTileThreads, "one thread per column of each tensor");
+  const int t = threadIdx.x, l16 = t & 15, seg = t >> 4;
+  if (t == 0) sh.odd = 0;
+  col_maxima<kN, false>(sh, v);
+  __syncthreads();
+  // A maximum with infinity or NaN in it marks the tile, which is then gone over again with the
+  // finite maxima; the first pass's scales are overwritten by the same threads.
+  col_scales<kN, true>(sh, out, mb, pow2);
+  __syncthreads();
+  const bool odd = sh.odd != 0;
+  if (odd) {
+    col_maxima<kN, true>(sh, v);
+    __syncthreads();
+    col_scales<kN, false>(sh, out, mb, pow2);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int k = 0; k < kN; ++k)
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const float r = sh.r[k][8 * l16 + i];
+      const float a = v[k][0][i], b = v[k][1][i], c = v[k][2][i], d = v[k][3][i];
+      sh.codes[k][(16 * i + l16) * ColTile<kN>::kPitch + seg] =
+          odd ? e4m3x4_any(a, b, c, d, r) : e4m3x4(a * r, b * r, c * r, d * r);
+    }
+  __syncthreads();
+  const int64_t row = mb * 128 + 16 * (t & 7);
+  const int64_t left = rows - row;
+#pragma unroll
+  for (int k = 0; k < kN; ++k)
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      const int pos = pass * 64 + (t >> 3);
+      const int64_t col = out[k].c0 + 8 * (pos & 15) + (pos >> 4);
+      const uint4 w = *reinterpret_cast<const uint4*>(
+          &sh.codes[k][pos * ColTile<kN>::kPitch + 4 * (t & 7)]);
+      if (col >= out[k].cols) continue;
+      uint8_t* p = out[k].qt + col * rows + row;
+      if (left >= 16) {
+        *reinterpret_cast<u32x4_by*>(p) = u32x4_by{w.x, w.y, w.z, w.w};
+      } else {
+        const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < left) p[i] = static_cast<uint8_t>(b[i >> 2] >> (8 * (i & 3)));
+      }
+    }
+}
+
+}  // namespace puro

@@ -244,6 +244,148 @@ puro_status puro_fp8_gemm_wgrad_pow2(const void* dytq, const float* sdyt, const 
                                      const float* sxt, float* dw, int64_t M, int64_t N, int64_t K,
                                      int accumulate, void* stream);
 
+/* ---------------------------------------------------------------- between the GEMMs
+ * The operators that stand between two FP8 GEMMs of a training step: the norms around a block
+ * with its gate and residual scale, the gated activation of the MLP, and 8-bit checkpoints of
+ * activations that the backward pass reads. They take bf16 activations and gradients, fp32
+ * weights and weight gradients, and a residual stream in bf16 or fp32, and write the GEMMs' FP8
+ * operands directly. Conventions as above, except where stated: rows and columns here may have
+ * any size from 0 to 2^24 (not only multiples of 128), and inputs may hold infinities and NaN.
+ * Sums and statistics are fp32 and run in an order fixed by the sizes alone, so results repeat
+ * exactly.
+ *
+ * Checkpoint format, of a matrix [rows][cols]: groups of 128 consecutive columns of a row (the
+ * last may be shorter);
+ *   codes   e4m3 [rows][cols]
+ *   scales  fp32 [ceil(cols/128)][rows]
+ * with amax the largest finite magnitude of a group, s = amax/448, q = E4M3_RNE(clamp(x *
+ * (448/amax))) as for the quantisers; a nonzero amax below 2^-119 counts as 2^-119, an infinity
+ * or NaN is stored as the NaN code with its sign, and a group without a nonzero finite element
+ * has s = 1. pow2 = 1 takes the power-of-two scale rule instead (pow2 = 0: amax/448). For sizes
+ * that are multiples of 128 and finite inputs within the quantisers' contract these are the bytes
+ * of puro_quant_act_1x128 (_pow2): a forward operand that is kept is a checkpoint. */
+#define PURO_TYPE_BF16 0
+#define PURO_TYPE_FP32 1
+
+/* Checkpoint of x (x_type PURO_TYPE_*, [rows][cols] with a row stride of ldx >= cols elements,
+ * aligned to its element). */
+puro_status puro_ckpt_pack(const void* x, int x_type, int64_t rows, int64_t cols, int64_t ldx,
+                           int pow2, void* q, float* s, void* stream);
+
+/* The values a checkpoint stands for, value(q) * s, rounded once to x_type; x as above. */
+puro_status puro_ckpt_unpack(const void* q, const float* s, int64_t rows, int64_t cols, void* x,
+                             int x_type, int64_t ldx, void* stream);
+
+/* A checkpoint requantised along its rows and transposed: the checkpoint, in the same format, of
+ * the transposed matrix of fp32 values value(q) * s. From a forward operand (puro_quant_act_1x128,
+ * puro_block_norm_fwd, puro_swiglu_fwd) it makes the weight gradient's operand, so no transposed
+ * copy has to be kept from the forward pass.
+ *   qt e4m3 [cols][rows], st fp32 [ceil(rows/128)][cols] (outputs) */
+puro_status puro_ckpt_transpose(const void* q, const float* s, int64_t rows, int64_t cols,
+                                int pow2, void* qt, float* st, void* stream);
+
+/* Block norm, forward: the RMS norm after a block, the gate and residual scales, and the RMS norm
+ * before the next block, row by row:
+ *   p = y * rstd_y * w_post,            rstd_y = 1/sqrt(mean(y^2) + eps)
+ *   r_out = beta * r + alpha * gate * p
+ *   n = r_out * rstd_r * w_pre,         rstd_r = 1/sqrt(mean(r_out^2) + eps)
+ * n is formed from the unrounded r_out. Either half may be left out: w_post and y NULL
+ * for the norm before a block alone (then r_out = beta * r), w_pre NULL for the norm after a block
+ * alone.
+ * cols <= PURO_NORM_MAX_COLS. Sums of squares must fit fp32. */
+#define PURO_NORM_MAX_COLS 16384
+#define PURO_GATE_NONE 0
+#define PURO_GATE_CHANNEL 1 /* fp32 [cols] */
+#define PURO_GATE_TOKEN 2   /* fp32 [rows] */
+#define PURO_GATE_FULL 3    /* bf16 [rows][cols] */
+typedef struct {
+  int64_t rows, cols;
+  int residual_type;        /* PURO_TYPE_* of r and r_out */
+  int gate_kind;            /* PURO_GATE_* */
+  int pow2;                 /* scale rule of the 8-bit outputs */
+  float alpha, beta, eps;   /* finite; eps > 0 */
+  const void* y;            /* bf16 [rows][cols]: the block's output, with w_post */
+  const void* r;            /* [rows][cols]: the residual stream */
+  const float* w_post;      /* [cols], or NULL */
+  const float* w_pre;       /* [cols], or NULL */
+  const void* gate;
+  void* r_out;              /* [rows][cols], required with w_post; may be r itself */
+  void* n;                  /* bf16 [rows][cols], or NULL */
+  void* nq;                 /* n as codes and scales: the next GEMM's operand, or both NULL */
+  float* ns;
+  float* rstd_y;            /* [rows], with w_post */
+  float* rstd_r;            /* [rows], with w_pre */
+  void* yq;                 /* checkpoint of y, or both NULL */
+  float* ys;
+  void* rq;                 /* checkpoint of the unrounded r_out, or both NULL */
+  float* rs;
+} puro_block_norm;
+puro_status puro_block_norm_fwd(const puro_block_norm* desc, void* stream);
+
+/* Block norm, backward. From the gradients of r_out (dr_out, NULL for zero) and n (dn) and from y and r_out as stored -- as they were, or
+ * as checkpoints -- with their rstd_y and rstd_r, and with yh = y rstd_y, rh = r_out rstd_r:
+ *   G  = dr_out + rstd_r (w_pre dn - rh mean(rh w_pre dn))
+ *   dr = beta G                                (may be dr_out itself; NULL to skip)
+ *   dp = alpha gate G,  dy = rstd_y (w_post dp - yh mean(yh w_post dp))
+ *   dw_post = sum over rows of dp yh,  dw_pre = sum over rows of dn rh     (NULL to skip)
+ *   dgate = alpha w_post yh G, summed over rows (PURO_GATE_CHANNEL), over columns
+ *           (PURO_GATE_TOKEN) or as it is (PURO_GATE_FULL), in the gate's type
+ * accumulate = 1 adds dw_post, dw_pre and a channel gate's gradient to what is there. w_post NULL:
+ * the norm after the block was left out; w_pre NULL: the norm before the next one. workspace: puro_block_norm_workspace(rows, cols) bytes
+ * of caller-owned device memory, 16-byte aligned, used by one call at a time. */
+#define PURO_NORM_MAX_BLOCKS 512
+typedef struct {
+  int64_t rows, cols;
+  int residual_type;        /* PURO_TYPE_* of dr_out, dr and r */
+  int gate_kind;
+  int accumulate;
+  float alpha, beta;
+  const void* dr_out;       /* [rows][cols], or NULL */
+  const void* dn;           /* bf16 [rows][cols], or NULL */
+  const void* y;            /* bf16 [rows][cols], or its checkpoint yq, ys */
+  const void* yq;
+  const float* ys;
+  const void* r;            /* r_out [rows][cols], or its checkpoint rq, rs */
+  const void* rq;
+  const float* rs;
+  const float* rstd_y;
+  const float* rstd_r;
+  const float* w_post;
+  const float* w_pre;
+  const void* gate;
+  void* dr;                 /* [rows][cols] */
+  void* dy;                 /* bf16 [rows][cols] */
+  float* dw_post;           /* [cols] */
+  float* dw_pre;            /* [cols] */
+  void* dgate;
+} puro_block_norm_grad;
+int64_t puro_block_norm_workspace(int64_t rows, int64_t cols);
+puro_status puro_block_norm_bwd(const puro_block_norm_grad* desc, void* workspace, void* stream);
+
+/* The MLP's gated activation, h = u * g * sigmoid(g), from the gate_up projection's output.
+ *   gu   bf16 [rows][2f]: g in the first f columns, u in the others
+ *   h    bf16 [rows][f], or NULL
+ *   hq, hs    h's codes [rows][f] and scales [ceil(f/128)][rows]: the down projection's operand
+ *   guq, gus  checkpoint of gu: codes [rows][2f], scales [2 ceil(f/128)][rows], g's groups first
+ *             (u's groups start at column f)
+ * Any output may be left out (each pair as a whole), not all of them. */
+puro_status puro_swiglu_fwd(const void* gu, int64_t rows, int64_t f, void* h, void* hq, float* hs,
+                            void* guq, float* gus, int pow2, void* stream);
+
+/* Backward: dgu bf16 [rows][2f] = [dh u sig (1 + g (1 - sig)) | dh g sig], sig = sigmoid(g), from
+ * dh bf16 [rows][f] and either gu (bf16) or its checkpoint guq, gus (gu NULL). */
+puro_status puro_swiglu_bwd(const void* dh, const void* gu, const void* guq, const float* gus,
+                            int64_t rows, int64_t f, void* dgu, void* stream);
+
+/* Backward to the FP8 operands of the GEMMs that follow, without dgu itself; rows and f must be
+ * multiples of 128. Encoded from fp32 values:
+ *   dguq  [rows][2f], dgus  [2f/128][rows]   dgu for gate_up's data gradient
+ *   dgutq [2f][rows], dguts [rows/128][2f]   dgu transposed, for gate_up's weight gradient
+ *   htq   [f][rows],  hts   [rows/128][f]    h transposed, for down's weight gradient */
+puro_status puro_swiglu_bwd_fp8(const void* dh, const void* gu, const void* guq, const float* gus,
+                                int64_t rows, int64_t f, int pow2, void* dguq, float* dgus,
+                                void* dgutq, float* dguts, void* htq, float* hts, void* stream);
+
 /* Debug mode: input checks on the device before every quantiser and GEMM.
  * At level 0 (the default) nothing is checked. At level 1 or more each quantiser and GEMM
  * entry point, after its host validation, scans its inputs on `stream`, waits for the scan
