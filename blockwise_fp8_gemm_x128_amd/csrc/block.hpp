@@ -143,9 +143,15 @@ __device__ __forceinline__ void store8(uint8_t* p, int n, const u32x2_el v) {
 }
 
 // ---------------------------------------------------------------- sums over lanes
+// A lane permutation within rows of 16 that the compiler can fold into the instruction using it.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dppu(uint32_t v) {
+  return static_cast<uint32_t>(
+      __builtin_amdgcn_mov_dpp(static_cast<int>(v), kCtrl, 0xF, 0xF, true));
+}
 template <int kCtrl>
 __device__ __forceinline__ float dppf(float v) {
-  return __uint_as_float(dpp<kCtrl>(__float_as_uint(v)));
+  return __uint_as_float(dppu<kCtrl>(__float_as_uint(v)));
 }
 // Sum over a team of kLanes (16, 32 or 64) consecutive lanes, the same bits in each of them: the
 // partners of every step hold mirrored operands of one addition.
@@ -172,15 +178,29 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // Magnitudes as bit patterns: for non-negative floats the order of the patterns is the order of
 // the values, with infinity and NaN above every finite value.
 __device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// Zero for infinities and NaN. For rare paths: the empty statement keeps the compiler from working
+// the magnitudes out ahead of the branch that leads here.
 __device__ __forceinline__ uint32_t finite_mag(float x) {
+  asm volatile("" : "+v"(x));
   const uint32_t m = mag(x);
   return m < kInfBits ? m : 0u;
 }
+// Largest magnitude of eight values as bits. Of stored values (kRaw) over the bit patterns, where
+// an infinity or NaN tops everything and so is noticed. Of computed values, whose NaN are quiet,
+// by three-operand maxima with free absolute values, which pass NaN over and notice infinities.
+template <bool kRaw>
 __device__ __forceinline__ uint32_t max8(const float* f) {
-  uint32_t m = mag(f[0]);
+  if constexpr (kRaw) {
+    uint32_t m = mag(f[0]);
 #pragma unroll
-  for (int i = 1; i < kVec; ++i) m = umax32(m, mag(f[i]));
-  return m;
+    for (int i = 1; i < kVec; ++i) m = umax32(m, mag(f[i]));
+    return m;
+  } else {
+    float m = __builtin_fabsf(f[0]);
+#pragma unroll
+    for (int i = 1; i < kVec; ++i) m = fmaxf(m, __builtin_fabsf(f[i]));
+    return __float_as_uint(m) & 0x7fffffffu;
+  }
 }
 __device__ __forceinline__ uint32_t finite_max8(const float* f) {
   uint32_t m = finite_mag(f[0]);
@@ -188,8 +208,12 @@ __device__ __forceinline__ uint32_t finite_max8(const float* f) {
   for (int i = 1; i < kVec; ++i) m = umax32(m, finite_mag(f[i]));
   return m;
 }
+// Over the 16 lanes of a DPP row: neighbours, pairs, halves of 8, the row.
 __device__ __forceinline__ uint32_t row16_umax(uint32_t u) {
-  return __float_as_uint(row16_max(__uint_as_float(u)));
+  u = umax32(u, dppu<0xB1>(u));
+  u = umax32(u, dppu<0x4E>(u));
+  u = umax32(u, dppu<0x141>(u));
+  return umax32(u, dppu<0x140>(u));
 }
 
 // Scale of a checkpoint group from its largest finite magnitude (bits): the quantisers' rule,
@@ -206,27 +230,17 @@ __device__ __forceinline__ void ckpt_scale(uint32_t amax, bool pow2, float& s, f
   if (amax == 0) s = r = 1.0f;
 }
 
-// Codes of a group that holds an infinity or NaN: those elements become the NaN code with their
-// sign, the finite ones are encoded as usual.
-__device__ __forceinline__ uint32_t e4m3x4_any(float a, float b, float c, float d, float r) {
-  uint32_t v = e4m3x4(a * r, b * r, c * r, d * r);
-  const float f[4] = {a, b, c, d};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (mag(f[i]) >= kInfBits)
-      v = (v & ~(0xffu << (8 * i))) | ((0x7fu | (__float_as_uint(f[i]) >> 24 & 0x80u)) << (8 * i));
-  return v;
+// Codes of four scaled values. A finite element of its own group is at most 448 (1 + 2^-22) in
+// magnitude, which rounds to 448, so nothing needs clamping; an infinity and a NaN convert to the
+// NaN code with their sign.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true));
 }
 __device__ __forceinline__ u32x2_el encode8(const float* f, float r) {
   u32x2_el v;
-  v[0] = e4m3x4(f[0] * r, f[1] * r, f[2] * r, f[3] * r);
-  v[1] = e4m3x4(f[4] * r, f[5] * r, f[6] * r, f[7] * r);
-  return v;
-}
-__device__ __forceinline__ u32x2_el encode8_any(const float* f, float r) {
-  u32x2_el v;
-  v[0] = e4m3x4_any(f[0], f[1], f[2], f[3], r);
-  v[1] = e4m3x4_any(f[4], f[5], f[6], f[7], r);
+  v[0] = codes4(f[0] * r, f[1] * r, f[2] * r, f[3] * r);
+  v[1] = codes4(f[4] * r, f[5] * r, f[6] * r, f[7] * r);
   return v;
 }
 
@@ -237,7 +251,6 @@ template <int kN>
 struct RowGroups {
   float r[kN];   // reciprocal scales
   float s;       // in lane k of the row (k < kN): group k's scale
-  bool odd;      // some group of this row of lanes holds an infinity or NaN
 };
 template <int kN, int kK = 0>
 __device__ __forceinline__ void take_scales(float r, float* out) {
@@ -246,7 +259,7 @@ __device__ __forceinline__ void take_scales(float r, float* out) {
     take_scales<kN, kK + 1>(r, out);
   }
 }
-template <int kN>
+template <bool kRaw, int kN>
 __device__ __forceinline__ RowGroups<kN> row_groups(const float (*f)[kVec], bool pow2) {
   static_assert(kN <= 16, "one lane per group");
   const int l16 = threadIdx.x & 15;
@@ -254,16 +267,21 @@ __device__ __forceinline__ RowGroups<kN> row_groups(const float (*f)[kVec], bool
   uint32_t mine = 0, all = 0;
 #pragma unroll
   for (int k = 0; k < kN; ++k) {
-    const uint32_t m = row16_umax(max8(f[k]));
+    const uint32_t m = row16_umax(max8<kRaw>(f[k]));
     all = umax32(all, m);
     mine = l16 == k ? m : mine;
   }
-  g.odd = all >= kInfBits;
-  if (g.odd) {
-    mine = 0;
-#pragma unroll
+  if (all >= kInfBits) {  // rare: an infinity or NaN, which the scale leaves out
+#pragma unroll 1
     for (int k = 0; k < kN; ++k) {
-      const uint32_t m = row16_umax(finite_max8(f[k]));
+      float v[kVec];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] = f[0][i];
+#pragma unroll
+      for (int j = 1; j < kN; ++j)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] = j == k ? f[j][i] : v[i];
+      const uint32_t m = row16_umax(finite_max8(v));
       mine = l16 == k ? m : mine;
     }
   }
@@ -271,10 +289,6 @@ __device__ __forceinline__ RowGroups<kN> row_groups(const float (*f)[kVec], bool
   ckpt_scale(mine, pow2, g.s, r);
   take_scales<kN>(r, g.r);
   return g;
-}
-template <int kN>
-__device__ __forceinline__ u32x2_el encode8(const RowGroups<kN>& g, int k, const float* f) {
-  return g.odd ? encode8_any(f, g.r[k]) : encode8(f, g.r[k]);
 }
 
 }  // namespace puro

@@ -38,11 +38,11 @@ __global__ __launch_bounds__(256) void ckpt_pack_kernel(const T* __restrict__ x,
     const int64_t row = r0 + 16 * p;
     v[p] = load8<true>(x + row * ldx + col, row < rows ? n : 0);
   }
-  const RowGroups<kPasses> g = row_groups<kPasses>(&v[0].f, pow2 != 0);
+  const RowGroups<kPasses> g = row_groups<true, kPasses>(&v[0].f, pow2 != 0);
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int64_t row = r0 + 16 * p;
-    if (row < rows) store8(q + row * cols + col, n, encode8(g, p, v[p].f));
+    if (row < rows) store8(q + row * cols + col, n, encode8(v[p].f, g.r[p]));
   }
   if (l16 < kPasses && r0 + 16 * l16 < rows) s[c * rows + r0 + 16 * l16] = g.s;
 }

@@ -47,10 +47,16 @@ __device__ __forceinline__ void col_maxima(ColTile<kN>& sh, const float (&v)[kN]
     uint32_t m[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      m[i] = 0;
+      if constexpr (kFinite) {
+        m[i] = finite_mag(v[t][0][i]);
 #pragma unroll
-      for (int p = 0; p < kTileRows; ++p)
-        m[i] = umax32(m[i], kFinite ? finite_mag(v[t][p][i]) : mag(v[t][p][i]));
+        for (int p = 1; p < kTileRows; ++p) m[i] = umax32(m[i], finite_mag(v[t][p][i]));
+      } else {  // computed values: NaN are quiet and passed over, infinities noticed
+        float x = __builtin_fabsf(v[t][0][i]);
+#pragma unroll
+        for (int p = 1; p < kTileRows; ++p) x = fmaxf(x, __builtin_fabsf(v[t][p][i]));
+        m[i] = __float_as_uint(x) & 0x7fffffffu;
+      }
       m[i] = __float_as_uint(across_rows_max(__uint_as_float(m[i])));
     }
     if (lane < 16) {
@@ -58,6 +64,7 @@ __device__ __forceinline__ void col_maxima(ColTile<kN>& sh, const float (&v)[kN]
       dst[0] = make_uint4(m[0], m[1], m[2], m[3]);
       dst[1] = make_uint4(m[4], m[5], m[6], m[7]);
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -66,7 +73,7 @@ __device__ __forceinline__ void col_scales(ColTile<kN>& sh, const ColOut (&out)[
                                            bool pow2) {
   const int t = threadIdx.x;
   if (t < kN * 128) {
-    const int k = t >> 7, c = t & 127;
+    const int k = __builtin_amdgcn_readfirstlane(t >> 7), c = t & 127;  // one tensor per wave
     uint32_t m = 0;
 #pragma unroll
     for (int w = 0; w < 8; ++w) m = umax32(m, sh.wmax[k][w][c]);
@@ -74,11 +81,10 @@ __device__ __forceinline__ void col_scales(ColTile<kN>& sh, const ColOut (&out)[
     float s, r;
     ckpt_scale(m, pow2, s, r);
     sh.r[k][c] = r;
-    ColOut o = out[0];
 #pragma unroll
-    for (int j = 1; j < kN; ++j)
-      if (k == j) o = out[j];
-    if (o.c0 + c < o.cols) o.st[mb * o.cols + o.c0 + c] = s;
+    for (int j = 0; j < kN; ++j)
+      if (k == j && out[j].c0 + c < out[j].cols)
+        out[j].st[mb * out[j].cols + out[j].c0 + c] = s;
   }
 }
 
@@ -93,26 +99,27 @@ __device__ __forceinline__ void col_codes(ColTile<kN>& sh, const float (&v)[kN][
   if (t == 0) sh.odd = 0;
   col_maxima<kN, false>(sh, v);
   __syncthreads();
-  // A maximum with infinity or NaN in it marks the tile, which is then gone over again with the
-  // finite maxima; the first pass's scales are overwritten by the same threads.
+  // An infinite maximum (or NaN: a column of nothing else) marks the tile, which is then gone over
+  // again with the finite maxima; the first pass's scales are overwritten by the same threads.
   col_scales<kN, true>(sh, out, mb, pow2);
   __syncthreads();
-  const bool odd = sh.odd != 0;
-  if (odd) {
+  if (sh.odd != 0) {
     col_maxima<kN, true>(sh, v);
     __syncthreads();
     col_scales<kN, false>(sh, out, mb, pow2);
     __syncthreads();
   }
 #pragma unroll
-  for (int k = 0; k < kN; ++k)
+  for (int k = 0; k < kN; ++k) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const float r = sh.r[k][8 * l16 + i];
       const float a = v[k][0][i], b = v[k][1][i], c = v[k][2][i], d = v[k][3][i];
       sh.codes[k][(16 * i + l16) * ColTile<kN>::kPitch + seg] =
-          odd ? e4m3x4_any(a, b, c, d, r) : e4m3x4(a * r, b * r, c * r, d * r);
+          codes4(a * r, b * r, c * r, d * r);
     }
+    __builtin_amdgcn_sched_barrier(0);
+  }
   __syncthreads();
   const int64_t row = mb * 128 + 16 * (t & 7);
   const int64_t left = rows - row;

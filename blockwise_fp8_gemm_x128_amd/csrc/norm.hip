@@ -84,11 +84,12 @@ struct FwdArgs {
   float* rs;
 };
 
+template <bool kRaw>
 __device__ __forceinline__ void store_codes(uint8_t* q, float* s, int64_t row, int64_t rows,
                                             int cols, int col, int n, const float* f, bool pow2) {
-  const RowGroups<1> g = row_groups<1>(reinterpret_cast<const float(*)[kVec]>(f), pow2);
+  const RowGroups<1> g = row_groups<kRaw, 1>(reinterpret_cast<const float(*)[kVec]>(f), pow2);
   if (n <= 0) return;
-  store8(q + row * cols + col, n, encode8(g, 0, f));
+  store8(q + row * cols + col, n, encode8(f, g.r[0]));
   if ((threadIdx.x & 15) == 0) s[static_cast<int64_t>(col >> 7) * rows + row] = g.s;
 }
 
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_fwd_kernel(const Fwd
         if (a.yq)
 #pragma unroll
           for (int j = 0; j < kNV; ++j)
-            store_codes(a.yq, a.ys, row, a.rows, a.cols, col[j], n[j], y[j].f, a.pow2 != 0);
+            store_codes<true>(a.yq, a.ys, row, a.rows, a.cols, col[j], n[j], y[j].f, a.pow2 != 0);
       }
       float gt = 1.0f;
       if (a.gate_kind == PURO_GATE_TOKEN && in) gt = static_cast<const float*>(a.gate)[row];
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_fwd_kernel(const Fwd
         }
         if (a.r_out) store8(static_cast<R*>(a.r_out) + row * a.cols + col[j], n[j], t[j]);
         if (a.rq)
-          store_codes(a.rq, a.rs, row, a.rows, a.cols, col[j], n[j], t[j], a.pow2 != 0);
+          store_codes<false>(a.rq, a.rs, row, a.rows, a.cols, col[j], n[j], t[j], a.pow2 != 0);
       }
     }
     if (!a.w_pre) {
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_fwd_kernel(const Fwd
 #pragma unroll
       for (int i = 0; i < kVec; ++i) o[i] = t[j][i] * rr * pw[j][i];
       if (a.n) store8(a.n + row * a.cols + col[j], n, o);
-      if (a.nq) store_codes(a.nq, a.ns, row, a.rows, a.cols, col[j], n, o, a.pow2 != 0);
+      if (a.nq) store_codes<false>(a.nq, a.ns, row, a.rows, a.cols, col[j], n, o, a.pow2 != 0);
     }
     if (kLanes == 0 && !a.y) __syncthreads();  // before sh[1] is written again
   }

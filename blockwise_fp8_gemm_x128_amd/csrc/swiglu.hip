@@ -103,16 +103,16 @@ __global__ __launch_bounds__(256) void swiglu_fwd_kernel(const FwdArgs a) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) v[2][i] = v[0][i] * sigmoid(v[0][i]) * v[1][i];
     if (a.h != nullptr && in) store8(a.h + row * a.f + col, n, v[2]);
-    const RowGroups<3> g = row_groups<3>(v, pow2);
+    const RowGroups<3> g = row_groups<true, 3>(v, pow2);
     if (!in) continue;
     if (a.hq != nullptr) {
-      store8(a.hq + row * a.f + col, n, encode8(g, 2, v[2]));
+      store8(a.hq + row * a.f + col, n, encode8(v[2], g.r[2]));
       if (l16 == 2) a.hs[c * a.rows + row] = g.s;
     }
     if (a.guq != nullptr) {
       uint8_t* q = a.guq + row * 2 * a.f + col;
-      store8(q, n, encode8(g, 0, v[0]));
-      store8(q + a.f, n, encode8(g, 1, v[1]));
+      store8(q, n, encode8(v[0], g.r[0]));
+      store8(q + a.f, n, encode8(v[1], g.r[1]));
       if (l16 < 2) a.gus[(l16 * chunks + c) * a.rows + row] = g.s;
     }
   }
@@ -177,46 +177,74 @@ struct BwdFp8Args {
   int pow2;
 };
 
+// Four waves per SIMD, two blocks per CU, so that one block's loads and stores run under the
+// other's arithmetic: that caps the registers at 128, of which the three tensors' values take 96.
+// Addresses are therefore one 32-bit offset per lane on top of a uniform pointer per row.
 template <bool kCodes>
-__global__ __launch_bounds__(kTileThreads) void swiglu_bwd_fp8_kernel(const BwdFp8Args a) {
+__global__ __launch_bounds__(kTileThreads, 4) void swiglu_bwd_fp8_kernel(const BwdFp8Args a) {
   __shared__ ColTile<3> sh;
   const int64_t chunks = a.f >> 7;
   const int64_t c = blockIdx.x % chunks, mb = blockIdx.x / chunks;
   const int l16 = threadIdx.x & 15;
-  const int64_t col = c * 128 + l16 * kVec;
-  const int64_t r0 = mb * 128 + (threadIdx.x >> 4) * kTileRows;
-  GuRaw<kCodes> raw[kTileRows];
-  u32x4_el dhr[kTileRows];
-#pragma unroll
-  for (int p = 0; p < kTileRows; ++p) {
-    raw[p] = load_gu<kCodes>(a.src, a.rows, a.f, chunks, r0 + p, c, col, kVec);
-    dhr[p] = load_raw<true>(a.dh + (r0 + p) * a.f + col, kVec);
-  }
+  const uint32_t f = static_cast<uint32_t>(a.f);
+  const uint32_t r4 = (threadIdx.x >> 4) * kTileRows;  // first of the thread's rows in the tile
+  // at most 127 (2 f) + 128 < 2^32 for f <= 2^24
+  const uint32_t at1 = r4 * f + l16 * kVec, at2 = r4 * 2 * f + l16 * kVec;
+  const int64_t base1 = mb * 128 * a.f + c * 128, base2 = mb * 256 * a.f + c * 128;
   float v[3][kTileRows][kVec];  // dg, du, h
+  {
+    GuRaw<kCodes> raw[kTileRows];
+    u32x4_el dhr[kTileRows];
 #pragma unroll
-  for (int p = 0; p < kTileRows; ++p) {
-    float g[kVec], u[kVec], dh[kVec];
-    values<kCodes>(raw[p], g, u);
-    widen8(dhr[p], dh);
+    for (int p = 0; p < kTileRows; ++p) {
+      if constexpr (kCodes) {
+        raw[p].g = load_raw<true>(a.src.q + base2 + p * 2 * a.f + at2, kVec);
+        raw[p].u = load_raw<true>(a.src.q + base2 + p * 2 * a.f + a.f + at2, kVec);
+      } else {
+        raw[p].g = load_raw<true>(a.src.gu + base2 + p * 2 * a.f + at2, kVec);
+        raw[p].u = load_raw<true>(a.src.gu + base2 + p * 2 * a.f + a.f + at2, kVec);
+      }
+      dhr[p] = load_raw<true>(a.dh + base1 + p * a.f + at1, kVec);
+    }
+    if constexpr (kCodes) {
+      const float4 sg = *reinterpret_cast<const float4*>(a.src.s + c * a.rows + mb * 128 + r4);
+      const float4 su =
+          *reinterpret_cast<const float4*>(a.src.s + (chunks + c) * a.rows + mb * 128 + r4);
+      raw[0].sg = sg.x, raw[1].sg = sg.y, raw[2].sg = sg.z, raw[3].sg = sg.w;
+      raw[0].su = su.x, raw[1].su = su.y, raw[2].su = su.z, raw[3].su = su.w;
+    }
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const float sg = sigmoid(g[i]);
-      const float t = dh[i] * sg;
-      v[0][p][i] = t * u[i] * fmaf(g[i], 1.0f - sg, 1.0f);
-      v[1][p][i] = t * g[i];
-      v[2][p][i] = g[i] * sg * u[i];
+    for (int p = 0; p < kTileRows; ++p) {
+      float g[kVec], u[kVec], dh[kVec];
+      values<kCodes>(raw[p], g, u);
+      widen8(dhr[p], dh);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const float sg = sigmoid(g[i]);
+        const float t = dh[i] * sg;
+        v[0][p][i] = t * u[i] * fmaf(g[i], 1.0f - sg, 1.0f);
+        v[1][p][i] = t * g[i];
+        v[2][p][i] = g[i] * sg * u[i];
+      }
+      // The compiler would rather keep the inputs and work the values out where they are used,
+      // which takes more registers than there are: the empty statements pin the values here.
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) asm volatile("" : "+v"(v[t][p][i]));
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   const bool pow2 = a.pow2 != 0;
-  const RowGroups<2 * kTileRows> rg = row_groups<2 * kTileRows>(v[0], pow2);
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int t = 0; t < 2; ++t) {
+    const RowGroups<kTileRows> rg = row_groups<false, kTileRows>(v[t], pow2);
 #pragma unroll
     for (int p = 0; p < kTileRows; ++p)
-      store8(a.dguq + (r0 + p) * 2 * a.f + t * a.f + col, kVec,
-             encode8(rg, t * kTileRows + p, v[t][p]));
-  if (l16 < 2 * kTileRows)
-    a.dgus[((l16 / kTileRows) * chunks + c) * a.rows + r0 + l16 % kTileRows] = rg.s;
+      store8(a.dguq + base2 + p * 2 * a.f + t * a.f + at2, kVec, encode8(v[t][p], rg.r[p]));
+    if (l16 < kTileRows) a.dgus[(t * chunks + c) * a.rows + mb * 128 + r4 + l16] = rg.s;
+    __builtin_amdgcn_sched_barrier(0);
+  }
   const ColOut out[3] = {{a.dgutq, a.dguts, 2 * a.f, c * 128},
                          {a.dgutq, a.dguts, 2 * a.f, a.f + c * 128},
                          {a.htq, a.hts, a.f, c * 128}};
