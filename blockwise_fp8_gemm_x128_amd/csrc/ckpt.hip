@@ -15,93 +15,92 @@ namespace puro {
 namespace {
 
 // ------------------------------------------------------------------ row groups
-// A 256-thread block covers 64 rows of one 128-column chunk: 16 lanes x 8 elements per row, 16
-// rows at a time, every load issued before the first group is scaled. The scales of a chunk are
-// contiguous over rows, so lane k of a 16-lane row stores those of its k-th row.
-constexpr int kPasses = 4;
-constexpr int kRowsPerBlock = 16 * kPasses;
+// Tiles as RowTile lays them out. Lane k of a 16-lane row stores the scale of the row's k-th pass.
+constexpr int kPasses = RowTile::kPasses;
 
-template <typename T>
+template <typename T, bool kShort>
 __global__ __launch_bounds__(256) void ckpt_pack_kernel(const T* __restrict__ x, int64_t rows,
                                                         int64_t cols, int64_t ldx, int pow2,
                                                         uint8_t* __restrict__ q,
                                                         float* __restrict__ s) {
-  const int64_t chunks = (cols + 127) >> 7;
-  const int64_t c = blockIdx.x % chunks;
-  const int64_t r0 = blockIdx.x / chunks * kRowsPerBlock + (threadIdx.x >> 4);
+  const RowTile t(cols, off_lines(cols));
   const int l16 = threadIdx.x & 15;
-  const int64_t col = c * 128 + l16 * kVec;
-  const int n = static_cast<int>(min(cols - col, int64_t(kVec)));
+  const int64_t c = t.chunk;
+  const Span<kShort> sp(t.col, cols, cols % (128 * RowTile::kChunks) != 0);
+  typename RawOf<T>::type raw[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p)  // rows past the end read the last one again
+    load<true, kShort>(raw[p], x + min(t.row(p), rows - 1) * ldx, sp);
   F8 v[kPasses];
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int64_t row = r0 + 16 * p;
-    v[p] = load8<true>(x + row * ldx + col, row < rows ? n : 0);
-  }
+  for (int p = 0; p < kPasses; ++p) values(raw[p], sp, v[p].f);
   const RowGroups<kPasses> g = row_groups<true, kPasses>(&v[0].f, pow2 != 0);
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int64_t row = r0 + 16 * p;
-    if (row < rows) store8(q + row * cols + col, n, encode8(v[p].f, g.r[p]));
+    const int64_t row = t.row(p);
+    if (row < rows) store8<true>(q + row * cols + t.col, sp.n, encode8(v[p].f, g.r[p]));
   }
-  if (l16 < kPasses && r0 + 16 * l16 < rows) s[c * rows + r0 + 16 * l16] = g.s;
+  if (l16 < kPasses && c * 128 < cols && t.row(l16) < rows) s[c * rows + t.row(l16)] = g.s;
 }
 
-template <typename T>
+template <typename T, bool kShort>
 __global__ __launch_bounds__(256) void ckpt_unpack_kernel(const uint8_t* __restrict__ q,
                                                           const float* __restrict__ s,
                                                           int64_t rows, int64_t cols, int64_t ldx,
                                                           T* __restrict__ x) {
-  const int64_t chunks = (cols + 127) >> 7;
-  const int64_t c = blockIdx.x % chunks;
-  const int64_t r0 = blockIdx.x / chunks * kRowsPerBlock + (threadIdx.x >> 4);
-  const int64_t col = c * 128 + (threadIdx.x & 15) * kVec;
-  const int n = static_cast<int>(min(cols - col, int64_t(kVec)));
-  u32x2_el v[kPasses];
+  const RowTile t(cols, off_lines(cols));
+  const Span<kShort> sp(t.col, cols, cols % (128 * RowTile::kChunks) != 0);
+  const int64_t c = min(t.chunk, (cols - 1) >> 7);
+  Fp8x8 raw[kPasses];
   float sc[kPasses];
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int64_t row = r0 + 16 * p;
-    v[p] = load_raw<true>(q + row * cols + col, row < rows ? n : 0);
-    sc[p] = row < rows ? s[c * rows + row] : 0.0f;
+  for (int p = 0; p < kPasses; ++p) {  // rows past the end read the last one again
+    const int64_t row = min(t.row(p), rows - 1);
+    load<true, kShort>(raw[p], q + row * cols, sp);
+    sc[p] = s[c * rows + row];
   }
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int64_t row = r0 + 16 * p;
+    const int64_t row = t.row(p);
     float f[kVec];
-    decode8(v[p], sc[p], f);
-    if (row < rows) store8(x + row * ldx + col, n, f);
+    values(raw[p], sp, sc[p], f);
+    if (row < rows) store8(x + row * ldx + t.col, sp.n, f);
   }
 }
 
 // ------------------------------------------------------------------ along the rows
 // Requantisation for the weight gradient: a 512-thread block decodes a 128 x 128 tile into
 // registers (4 consecutive rows x 8 columns a thread) and encodes its column groups.
+template <bool kShort>
 __global__ __launch_bounds__(kTileThreads) void ckpt_transpose_kernel(
     const uint8_t* __restrict__ q, const float* __restrict__ s, int64_t rows, int64_t cols,
     int pow2, uint8_t* __restrict__ qt, float* __restrict__ st) {
   __shared__ ColTile<1> sh;
-  const int64_t chunks = (cols + 127) >> 7;
-  const int64_t cb = blockIdx.x % chunks, mb = blockIdx.x / chunks;
-  const int64_t col = cb * 128 + (threadIdx.x & 15) * kVec;
+  const uint32_t chunks = static_cast<uint32_t>((cols + 127) >> 7);
+  const uint32_t b = off_lines(cols) || off_lines(rows) ? xcd_range(blockIdx.x, gridDim.x)
+                                                        : blockIdx.x;
+  const int64_t cb = b % chunks, mb = b / chunks;
+  const Span<kShort> sp(cb * 128 + (threadIdx.x & 15) * kVec, cols, off_lines(cols));
   const int64_t r0 = mb * 128 + (threadIdx.x >> 4) * kTileRows;
-  const int n = static_cast<int>(min(cols - col, int64_t(kVec)));
-  u32x2_el raw[kTileRows];
+  Fp8x8 raw[kTileRows];
   float sc[kTileRows];
 #pragma unroll
   for (int p = 0; p < kTileRows; ++p) {
-    raw[p] = load_raw<false>(q + (r0 + p) * cols + col, r0 + p < rows ? n : 0);
-    sc[p] = r0 + p < rows ? s[cb * rows + r0 + p] : 0.0f;
+    const int64_t row = min(r0 + p, rows - 1);
+    load<true, kShort>(raw[p], q + row * cols, sp);
+    sc[p] = s[cb * rows + row];
   }
+  // A row past the end holds the last one again: it changes no maximum, and its codes are not
+  // stored.
   float v[1][kTileRows][kVec];
 #pragma unroll
-  for (int p = 0; p < kTileRows; ++p) decode8(raw[p], sc[p], v[0][p]);
+  for (int p = 0; p < kTileRows; ++p) values(raw[p], sp, sc[p], v[0][p]);
   const ColOut out[1] = {{qt, st, cols, cb * 128}};
   col_codes<1>(sh, v, out, rows, mb, pow2 != 0);
 }
 
 puro_status check_rows(int64_t rows, int64_t cols, int64_t* blocks) {
-  *blocks = ceil_div(rows, kRowsPerBlock) * ceil_div(cols, 128);
+  *blocks = row_tiles(rows, cols);
   return *blocks > INT32_MAX ? PURO_ERR_SHAPE : PURO_OK;
 }
 
@@ -132,14 +131,16 @@ extern "C" puro_status puro_ckpt_pack(const void* x, int x_type, int64_t rows, i
   PURO_TRY(check_rows(rows, cols, &blocks));
   const dim3 grid(static_cast<uint32_t>(blocks));
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (x_type == PURO_TYPE_BF16)
-    hipLaunchKernelGGL(ckpt_pack_kernel<uint16_t>, grid, dim3(256), 0, st,
-                       static_cast<const uint16_t*>(x), rows, cols, ldx, pow2,
-                       static_cast<uint8_t*>(q), s);
-  else
-    hipLaunchKernelGGL(ckpt_pack_kernel<float>, grid, dim3(256), 0, st,
-                       static_cast<const float*>(x), rows, cols, ldx, pow2,
-                       static_cast<uint8_t*>(q), s);
+  if (x_type == PURO_TYPE_BF16) {
+    const auto k = cols < kVec ? ckpt_pack_kernel<uint16_t, true>
+                               : ckpt_pack_kernel<uint16_t, false>;
+    hipLaunchKernelGGL(k, grid, dim3(256), 0, st, static_cast<const uint16_t*>(x), rows, cols, ldx,
+                       pow2, static_cast<uint8_t*>(q), s);
+  } else {
+    const auto k = cols < kVec ? ckpt_pack_kernel<float, true> : ckpt_pack_kernel<float, false>;
+    hipLaunchKernelGGL(k, grid, dim3(256), 0, st, static_cast<const float*>(x), rows, cols, ldx,
+                       pow2, static_cast<uint8_t*>(q), s);
+  }
   return launch_status();
 }
 
@@ -155,14 +156,17 @@ extern "C" puro_status puro_ckpt_unpack(const void* q, const float* s, int64_t r
   PURO_TRY(check_rows(rows, cols, &blocks));
   const dim3 grid(static_cast<uint32_t>(blocks));
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (x_type == PURO_TYPE_BF16)
-    hipLaunchKernelGGL(ckpt_unpack_kernel<uint16_t>, grid, dim3(256), 0, st,
-                       static_cast<const uint8_t*>(q), s, rows, cols, ldx,
-                       static_cast<uint16_t*>(x));
-  else
-    hipLaunchKernelGGL(ckpt_unpack_kernel<float>, grid, dim3(256), 0, st,
-                       static_cast<const uint8_t*>(q), s, rows, cols, ldx,
-                       static_cast<float*>(x));
+  if (x_type == PURO_TYPE_BF16) {
+    const auto k = cols < kVec ? ckpt_unpack_kernel<uint16_t, true>
+                               : ckpt_unpack_kernel<uint16_t, false>;
+    hipLaunchKernelGGL(k, grid, dim3(256), 0, st, static_cast<const uint8_t*>(q), s, rows, cols,
+                       ldx, static_cast<uint16_t*>(x));
+  } else {
+    const auto k = cols < kVec ? ckpt_unpack_kernel<float, true>
+                               : ckpt_unpack_kernel<float, false>;
+    hipLaunchKernelGGL(k, grid, dim3(256), 0, st, static_cast<const uint8_t*>(q), s, rows, cols,
+                       ldx, static_cast<float*>(x));
+  }
   return launch_status();
 }
 
@@ -179,7 +183,8 @@ extern "C" puro_status puro_ckpt_transpose(const void* q, const float* s, int64_
   if (empty) return PURO_OK;
   const int64_t blocks = ceil_div(rows, 128) * ceil_div(cols, 128);
   if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
-  hipLaunchKernelGGL(ckpt_transpose_kernel, dim3(static_cast<uint32_t>(blocks)),
+  const auto k = cols < kVec ? ckpt_transpose_kernel<true> : ckpt_transpose_kernel<false>;
+  hipLaunchKernelGGL(k, dim3(static_cast<uint32_t>(blocks)),
                      dim3(kTileThreads), 0, static_cast<hipStream_t>(stream),
                      static_cast<const uint8_t*>(q), s, rows, cols, pow2,
                      static_cast<uint8_t*>(qt), st);

@@ -89,7 +89,8 @@ __device__ __forceinline__ void col_scales(ColTile<kN>& sh, const ColOut (&out)[
 }
 
 // All 512 threads call it once; v[t][p][i] is element (row m0 + 4 (thread/16) + p, column
-// c0 + 8 (thread mod 16) + i) of tensor t, zero outside it.
+// c0 + 8 (thread mod 16) + i) of tensor t; columns past the end are zero, rows past the end repeat
+// the last one (which changes no maximum; their codes are not stored).
 template <int kN>
 __device__ __forceinline__ void col_codes(ColTile<kN>& sh, const float (&v)[kN][kTileRows][kVec],
                                           const ColOut (&out)[kN], int64_t rows, int64_t mb,

@@ -33,7 +33,7 @@ template <int kLanes, int kN>
 __device__ __forceinline__ void team_sum(float (&v)[kN], float (*sh)[kMaxWaves], int wpt) {
   if constexpr (kLanes != 0) {
 #pragma unroll
-    for (int k = 0; k < kN; ++k) v[k] = lanes_sum<kLanes>(v[k]);
+    for (int k = 0; k < kN; ++k) v[k] = lanes_sum<kLanes == 1 ? 16 : kLanes>(v[k]);
   } else {
     const int wave = threadIdx.x >> 6, w0 = wave - wave % wpt;
 #pragma unroll
@@ -43,13 +43,30 @@ __device__ __forceinline__ void team_sum(float (&v)[kN], float (*sh)[kMaxWaves],
       for (int k = 0; k < kN; ++k) sh[k][wave] = v[k];
     }
     __syncthreads();
+    // lane w of each 16 takes wave w's sum, and the 16 are summed like the lanes before
+    const int w = threadIdx.x & 15;
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      float t = sh[k][w0];
-      for (int w = 1; w < wpt; ++w) t += sh[k][w0 + w];
-      v[k] = t;
+      const float t = sh[k][min(w0 + w, kMaxWaves - 1)];
+      v[k] = lanes_sum<16>(w < wpt ? t : 0.0f);
     }
   }
+}
+
+// Sum over a wave's teams of kLanes lanes, lane by lane.
+template <int kLanes>
+__device__ __forceinline__ float teams_sum(float v) {
+  if constexpr (kLanes == 1 || kLanes == 16) {
+    const uint32_t u = __float_as_uint(v);
+    const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  if constexpr (kLanes == 1 || kLanes == 16 || kLanes == 32) {
+    const uint32_t u = __float_as_uint(v);
+    const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  return v;
 }
 
 // The lanes of one team and the rows of one block.
@@ -57,12 +74,28 @@ template <int kLanes>
 struct Team {
   int lanes, lane, team, teams;
   __device__ __forceinline__ explicit Team(int wpt) {
-    lanes = kLanes ? kLanes : wpt * 64;
+    lanes = kLanes == 1 ? 16 : kLanes ? kLanes : wpt * 64;
     team = threadIdx.x / lanes;
+    // teams of whole waves: the row is the same in all lanes of a wave, and its addresses are scalar
+    if (kLanes == 0 || kLanes == 64) team = __builtin_amdgcn_readfirstlane(team);
     lane = threadIdx.x - team * lanes;
     teams = blockDim.x / lanes;
   }
 };
+
+// Eight of a vector over the columns (a weight, a gate), or `none` where there is none.
+template <bool kShort>
+__device__ __forceinline__ void row_vector(const float* w, const Span<kShort>& sp, float none,
+                                           float* f) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) f[i] = none;
+    return;
+  }
+  F8 r;
+  load<false, kShort>(r, w, sp);
+  values(r, sp, f);
+}
 
 // ------------------------------------------------------------------ forward
 struct FwdArgs {
@@ -84,110 +117,158 @@ struct FwdArgs {
   float* rs;
 };
 
-template <bool kRaw>
-__device__ __forceinline__ void store_codes(uint8_t* q, float* s, int64_t row, int64_t rows,
-                                            int cols, int col, int n, const float* f, bool pow2) {
-  const RowGroups<1> g = row_groups<kRaw, 1>(reinterpret_cast<const float(*)[kVec]>(f), pow2);
-  if (n <= 0) return;
-  store8(q + row * cols + col, n, encode8(f, g.r[0]));
-  if ((threadIdx.x & 15) == 0) s[static_cast<int64_t>(col >> 7) * rows + row] = g.s;
+// Where a row's 8-bit form goes.
+struct CodeOut {
+  uint8_t* q;
+  float* s;
+};
+// A lane's eight codes; `lane` of the 16 that share the group stores its scale.
+template <bool kUniform, bool kLater>
+__device__ __forceinline__ void store_codes(const CodeOut& o, int64_t row, int64_t rows,
+                                            uint32_t cols, uint32_t col, int n, bool in,
+                                            const float* f, float r, float scale, uint32_t lane) {
+  store8<kLater>(row_ptr<kUniform>(o.q, row * cols) + col, n, encode8(f, r));
+  if ((threadIdx.x & 15) == lane && in && (col & ~127u) < cols)
+    row_ptr<kUniform>(o.s, row)[static_cast<int64_t>(col >> 7) * rows] = scale;
+}
+
+// One row's inputs as loaded.
+template <typename R, int kNV>
+struct FwdRow {
+  typename RawOf<R>::type r[kNV];
+  Bf16x8 y[kNV], gate[kNV];
+  float gt;
+};
+
+template <bool kUniform, typename R, int kNV, bool kShort>
+__device__ __forceinline__ void load_row(FwdRow<R, kNV>& w, const FwdArgs& a, int64_t row,
+                                         const Span<kShort> (&sp)[kNV]) {
+  const int64_t at = row * a.cols;
+  w.gt = a.gate_kind == PURO_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
+#pragma unroll
+  for (int j = 0; j < kNV; ++j) {
+    if (a.y) load<true, kShort>(w.y[j], row_ptr<kUniform>(a.y, at), sp[j]);
+    load<true, kShort>(w.r[j], row_ptr<kUniform>(static_cast<const R*>(a.r), at), sp[j]);
+    if (a.gate_kind == PURO_GATE_FULL)
+      load<true, kShort>(w.gate[j],
+                         row_ptr<kUniform>(static_cast<const uint16_t*>(a.gate), at), sp[j]);
+  }
 }
 
 template <typename R, int kLanes, int kNV>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_fwd_kernel(const FwdArgs a) {
   __shared__ float sh[2][1][kMaxWaves];
+  constexpr bool kShort = kLanes == 1;  // rows of fewer than eight columns, in one lane of 16
+  constexpr bool kUniform = kLanes == 0 || kLanes == 64;
   const Team<kLanes> tm(a.wpt);
   const float inv_d = 1.0f / static_cast<float>(a.cols);
-  const bool channel = a.gate_kind == PURO_GATE_CHANNEL;
+  const bool channel = a.gate_kind == PURO_GATE_CHANNEL, full = a.gate_kind == PURO_GATE_FULL;
+  const bool pow2 = a.pow2 != 0;
 
   float cw[kNV][kVec], pw[kNV][kVec];  // alpha (gate) w_post; w_pre
-  int col[kNV], left[kNV];
+  Span<kShort> sp[kNV];
 #pragma unroll
   for (int j = 0; j < kNV; ++j) {
-    col[j] = (j * tm.lanes + tm.lane) * kVec;
-    left[j] = a.cols - col[j];
-    F8 w = {}, g = {};
-    if (a.w_post) w = load8<false>(a.w_post + col[j], left[j]);
-    if (channel) g = load8<false>(static_cast<const float*>(a.gate) + col[j], left[j]);
+    sp[j] = Span<kShort>((j * tm.lanes + tm.lane) * kVec, a.cols,
+                         a.cols != tm.lanes * kVec * kNV);
+    row_vector(a.w_post, sp[j], 0.0f, cw[j]);
+    float g[kVec];
+    row_vector(channel ? static_cast<const float*>(a.gate) : nullptr, sp[j], 1.0f, g);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) cw[j][i] = a.alpha * w.f[i] * (channel ? g.f[i] : 1.0f);
-    F8 p = {};
-    if (a.w_pre) p = load8<false>(a.w_pre + col[j], left[j]);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) pw[j][i] = p.f[i];
+    for (int i = 0; i < kVec; ++i) cw[j][i] *= a.alpha * g[i];
+    row_vector(a.w_pre, sp[j], 0.0f, pw[j]);
   }
 
   const int64_t first = int64_t(blockIdx.x) * a.rows_per_block;
   const int64_t end = min(a.rows, first + a.rows_per_block);
+  // A team past the end works on the last row again and stores nothing.
+  FwdRow<R, kNV> w;
   for (int64_t base = first; base < end; base += tm.teams) {  // the same count for every team
-    const int64_t row = base + tm.team;
-    const bool in = row < end;
-    float t[kNV][kVec];
-    {
-      F8 y[kNV], r[kNV];
-      int n[kNV];
+    const int64_t row = min(base + tm.team, end - 1);
+    const bool in = base + tm.team < end;
+    load_row<kUniform>(w, a, row, sp);
+    const int64_t at = row * a.cols;
+    float y[kNV][kVec], t[kNV][kVec];
+    uint32_t ymax[kNV];
+    float ry = 0.0f;
+    if (a.y) {
+      float ss[1] = {0.0f};
 #pragma unroll
       for (int j = 0; j < kNV; ++j) {
-        n[j] = in ? left[j] : 0;
-        if (a.y) y[j] = load8<true>(a.y + row * a.cols + col[j], n[j]);
-        r[j] = load8<true>(static_cast<const R*>(a.r) + row * a.cols + col[j], n[j]);
+        settle(w.y[j], sp[j]);
+        widen8(w.y[j].v, y[j]);
+        ymax[j] = max8(w.y[j]);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) ss[0] = fmaf(y[j][i], y[j][i], ss[0]);
       }
-      float ry = 0.0f;
+      team_sum<kLanes, 1>(ss, sh[0], a.wpt);
+      ry = rsqrtf(fmaf(ss[0], inv_d, a.eps));
+      if (in && tm.lane == 0) a.rstd_y[row] = ry;
+    }
+#pragma unroll
+    for (int j = 0; j < kNV; ++j) {
+      float r[kVec];
+      values(w.r[j], sp[j], r);
       if (a.y) {
-        float ss[1] = {0.0f};
+        const float f = ry * w.gt;
+        if (full) {
+          float g[kVec];
+          values(w.gate[j], sp[j], g);
 #pragma unroll
-        for (int j = 0; j < kNV; ++j)
+          for (int i = 0; i < kVec; ++i)
+            t[j][i] = fmaf(y[j][i] * cw[j][i] * g[i], f, a.beta * r[i]);
+        } else {
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) ss[0] = fmaf(y[j].f[i], y[j].f[i], ss[0]);
-        team_sum<kLanes, 1>(ss, sh[0], a.wpt);
-        ry = rsqrtf(fmaf(ss[0], inv_d, a.eps));
-        if (in && tm.lane == 0) a.rstd_y[row] = ry;
-        if (a.yq)
-#pragma unroll
-          for (int j = 0; j < kNV; ++j)
-            store_codes<true>(a.yq, a.ys, row, a.rows, a.cols, col[j], n[j], y[j].f, a.pow2 != 0);
-      }
-      float gt = 1.0f;
-      if (a.gate_kind == PURO_GATE_TOKEN && in) gt = static_cast<const float*>(a.gate)[row];
-#pragma unroll
-      for (int j = 0; j < kNV; ++j) {
-        F8 g;
-        if (a.gate_kind == PURO_GATE_FULL)
-          g = load8<true>(static_cast<const uint16_t*>(a.gate) + row * a.cols + col[j], n[j]);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          float p = 0.0f;
-          if (a.y) {
-            p = y[j].f[i] * ry * cw[j][i] * gt;
-            if (a.gate_kind == PURO_GATE_FULL) p *= g.f[i];
-          }
-          t[j][i] = fmaf(a.beta, r[j].f[i], p);
+          for (int i = 0; i < kVec; ++i)
+            t[j][i] = fmaf(y[j][i] * cw[j][i], f, a.beta * r[i]);
         }
-        if (a.r_out) store8(static_cast<R*>(a.r_out) + row * a.cols + col[j], n[j], t[j]);
-        if (a.rq)
-          store_codes<false>(a.rq, a.rs, row, a.rows, a.cols, col[j], n[j], t[j], a.pow2 != 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) t[j][i] = a.beta * r[i];
+      }
+    }
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < kNV; ++j) {
+      const int n = in ? sp[j].n : 0;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) ss[0] = fmaf(t[j][i], t[j][i], ss[0]);
+      if (a.r_out) store8<true>(row_ptr<kUniform>(static_cast<R*>(a.r_out), at) + sp[j].col, n, t[j]);
+      if (a.yq && a.rq) {  // both scales from one pair of divisions
+        float both[2][kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) both[0][i] = y[j][i], both[1][i] = t[j][i];
+        const uint32_t m[2] = {ymax[j], max8<false>(t[j])};
+        const RowGroups<2> g = row_groups<2>(m, both, pow2);
+        store_codes<kUniform, true>({a.yq, a.ys}, row, a.rows, a.cols, sp[j].col, n, in, y[j], g.r[0], g.s, 0);
+        store_codes<kUniform, true>({a.rq, a.rs}, row, a.rows, a.cols, sp[j].col, n, in, t[j], g.r[1], g.s, 1);
+      } else if (a.yq) {
+        const uint32_t m[1] = {ymax[j]};
+        const RowGroups<1> g = row_groups<1>(m, &y[j], pow2);
+        store_codes<kUniform, true>({a.yq, a.ys}, row, a.rows, a.cols, sp[j].col, n, in, y[j], g.r[0], g.s, 0);
+      } else if (a.rq) {
+        const RowGroups<1> g = row_groups<false, 1>(&t[j], pow2);
+        store_codes<kUniform, true>({a.rq, a.rs}, row, a.rows, a.cols, sp[j].col, n, in, t[j], g.r[0], g.s, 0);
       }
     }
     if (!a.w_pre) {
       if constexpr (kLanes == 0) __syncthreads();  // before sh[0] is written again
       continue;
     }
-    float ss[1] = {0.0f};
-#pragma unroll
-    for (int j = 0; j < kNV; ++j)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) ss[0] = fmaf(t[j][i], t[j][i], ss[0]);
     team_sum<kLanes, 1>(ss, sh[1], a.wpt);
     const float rr = rsqrtf(fmaf(ss[0], inv_d, a.eps));
     if (in && tm.lane == 0) a.rstd_r[row] = rr;
 #pragma unroll
     for (int j = 0; j < kNV; ++j) {
-      const int n = in ? left[j] : 0;
+      const int n = in ? sp[j].n : 0;
       float o[kVec];
 #pragma unroll
       for (int i = 0; i < kVec; ++i) o[i] = t[j][i] * rr * pw[j][i];
-      if (a.n) store8(a.n + row * a.cols + col[j], n, o);
-      if (a.nq) store_codes<false>(a.nq, a.ns, row, a.rows, a.cols, col[j], n, o, a.pow2 != 0);
+      if (a.n) store8(row_ptr<kUniform>(a.n, at) + sp[j].col, n, o);
+      if (a.nq) {
+        const RowGroups<1> g = row_groups<false, 1>(&o, pow2);
+        store_codes<kUniform, false>({a.nq, a.ns}, row, a.rows, a.cols, sp[j].col, n, in, o, g.r[0], g.s, 0);
+      }
     }
     if (kLanes == 0 && !a.y) __syncthreads();  // before sh[1] is written again
   }
@@ -215,138 +296,241 @@ struct BwdArgs {
   float* partials;   // [blocks][2][cols]: sums of g yh G and of dn rh
 };
 
-template <typename R, int kLanes, int kNV>
-__global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_bwd_kernel(const BwdArgs a) {
-  __shared__ float sh[2][3][kMaxWaves];
-  const Team<kLanes> tm(a.wpt);
-  const float inv_d = 1.0f / static_cast<float>(a.cols);
-  const bool channel = a.gate_kind == PURO_GATE_CHANNEL;
-  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
+// One row's inputs as loaded: the stored activations as codes (kCodes) or as they were.
+template <typename R, int kNV, bool kCodes>
+struct BwdRow {
+  typename RawOf<R>::type d[kNV], r[kNV];
+  Bf16x8 dn[kNV], y[kNV], gate[kNV];
+  float ry, rr, gt;
+};
+template <typename R, int kNV>
+struct BwdRow<R, kNV, true> {
+  typename RawOf<R>::type d[kNV];
+  Fp8x8 r[kNV], y[kNV];
+  Bf16x8 dn[kNV], gate[kNV];
+  float rs[kNV], ys[kNV];
+  float ry, rr, gt;
+};
 
-  float wo[kNV][kVec], wp[kNV][kVec], gc[kNV][kVec];
-  float acc[2][kNV][kVec] = {};
-  int col[kNV], left[kNV];
+template <bool kUniform, typename R, int kNV, bool kCodes, bool kShort>
+__device__ __forceinline__ void load_row(BwdRow<R, kNV, kCodes>& w, const BwdArgs& a, int64_t row,
+                                         const Span<kShort> (&sp)[kNV]) {
+  const int64_t at = row * a.cols;
+  w.gt = a.gate_kind == PURO_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
+  w.ry = a.w_post ? a.rstd_y[row] : 0.0f;
+  w.rr = a.w_pre ? a.rstd_r[row] : 0.0f;
 #pragma unroll
   for (int j = 0; j < kNV; ++j) {
-    col[j] = (j * tm.lanes + tm.lane) * kVec;
-    left[j] = a.cols - col[j];
-    F8 w = {}, p = {}, g = {};
-    if (post) w = load8<false>(a.w_post + col[j], left[j]);
-    if (pre) p = load8<false>(a.w_pre + col[j], left[j]);
-    if (channel) g = load8<false>(static_cast<const float*>(a.gate) + col[j], left[j]);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      wo[j][i] = w.f[i];
-      wp[j][i] = p.f[i];
-      gc[j][i] = channel ? g.f[i] : 1.0f;
+    const int64_t sat = int64_t(min(sp[j].col, a.cols - 1u) >> 7) * a.rows;
+    if (a.dr_out)
+      load<true, kShort>(w.d[j], row_ptr<kUniform>(static_cast<const R*>(a.dr_out), at), sp[j]);
+    if (a.w_pre) {
+      load<true, kShort>(w.dn[j], row_ptr<kUniform>(a.dn, at), sp[j]);
+      if constexpr (kCodes) {
+        load<true, kShort>(w.r[j], row_ptr<kUniform>(a.rq, at), sp[j]);
+        w.rs[j] = row_ptr<kUniform>(a.rs, row)[sat];
+      } else {
+        load<true, kShort>(w.r[j], row_ptr<kUniform>(static_cast<const R*>(a.r), at), sp[j]);
+      }
     }
+    if (a.w_post) {
+      if constexpr (kCodes) {
+        load<true, kShort>(w.y[j], row_ptr<kUniform>(a.yq, at), sp[j]);
+        w.ys[j] = row_ptr<kUniform>(a.ys, row)[sat];
+      } else {
+        load<true, kShort>(w.y[j], row_ptr<kUniform>(a.y, at), sp[j]);
+      }
+    }
+    if (a.gate_kind == PURO_GATE_FULL)
+      load<true, kShort>(w.gate[j],
+                         row_ptr<kUniform>(static_cast<const uint16_t*>(a.gate), at), sp[j]);
+  }
+}
+
+// With two vectors per lane the weights are read again for each row (from the caches) and nothing is
+// loaded ahead: there are no registers for either.
+template <typename R, int kLanes, int kNV, bool kCodes>
+__global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(
+    const BwdArgs a) {
+  __shared__ float sh[2][3][kMaxWaves];
+  constexpr bool kShort = kLanes == 1;  // rows of fewer than eight columns, in one lane of 16
+  constexpr bool kUniform = kLanes == 0 || kLanes == 64;
+  const Team<kLanes> tm(a.wpt);
+  const float inv_d = 1.0f / static_cast<float>(a.cols);
+  const bool channel = a.gate_kind == PURO_GATE_CHANNEL, full = a.gate_kind == PURO_GATE_FULL;
+  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
+
+  float wg[kNV][kVec], wp[kNV][kVec];  // w_post (times a channel gate); w_pre
+  float acc[2][kNV][kVec] = {};
+  Span<kShort> sp[kNV];
+#pragma unroll
+  for (int j = 0; j < kNV; ++j) {
+    sp[j] = Span<kShort>((j * tm.lanes + tm.lane) * kVec, a.cols,
+                         a.cols != tm.lanes * kVec * kNV);
+    row_vector(a.w_post, sp[j], 0.0f, wg[j]);
+    float g[kVec];
+    row_vector(channel ? static_cast<const float*>(a.gate) : nullptr, sp[j], 1.0f, g);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) wg[j][i] *= g[i];
+    row_vector(a.w_pre, sp[j], 0.0f, wp[j]);
   }
 
   const int64_t first = int64_t(blockIdx.x) * a.rows_per_block;
   const int64_t end = min(a.rows, first + a.rows_per_block);
   int buf = 0;
+  BwdRow<R, kNV, kCodes> w;
+  load_row<kUniform>(w, a, min(first + tm.team, end - 1), sp);
   for (int64_t base = first; base < end; base += tm.teams, buf ^= 1) {
-    const int64_t row = base + tm.team;
-    const bool in = row < end;
-    float A[kNV][kVec], yh[kNV][kVec], rh[kNV][kVec], g[kNV][kVec];
+    // A team past the end works on the last row again, with its statistics taken as zero, so that
+    // it adds nothing to a column sum, and stores nothing.
+    const int64_t row = min(base + tm.team, end - 1);
+    const bool in = base + tm.team < end;
+    const float ry = in ? w.ry : 0.0f, rr = in ? w.rr : 0.0f, gt = w.gt;
+    float A[kNV][kVec], yh[kNV][kVec], rh[kNV][kVec];
+    Bf16x8 graw[kNV];
     float sums[3] = {0.0f, 0.0f, 0.0f};
-    const float ry = post && in ? a.rstd_y[row] : 0.0f;
-    const float rr = pre && in ? a.rstd_r[row] : 0.0f;
-    float gt = 1.0f;
-    if (a.gate_kind == PURO_GATE_TOKEN && in) gt = static_cast<const float*>(a.gate)[row];
 #pragma unroll
     for (int j = 0; j < kNV; ++j) {
-      const int n = in ? left[j] : 0;
-      const int64_t at = row * a.cols + col[j];
-      const int64_t sat = static_cast<int64_t>(col[j] >> 7) * a.rows + row;
-      F8 d = {}, dn = {}, y = {}, r = {};
-      if (a.dr_out) d = load8<true>(static_cast<const R*>(a.dr_out) + at, n);
+      if (a.dr_out) {
+        values(w.d[j], sp[j], A[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) A[j][i] = 0.0f;
+      }
       if (pre) {
-        dn = load8<true>(a.dn + at, n);
-        if (a.rq)
-          decode8(load_raw<true>(a.rq + at, n), n > 0 ? a.rs[sat] : 0.0f, r.f);
+        float dn[kVec];
+        values(w.dn[j], sp[j], dn);
+        if constexpr (kCodes)
+          values(w.r[j], sp[j], w.rs[j], rh[j]);
         else
-          r = load8<true>(static_cast<const R*>(a.r) + at, n);
+          values(w.r[j], sp[j], rh[j]);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          rh[j][i] *= rr;
+          const float x = wp[j][i] * dn[i];
+          A[j][i] = fmaf(rr, x, A[j][i]);
+          sums[0] = fmaf(rh[j][i], x, sums[0]);
+          acc[1][j][i] = fmaf(dn[i], rh[j][i], acc[1][j][i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) rh[j][i] = 0.0f;
       }
       if (post) {
-        if (a.yq)
-          decode8(load_raw<true>(a.yq + at, n), n > 0 ? a.ys[sat] : 0.0f, y.f);
+        if constexpr (kCodes)
+          values(w.y[j], sp[j], w.ys[j], yh[j]);
         else
-          y = load8<true>(a.y + at, n);
-      }
-      F8 ge;
-      if (a.gate_kind == PURO_GATE_FULL)
-        ge = load8<true>(static_cast<const uint16_t*>(a.gate) + at, n);
+          values(w.y[j], sp[j], yh[j]);
+        float q[kVec];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        g[j][i] = a.gate_kind == PURO_GATE_FULL ? ge.f[i] : gc[j][i];
-        yh[j][i] = y.f[i] * ry;
-        rh[j][i] = r.f[i] * rr;
-        const float x = wp[j][i] * dn.f[i];
-        A[j][i] = fmaf(rr, x, d.f[i]);
-        sums[0] = fmaf(rh[j][i], x, sums[0]);
-        const float q = yh[j][i] * wo[j][i] * g[j][i];
-        sums[1] = fmaf(q, A[j][i], sums[1]);
-        sums[2] = fmaf(q, rh[j][i], sums[2]);
-        acc[1][j][i] = fmaf(dn.f[i], rh[j][i], acc[1][j][i]);
+        for (int i = 0; i < kVec; ++i) {
+          yh[j][i] *= ry;
+          q[i] = yh[j][i] * wg[j][i];
+        }
+        if (full) {
+          float g[kVec];
+          graw[j] = w.gate[j];
+          values(graw[j], sp[j], g);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) q[i] *= g[i];
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          sums[1] = fmaf(q[i], A[j][i], sums[1]);
+          sums[2] = fmaf(q[i], rh[j][i], sums[2]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) yh[j][i] = 0.0f;
       }
     }
+    // the next row's loads go out before this one's sums and stores
+    if (base + tm.teams < end)
+      load_row<kUniform>(w, a, min(base + tm.teams + tm.team, end - 1), sp);
     team_sum<kLanes, 3>(sums, sh[buf], a.wpt);
     const float k1 = rr * sums[0] * inv_d;
-    const float qg = sums[1] - k1 * sums[2];           // sum of q G
-    const float k2 = a.alpha * gt * qg * inv_d;
+    const float qg = sums[1] - k1 * sums[2];  // sum of q G
+    const float ag = a.alpha * ry;
+    const float k2 = -ag * gt * qg * inv_d;
     if (a.gate_kind == PURO_GATE_TOKEN && in && tm.lane == 0)
       static_cast<float*>(a.dgate)[row] = a.alpha * qg;
 #pragma unroll
     for (int j = 0; j < kNV; ++j) {
-      const int n = in ? left[j] : 0;
-      const int64_t at = row * a.cols + col[j];
-      float dr[kVec], dy[kVec], dg[kVec];
+      const int n = in ? sp[j].n : 0;
+      const int64_t at = row * a.cols;
+      const uint32_t col = sp[j].col;
+      float G[kVec], o[kVec];
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        const float G = fmaf(-k1, rh[j][i], A[j][i]);
-        const float gg = g[j][i] * gt;
-        dr[i] = a.beta * G;
-        const float dp = a.alpha * gg * G;
-        dy[i] = ry * fmaf(wo[j][i], dp, -k2 * yh[j][i]);
-        dg[i] = a.alpha * yh[j][i] * wo[j][i] * G;
-        // a channel gate is factored out of the column sum, which then serves dw_post and dgate
-        acc[0][j][i] = fmaf(yh[j][i] * (channel ? 1.0f : gg), G, acc[0][j][i]);
+        G[i] = fmaf(-k1, rh[j][i], A[j][i]);
+        o[i] = a.beta * G[i];
       }
-      if (a.dr) store8(static_cast<R*>(a.dr) + at, n, dr);
+      if (a.dr) store8<true>(row_ptr<kUniform>(static_cast<R*>(a.dr), at) + col, n, o);
       if (post) {
-        store8(a.dy + at, n, dy);
-        if (a.gate_kind == PURO_GATE_FULL)
-          store8(static_cast<uint16_t*>(a.dgate) + at, n, dg);
+        if (full) {
+          float g[kVec];
+          values(graw[j], sp[j], g);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) o[i] = a.alpha * yh[j][i] * wg[j][i] * G[i];
+          store8(row_ptr<kUniform>(static_cast<uint16_t*>(a.dgate), at) + col, n, o);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) G[i] *= g[i];
+        }
+        // a channel gate is left out of the column sum, which so serves dw_post and dgate
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          G[i] *= gt;
+          acc[0][j][i] = fmaf(yh[j][i], G[i], acc[0][j][i]);
+          o[i] = fmaf(wg[j][i] * ag, G[i], k2 * yh[j][i]);
+        }
+        store8(row_ptr<kUniform>(a.dy, at) + col, n, o);
       }
     }
   }
 
-  // Column sums of the block: over its teams through LDS, then one partial per block.
+  // Column sums of the block: over the teams of a wave in registers, over the others through LDS,
+  // where each thread then sums whole columns; one partial per block.
   extern __shared__ float red[];
+  const int lanes = kLanes == 0 ? tm.lanes : kLanes == 1 ? 16 : kLanes;
+  const int rows = kLanes == 0 ? tm.teams : static_cast<int>(blockDim.x >> 6);
+  const int at = kLanes == 0 ? threadIdx.x
+                             : (threadIdx.x >> 6) * lanes + (threadIdx.x & 63);  // of kLanes lanes
+  const int width = lanes * kVec;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int j = 0; j < kNV; ++j) {
 #pragma unroll
-    for (int j = 0; j < kNV; ++j) {
-      if (tm.teams > 1) {
-        __syncthreads();
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) red[i * blockDim.x + threadIdx.x] = acc[k][j][i];
-        __syncthreads();
-        if (tm.team == 0)
-#pragma unroll
-          for (int i = 0; i < kVec; ++i)
-            for (int w = 1; w < tm.teams; ++w)
-              acc[k][j][i] += red[i * blockDim.x + w * tm.lanes + tm.lane];
-      }
-      if (tm.team == 0)
-        store8(a.partials + (int64_t(blockIdx.x) * 2 + k) * a.cols + col[j], left[j],
-               acc[k][j]);
+      for (int i = 0; i < kVec; ++i) acc[k][j][i] = teams_sum<kLanes>(acc[k][j][i]);
     }
+    if (rows == 1) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        store8(a.partials + (int64_t(blockIdx.x) * 2 + k) * a.cols + sp[j].col, sp[j].n,
+               acc[k][j]);
+      continue;
+    }
+    __syncthreads();
+    if (kLanes == 0 || kLanes == 64 || (threadIdx.x & 63) < lanes)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float4* dst = reinterpret_cast<float4*>(red + k * rows * width + at * kVec);
+        dst[0] = make_float4(acc[k][j][0], acc[k][j][1], acc[k][j][2], acc[k][j][3]);
+        dst[1] = make_float4(acc[k][j][4], acc[k][j][5], acc[k][j][6], acc[k][j][7]);
+      }
+    __syncthreads();
+    for (int t = threadIdx.x; t < 2 * width; t += blockDim.x) {
+      const int k = t >= width, c = t - k * width;
+      float v = 0.0f;
+      for (int w = 0; w < rows; ++w) v += red[(k * rows + w) * width + c];
+      if (j * width + c < a.cols)
+        a.partials[(int64_t(blockIdx.x) * 2 + k) * a.cols + j * width + c] = v;
+    }
+  }
 }
 
-// Sum of the block partials per column in a fixed order: 32 columns x 32 rows of threads
-// per block, each thread every 32nd partial.
+// Sum of the block partials per column in a fixed order: a block of 1024 threads has 32 columns,
+// four to a thread, and every 128th partial to a thread; then a tree over the threads in LDS.
 struct ReduceArgs {
   const float* partials;
   int blocks, cols, gate_kind, accumulate;
@@ -355,37 +539,55 @@ struct ReduceArgs {
   float *dw_post, *dw_pre, *dgate;
 };
 
-constexpr int kRedCols = 32, kRedRows = 32;
+constexpr int kRedCols = 32, kRedRows = 128;
 
-__global__ __launch_bounds__(kRedCols* kRedRows) void norm_reduce_kernel(const ReduceArgs a) {
-  __shared__ float sh[kRedRows][kRedCols + 1];
-  const int c = blockIdx.x * kRedCols + threadIdx.x % kRedCols;
-  const int k = blockIdx.y, y = threadIdx.x / kRedCols;
-  float t = 0.0f;
-  if (c < a.cols)
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(const ReduceArgs a) {
+  __shared__ float sh[kRedRows][kRedCols + 4];
+  const int k = blockIdx.y, y = threadIdx.x >> 3, c0 = (threadIdx.x & 7) * 4;
+  const int col = blockIdx.x * kRedCols + c0, n = a.cols - col;
+  float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (n >= 4) {
+#pragma unroll 4
+    for (int b = y; b < a.blocks; b += kRedRows) {
+      const f32x4_el v =
+          *reinterpret_cast<const f32x4_el*>(a.partials + (int64_t(b) * 2 + k) * a.cols + col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] += v[i];
+    }
+  } else {
     for (int b = y; b < a.blocks; b += kRedRows)
-      t += a.partials[(int64_t(b) * 2 + k) * a.cols + c];
-  sh[y][threadIdx.x % kRedCols] = t;
+      for (int i = 0; i < n; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          t[j] += i == j ? a.partials[(int64_t(b) * 2 + k) * a.cols + col + i] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sh[y][c0 + i] = t[i];
   __syncthreads();
-  if (y != 0 || c >= a.cols) return;
-  for (int w = 1; w < kRedRows; ++w) t += sh[w][threadIdx.x];
+  // 32 threads per column: four partials each, then over the 32 lanes
+  const int c = blockIdx.x * kRedCols + (threadIdx.x >> 5), l = threadIdx.x & 31;
+  float v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kRedRows / 32; ++i) v += sh[i * 32 + l][threadIdx.x >> 5];
+  v = lanes_sum<32>(v);
+  if (l != 0 || c >= a.cols) return;
   if (k == 1) {
-    if (a.dw_pre) a.dw_pre[c] = t + (a.accumulate ? a.dw_pre[c] : 0.0f);
+    if (a.dw_pre) a.dw_pre[c] = v + (a.accumulate ? a.dw_pre[c] : 0.0f);
     return;
   }
   const bool channel = a.gate_kind == PURO_GATE_CHANNEL;
   if (a.dw_post)
-    a.dw_post[c] = a.alpha * (channel ? a.gate[c] : 1.0f) * t +
+    a.dw_post[c] = a.alpha * (channel ? a.gate[c] : 1.0f) * v +
                    (a.accumulate ? a.dw_post[c] : 0.0f);
   if (channel && a.dgate)
-    a.dgate[c] = a.alpha * a.w_post[c] * t + (a.accumulate ? a.dgate[c] : 0.0f);
+    a.dgate[c] = a.alpha * a.w_post[c] * v + (a.accumulate ? a.dgate[c] : 0.0f);
 }
 
 // ------------------------------------------------------------------ host side
 // How a row is laid over lanes: 16, 32 or 64 lanes of 8 columns up to 512 columns, then whole
 // waves, one vector per lane up to 8192 columns and two beyond.
 struct Shape {
-  int lanes;     // 16, 32, 64, or 0 for whole waves
+  int lanes;     // 16, 32, 64, 1 (16 of which one has the row), or 0 for whole waves
   int nv;        // vectors of 8 columns per lane
   int wpt;       // waves per team (whole waves)
   int threads;   // per block
@@ -393,11 +595,11 @@ struct Shape {
 };
 
 Shape shape_of(int64_t cols, int most_threads) {
-  Shape s = {0, 1, 0, 256, 0};
+  Shape s = {0, 1, 0, most_threads, 0};
   const int64_t vecs = ceil_div(cols, kVec);
   if (vecs <= 64) {
-    s.lanes = vecs <= 16 ? 16 : vecs <= 32 ? 32 : 64;
-    s.teams = s.threads / s.lanes;
+    s.lanes = cols < kVec ? 1 : vecs <= 16 ? 16 : vecs <= 32 ? 32 : 64;
+    s.teams = s.threads / std::max(s.lanes, 16);
     return s;
   }
   s.nv = vecs <= 1024 ? 1 : 2;
@@ -413,43 +615,57 @@ bool norm_dims_ok(int64_t rows, int64_t cols) {
   return any_dim_ok(rows) && cols >= 0 && cols <= PURO_NORM_MAX_COLS;
 }
 
-// Blocks and rows per block: enough blocks to fill the chip, each with consecutive rows.
-void split_rows(int64_t rows, const Shape& s, int64_t most_blocks, int* per_block, int* blocks) {
-  const int64_t steps = ceil_div(rows, s.teams);             // of the whole grid, one team row each
-  const int64_t per = std::max<int64_t>(1, ceil_div(steps, most_blocks));
-  *per_block = static_cast<int>(per * s.teams);
-  *blocks = static_cast<int>(ceil_div(rows, *per_block));
+// Blocks and rows per block. A block keeps its weights (and column sums) over consecutive rows, so
+// the grid is at most what the chip holds at once: `waves` per CU, which the kernel's registers
+// allow, in a whole number of blocks per CU, at least half as many. Of these numbers the one whose
+// busiest CU gets the fewest row steps is taken, the larger of equals: for 8192 rows of 2048
+// columns forward 4 blocks per CU of 8 rows each (33 us) and not 5 or 6 of 7 or 6 (34 to 36 us);
+// for 5120 columns 2 blocks of ten waves (44 us) and not 4 (53 us).
+constexpr int kCus = 256;
+struct Split {
+  int blocks, rows_per_block;
+};
+Split split_rows(int64_t rows, const Shape& s, int waves, int most_blocks) {
+  const int64_t steps = ceil_div(rows, s.teams);  // of one row per team
+  const int most = std::min(most_blocks / kCus, std::max(1, waves / (s.threads / 64)));
+  int64_t per = 0, busiest = INT64_MAX;
+  for (int k = most; 2 * k >= most && k > 0; --k) {
+    const int64_t n = std::max<int64_t>(1, ceil_div(steps, int64_t(kCus) * k));
+    if (n * k < busiest) busiest = n * k, per = n;
+  }
+  Split p;
+  p.rows_per_block = static_cast<int>(per * s.teams);
+  p.blocks = static_cast<int>(ceil_div(rows, p.rows_per_block));
+  return p;
 }
-
-constexpr int kBwdBlocks = PURO_NORM_MAX_BLOCKS;
+constexpr int kFwdThreads = 256, kFwdWaves = 24;  // threads of blocks of several teams
+constexpr int kBwdThreads = 512, kBwdWaves = 16;
 
 template <typename R>
 void launch_fwd(const FwdArgs& a, const Shape& s, int blocks, hipStream_t st) {
-  const dim3 grid(blocks), block(s.threads);
-  switch (s.lanes) {
-    case 16: hipLaunchKernelGGL((norm_fwd_kernel<R, 16, 1>), grid, block, 0, st, a); return;
-    case 32: hipLaunchKernelGGL((norm_fwd_kernel<R, 32, 1>), grid, block, 0, st, a); return;
-    case 64: hipLaunchKernelGGL((norm_fwd_kernel<R, 64, 1>), grid, block, 0, st, a); return;
-  }
-  if (s.nv == 1)
-    hipLaunchKernelGGL((norm_fwd_kernel<R, 0, 1>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((norm_fwd_kernel<R, 0, 2>), grid, block, 0, st, a);
+  const auto k = s.lanes == 1    ? norm_fwd_kernel<R, 1, 1>
+                 : s.lanes == 16 ? norm_fwd_kernel<R, 16, 1>
+                 : s.lanes == 32 ? norm_fwd_kernel<R, 32, 1>
+                 : s.lanes == 64 ? norm_fwd_kernel<R, 64, 1>
+                 : s.nv == 1     ? norm_fwd_kernel<R, 0, 1>
+                                 : norm_fwd_kernel<R, 0, 2>;
+  hipLaunchKernelGGL(k, dim3(blocks), dim3(s.threads), 0, st, a);
 }
 
-template <typename R>
+template <typename R, bool kCodes>
 void launch_bwd(const BwdArgs& a, const Shape& s, int blocks, hipStream_t st) {
   const dim3 grid(blocks), block(s.threads);
-  const size_t lds = s.teams > 1 ? size_t(s.threads) * kVec * sizeof(float) : 0;
-  switch (s.lanes) {
-    case 16: hipLaunchKernelGGL((norm_bwd_kernel<R, 16, 1>), grid, block, lds, st, a); return;
-    case 32: hipLaunchKernelGGL((norm_bwd_kernel<R, 32, 1>), grid, block, lds, st, a); return;
-    case 64: hipLaunchKernelGGL((norm_bwd_kernel<R, 64, 1>), grid, block, lds, st, a); return;
-  }
-  if (s.nv == 1)
-    hipLaunchKernelGGL((norm_bwd_kernel<R, 0, 1>), grid, block, lds, st, a);
-  else
-    hipLaunchKernelGGL((norm_bwd_kernel<R, 0, 2>), grid, block, lds, st, a);
+  // two accumulators of the teams (of the waves, for teams within one) as whole rows
+  const int rows = s.lanes ? s.threads / 64 : s.teams;
+  const int lanes = s.lanes ? std::max(s.lanes, 16) : s.wpt * 64;
+  const size_t lds = rows > 1 ? size_t(2) * rows * lanes * kVec * sizeof(float) : 0;
+  const auto k = s.lanes == 1    ? norm_bwd_kernel<R, 1, 1, kCodes>
+                 : s.lanes == 16 ? norm_bwd_kernel<R, 16, 1, kCodes>
+                 : s.lanes == 32 ? norm_bwd_kernel<R, 32, 1, kCodes>
+                 : s.lanes == 64 ? norm_bwd_kernel<R, 64, 1, kCodes>
+                 : s.nv == 1     ? norm_bwd_kernel<R, 0, 1, kCodes>
+                                 : norm_bwd_kernel<R, 0, 2, kCodes>;
+  hipLaunchKernelGGL(k, grid, block, lds, st, a);
 }
 
 // A pair of code and scale pointers: both or neither.
@@ -496,27 +712,25 @@ extern "C" puro_status puro_block_norm_fwd(const puro_block_norm* d, void* strea
   PURO_TRY(check_pair(d->yq, d->ys));
   PURO_TRY(check_pair(d->rq, d->rs));
 
-  const Shape s = shape_of(d->cols, 256);
+  const Shape s = shape_of(d->cols, kFwdThreads);
   FwdArgs a = {static_cast<const uint16_t*>(d->y), d->r, d->w_post, d->w_pre, d->gate,
                d->gate_kind, d->pow2, d->rows, static_cast<int>(d->cols), s.wpt, 0, d->alpha,
                d->beta, d->eps, d->r_out, static_cast<uint16_t*>(d->n),
                static_cast<uint8_t*>(d->nq), d->ns, d->rstd_y, d->rstd_r,
                static_cast<uint8_t*>(d->yq), d->ys, static_cast<uint8_t*>(d->rq), d->rs};
-  int blocks;
-  split_rows(d->rows, s, 2048, &a.rows_per_block, &blocks);
+  const Split p = split_rows(d->rows, s, kFwdWaves, INT32_MAX);
+  a.rows_per_block = p.rows_per_block;
   if (d->residual_type == PURO_TYPE_BF16)
-    launch_fwd<uint16_t>(a, s, blocks, static_cast<hipStream_t>(stream));
+    launch_fwd<uint16_t>(a, s, p.blocks, static_cast<hipStream_t>(stream));
   else
-    launch_fwd<float>(a, s, blocks, static_cast<hipStream_t>(stream));
+    launch_fwd<float>(a, s, p.blocks, static_cast<hipStream_t>(stream));
   return launch_status();
 }
 
 extern "C" int64_t puro_block_norm_workspace(int64_t rows, int64_t cols) {
   if (!norm_dims_ok(rows, cols) || rows == 0 || cols == 0) return 0;
-  const Shape s = shape_of(cols, 512);
-  int per, blocks;
-  split_rows(rows, s, kBwdBlocks, &per, &blocks);
-  return int64_t(blocks) * 2 * cols * sizeof(float);
+  const Shape s = shape_of(cols, kBwdThreads);
+  return int64_t(split_rows(rows, s, kBwdWaves, PURO_NORM_MAX_BLOCKS).blocks) * 2 * cols * sizeof(float);
 }
 
 extern "C" puro_status puro_block_norm_bwd(const puro_block_norm_grad* d, void* workspace,
@@ -551,6 +765,7 @@ extern "C" puro_status puro_block_norm_bwd(const puro_block_norm_grad* d, void* 
     }
     PURO_TRY(check_pair(d->yq, d->ys));
     PURO_TRY(check_pair(d->rq, d->rs));
+    if ((d->yq && d->r) || (d->y && d->rq)) return PURO_ERR_ARG;  // one form for both
     PURO_TRY(check_ptr(workspace, false));
   }
   if (post) {
@@ -566,7 +781,7 @@ extern "C" puro_status puro_block_norm_bwd(const puro_block_norm_grad* d, void* 
   PURO_TRY(check_optional(d->dw_pre));
 
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const Shape s = shape_of(d->cols, 512);
+  const Shape s = shape_of(d->cols, kBwdThreads);
   int blocks = 0;
   if (!empty) {
     BwdArgs a = {d->dr_out, static_cast<const uint16_t*>(d->dn),
@@ -575,11 +790,14 @@ extern "C" puro_status puro_block_norm_bwd(const puro_block_norm_grad* d, void* 
                  d->w_pre, d->gate, d->gate_kind, d->rows, static_cast<int>(d->cols), s.wpt, 0,
                  d->alpha, d->beta, d->dr, static_cast<uint16_t*>(d->dy), d->dgate,
                  static_cast<float*>(workspace)};
-    split_rows(d->rows, s, kBwdBlocks, &a.rows_per_block, &blocks);
-    if (d->residual_type == PURO_TYPE_BF16)
-      launch_bwd<uint16_t>(a, s, blocks, st);
-    else
-      launch_bwd<float>(a, s, blocks, st);
+    const Split p = split_rows(d->rows, s, kBwdWaves, PURO_NORM_MAX_BLOCKS);
+    a.rows_per_block = p.rows_per_block;
+    blocks = p.blocks;
+    const bool codes = d->yq != nullptr || d->rq != nullptr;
+    const auto launch = d->residual_type == PURO_TYPE_BF16
+                            ? (codes ? launch_bwd<uint16_t, true> : launch_bwd<uint16_t, false>)
+                            : (codes ? launch_bwd<float, true> : launch_bwd<float, false>);
+    launch(a, s, blocks, st);
     PURO_TRY(launch_status());
   }
   const bool channel = d->gate_kind == PURO_GATE_CHANNEL;
@@ -590,6 +808,6 @@ extern "C" puro_status puro_block_norm_bwd(const puro_block_norm_grad* d, void* 
                          channel ? static_cast<float*>(d->dgate) : nullptr};
   hipLaunchKernelGGL(norm_reduce_kernel,
                      dim3(static_cast<uint32_t>(ceil_div(d->cols, kRedCols)), 2),
-                     dim3(kRedCols * kRedRows), 0, st, ra);
+                     dim3(1024), 0, st, ra);
   return launch_status();
 }

@@ -20,7 +20,7 @@ __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
 }
 
-// One row of eight: values of g and u, from bf16 or from the checkpoint.
+// Eight columns of g and u of one row, from bf16 or from the checkpoint.
 struct GuSource {
   const uint16_t* gu;   // bf16 [rows][2f], or NULL
   const uint8_t* q;     // codes [rows][2f]
@@ -28,45 +28,44 @@ struct GuSource {
 };
 template <bool kCodes>
 struct GuRaw {
-  u32x4_el g, u;
+  Bf16x8 g, u;
 };
 template <>
 struct GuRaw<true> {
-  u32x2_el g, u;
+  Fp8x8 g, u;
   float sg, su;
 };
-template <bool kCodes>
+template <bool kCodes, bool kShort>
 __device__ __forceinline__ GuRaw<kCodes> load_gu(const GuSource& a, int64_t rows, int64_t f,
                                                  int64_t chunks, int64_t row, int64_t c,
-                                                 int64_t col, int n) {
+                                                 const Span<kShort>& sp) {
   GuRaw<kCodes> o;
-  const int64_t at = row * 2 * f + col;
   if constexpr (kCodes) {
-    o.g = load_raw<true>(a.q + at, n);
-    o.u = load_raw<true>(a.q + at + f, n);
-    o.sg = n > 0 ? a.s[c * rows + row] : 0.0f;
-    o.su = n > 0 ? a.s[(chunks + c) * rows + row] : 0.0f;
+    load<true, kShort>(o.g, a.q + row * 2 * f, sp);
+    load<true, kShort>(o.u, a.q + row * 2 * f + f, sp);
+    o.sg = a.s[c * rows + row];
+    o.su = a.s[(chunks + c) * rows + row];
   } else {
-    o.g = load_raw<true>(a.gu + at, n);
-    o.u = load_raw<true>(a.gu + at + f, n);
+    load<true, kShort>(o.g, a.gu + row * 2 * f, sp);
+    load<true, kShort>(o.u, a.gu + row * 2 * f + f, sp);
   }
   return o;
 }
-template <bool kCodes>
-__device__ __forceinline__ void values(const GuRaw<kCodes>& w, float* g, float* u) {
+template <bool kCodes, bool kShort>
+__device__ __forceinline__ void gu_values(const GuRaw<kCodes>& w, const Span<kShort>& sp, float* g,
+                                          float* u) {
   if constexpr (kCodes) {
-    decode8(w.g, w.sg, g);
-    decode8(w.u, w.su, u);
+    values(w.g, sp, w.sg, g);
+    values(w.u, sp, w.su, u);
   } else {
-    widen8(w.g, g);
-    widen8(w.u, u);
+    values(w.g, sp, g);
+    values(w.u, sp, u);
   }
 }
 
 // ------------------------------------------------------------------ forward
-// As the 1x128 quantisers: a 256-thread block covers 64 rows of one 128-column chunk of h.
-constexpr int kPasses = 4;
-constexpr int kRowsPerBlock = 16 * kPasses;
+// Tiles of h as RowTile lays them out.
+constexpr int kPasses = RowTile::kPasses;
 
 struct FwdArgs {
   const uint16_t* gu;
@@ -79,40 +78,39 @@ struct FwdArgs {
   int pow2;
 };
 
+template <bool kShort>
 __global__ __launch_bounds__(256) void swiglu_fwd_kernel(const FwdArgs a) {
   const int64_t chunks = (a.f + 127) >> 7;
-  const int64_t c = blockIdx.x % chunks;
-  const int64_t r0 = blockIdx.x / chunks * kRowsPerBlock + (threadIdx.x >> 4);
+  const RowTile t(a.f, off_lines(a.f));
   const int l16 = threadIdx.x & 15;
-  const int64_t col = c * 128 + l16 * kVec;
-  const int n = static_cast<int>(min(a.f - col, int64_t(kVec)));
+  const int64_t c = t.chunk, col = t.col;
+  const Span<kShort> sp(col, a.f, a.f % (128 * RowTile::kChunks) != 0);
+  const int n = sp.n;
   const GuSource src = {a.gu, nullptr, nullptr};
   GuRaw<false> raw[kPasses];
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int64_t row = r0 + 16 * p;
-    raw[p] = load_gu<false>(src, a.rows, a.f, chunks, row, c, col, row < a.rows ? n : 0);
-  }
+  for (int p = 0; p < kPasses; ++p)  // rows past the end read the last one again
+    raw[p] = load_gu<false, kShort>(src, a.rows, a.f, chunks, min(t.row(p), a.rows - 1), c, sp);
   const bool pow2 = a.pow2 != 0;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int64_t row = r0 + 16 * p;
+    const int64_t row = t.row(p);
     const bool in = row < a.rows;
     float v[3][kVec];  // g, u, h
-    values<false>(raw[p], v[0], v[1]);
+    gu_values<false, kShort>(raw[p], sp, v[0], v[1]);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) v[2][i] = v[0][i] * sigmoid(v[0][i]) * v[1][i];
     if (a.h != nullptr && in) store8(a.h + row * a.f + col, n, v[2]);
     const RowGroups<3> g = row_groups<true, 3>(v, pow2);
-    if (!in) continue;
+    if (!in || c >= chunks) continue;
     if (a.hq != nullptr) {
       store8(a.hq + row * a.f + col, n, encode8(v[2], g.r[2]));
       if (l16 == 2) a.hs[c * a.rows + row] = g.s;
     }
     if (a.guq != nullptr) {
       uint8_t* q = a.guq + row * 2 * a.f + col;
-      store8(q, n, encode8(v[0], g.r[0]));
-      store8(q + a.f, n, encode8(v[1], g.r[1]));
+      store8<true>(q, n, encode8(v[0], g.r[0]));
+      store8<true>(q + a.f, n, encode8(v[1], g.r[1]));
       if (l16 < 2) a.gus[(l16 * chunks + c) * a.rows + row] = g.s;
     }
   }
@@ -126,40 +124,38 @@ struct BwdArgs {
   uint16_t* dgu;
 };
 
-template <bool kCodes>
+template <bool kCodes, bool kShort>
 __global__ __launch_bounds__(256) void swiglu_bwd_kernel(const BwdArgs a) {
   const int64_t chunks = (a.f + 127) >> 7;
-  const int64_t c = blockIdx.x % chunks;
-  const int64_t r0 = blockIdx.x / chunks * kRowsPerBlock + (threadIdx.x >> 4);
-  const int64_t col = c * 128 + (threadIdx.x & 15) * kVec;
-  const int n = static_cast<int>(min(a.f - col, int64_t(kVec)));
+  const RowTile t(a.f, off_lines(a.f));
+  const int64_t c = min(t.chunk, chunks - 1), col = t.col;
+  const Span<kShort> sp(col, a.f, a.f % (128 * RowTile::kChunks) != 0);
   GuRaw<kCodes> raw[kPasses];
-  u32x4_el dhr[kPasses];
+  Bf16x8 dhr[kPasses];
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int64_t row = r0 + 16 * p;
-    const int k = row < a.rows ? n : 0;
-    raw[p] = load_gu<kCodes>(a.src, a.rows, a.f, chunks, row, c, col, k);
-    dhr[p] = load_raw<true>(a.dh + row * a.f + col, k);
+  for (int p = 0; p < kPasses; ++p) {  // rows past the end read the last one again
+    const int64_t row = min(t.row(p), a.rows - 1);
+    raw[p] = load_gu<kCodes, kShort>(a.src, a.rows, a.f, chunks, row, c, sp);
+    load<true, kShort>(dhr[p], a.dh + row * a.f, sp);
   }
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int64_t row = r0 + 16 * p;
+    const int64_t row = t.row(p);
     if (row >= a.rows) break;
     float g[kVec], u[kVec], dh[kVec];
-    values<kCodes>(raw[p], g, u);
-    widen8(dhr[p], dh);
+    gu_values<kCodes, kShort>(raw[p], sp, g, u);
+    values(dhr[p], sp, dh);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const float sg = sigmoid(g[i]);
-      const float t = dh[i] * sg;
+      const float w = dh[i] * sg;
       const float gi = g[i];
-      g[i] = t * u[i] * fmaf(gi, 1.0f - sg, 1.0f);
-      u[i] = t * gi;
+      g[i] = w * u[i] * fmaf(gi, 1.0f - sg, 1.0f);
+      u[i] = w * gi;
     }
     uint16_t* o = a.dgu + row * 2 * a.f + col;
-    store8(o, n, g);
-    store8(o + a.f, n, u);
+    store8(o, sp.n, g);
+    store8(o + a.f, sp.n, u);
   }
 }
 
@@ -184,7 +180,8 @@ template <bool kCodes>
 __global__ __launch_bounds__(kTileThreads, 4) void swiglu_bwd_fp8_kernel(const BwdFp8Args a) {
   __shared__ ColTile<3> sh;
   const int64_t chunks = a.f >> 7;
-  const int64_t c = blockIdx.x % chunks, mb = blockIdx.x / chunks;
+  const uint32_t across = static_cast<uint32_t>(chunks);
+  const int64_t c = blockIdx.x % across, mb = blockIdx.x / across;
   const int l16 = threadIdx.x & 15;
   const uint32_t f = static_cast<uint32_t>(a.f);
   const uint32_t r4 = (threadIdx.x >> 4) * kTileRows;  // first of the thread's rows in the tile
@@ -194,17 +191,20 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_bwd_fp8_kernel(const B
   float v[3][kTileRows][kVec];  // dg, du, h
   {
     GuRaw<kCodes> raw[kTileRows];
-    u32x4_el dhr[kTileRows];
+    Bf16x8 dhr[kTileRows];
+    constexpr bool kShort = false;
+    Span<kShort> sp;  // whole groups: never cut short
+    sp.at = 0, sp.n = kVec, sp.cut = false;
 #pragma unroll
     for (int p = 0; p < kTileRows; ++p) {
       if constexpr (kCodes) {
-        raw[p].g = load_raw<true>(a.src.q + base2 + p * 2 * a.f + at2, kVec);
-        raw[p].u = load_raw<true>(a.src.q + base2 + p * 2 * a.f + a.f + at2, kVec);
+        load<true, kShort>(raw[p].g, a.src.q + base2 + p * 2 * a.f + at2, sp);
+        load<true, kShort>(raw[p].u, a.src.q + base2 + p * 2 * a.f + a.f + at2, sp);
       } else {
-        raw[p].g = load_raw<true>(a.src.gu + base2 + p * 2 * a.f + at2, kVec);
-        raw[p].u = load_raw<true>(a.src.gu + base2 + p * 2 * a.f + a.f + at2, kVec);
+        load<true, kShort>(raw[p].g, a.src.gu + base2 + p * 2 * a.f + at2, sp);
+        load<true, kShort>(raw[p].u, a.src.gu + base2 + p * 2 * a.f + a.f + at2, sp);
       }
-      dhr[p] = load_raw<true>(a.dh + base1 + p * a.f + at1, kVec);
+      load<true, kShort>(dhr[p], a.dh + base1 + p * a.f + at1, sp);
     }
     if constexpr (kCodes) {
       const float4 sg = *reinterpret_cast<const float4*>(a.src.s + c * a.rows + mb * 128 + r4);
@@ -216,8 +216,8 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_bwd_fp8_kernel(const B
 #pragma unroll
     for (int p = 0; p < kTileRows; ++p) {
       float g[kVec], u[kVec], dh[kVec];
-      values<kCodes>(raw[p], g, u);
-      widen8(dhr[p], dh);
+      gu_values<kCodes, kShort>(raw[p], sp, g, u);
+      values(dhr[p], sp, dh);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
         const float sg = sigmoid(g[i]);
@@ -280,11 +280,12 @@ extern "C" puro_status puro_swiglu_fwd(const void* gu, int64_t rows, int64_t f, 
     PURO_TRY(check_ptr(guq, false));
     PURO_TRY(check_ptr(gus, false));
   }
-  const int64_t blocks = ceil_div(rows, kRowsPerBlock) * ceil_div(f, 128);
+  const int64_t blocks = row_tiles(rows, f);
   if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
   const FwdArgs a = {static_cast<const uint16_t*>(gu), rows, f, static_cast<uint16_t*>(h),
                      static_cast<uint8_t*>(hq), hs, static_cast<uint8_t*>(guq), gus, pow2};
-  hipLaunchKernelGGL(swiglu_fwd_kernel, dim3(static_cast<uint32_t>(blocks)), dim3(256), 0,
+  const auto k = f < kVec ? swiglu_fwd_kernel<true> : swiglu_fwd_kernel<false>;
+  hipLaunchKernelGGL(k, dim3(static_cast<uint32_t>(blocks)), dim3(256), 0,
                      static_cast<hipStream_t>(stream), a);
   return launch_status();
 }
@@ -298,18 +299,16 @@ extern "C" puro_status puro_swiglu_bwd(const void* dh, const void* gu, const voi
   PURO_TRY(check_gu(gu, guq, gus, empty));
   PURO_TRY(check_ptr(dgu, empty));
   if (empty) return PURO_OK;
-  const int64_t blocks = ceil_div(rows, kRowsPerBlock) * ceil_div(f, 128);
+  const int64_t blocks = row_tiles(rows, f);
   if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
   const BwdArgs a = {static_cast<const uint16_t*>(dh),
                      {static_cast<const uint16_t*>(gu), static_cast<const uint8_t*>(guq), gus},
                      rows, f, static_cast<uint16_t*>(dgu)};
   const dim3 grid(static_cast<uint32_t>(blocks));
-  if (gu != nullptr)
-    hipLaunchKernelGGL(swiglu_bwd_kernel<false>, grid, dim3(256), 0,
-                       static_cast<hipStream_t>(stream), a);
-  else
-    hipLaunchKernelGGL(swiglu_bwd_kernel<true>, grid, dim3(256), 0,
-                       static_cast<hipStream_t>(stream), a);
+  const auto k = gu != nullptr
+                     ? (f < kVec ? swiglu_bwd_kernel<false, true> : swiglu_bwd_kernel<false, false>)
+                     : (f < kVec ? swiglu_bwd_kernel<true, true> : swiglu_bwd_kernel<true, false>);
+  hipLaunchKernelGGL(k, grid, dim3(256), 0, static_cast<hipStream_t>(stream), a);
   return launch_status();
 }
 

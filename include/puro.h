@@ -332,7 +332,9 @@ puro_status puro_block_norm_fwd(const puro_block_norm* desc, void* stream);
  *           (PURO_GATE_TOKEN) or as it is (PURO_GATE_FULL), in the gate's type
  * accumulate = 1 adds dw_post, dw_pre and a channel gate's gradient to what is there. w_post NULL:
  * the norm after the block was left out; w_pre NULL: the norm before the next one. workspace: puro_block_norm_workspace(rows, cols) bytes
- * of caller-owned device memory, 16-byte aligned, used by one call at a time. */
+ * of caller-owned device memory, 16-byte aligned, used by one call at a time (at most
+ * PURO_NORM_MAX_BLOCKS partial sums of 8 bytes per column). y and r are both as they were or both
+ * checkpoints. */
 #define PURO_NORM_MAX_BLOCKS 512
 typedef struct {
   int64_t rows, cols;
