@@ -84,9 +84,10 @@ SIGNATURES.update({
     "puro_ckpt_pack": ([_P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P], _INT),
     "puro_ckpt_unpack": ([_P, _P, _I64, _I64, _P, _INT, _I64, _P], _INT),
     "puro_ckpt_transpose": ([_P, _P, _I64, _I64, _INT, _P, _P, _P], _INT),
-    "puro_block_norm_fwd": ([ctypes.POINTER(PuroBlockNorm), _P], _INT),
+    # (the structures as bytes, or by reference)
+    "puro_block_norm_fwd": ([_P, _P], _INT),
     "puro_block_norm_workspace": ([_I64, _I64], _I64),
-    "puro_block_norm_bwd": ([ctypes.POINTER(PuroBlockNormGrad), _P, _P], _INT),
+    "puro_block_norm_bwd": ([_P, _P, _P], _INT),
     "puro_swiglu_fwd": ([_P, _I64, _I64, _P, _P, _P, _P, _P, _INT, _P], _INT),
     "puro_swiglu_bwd": ([_P, _P, _P, _P, _I64, _I64, _P, _P], _INT),
     "puro_swiglu_bwd_fp8": ([_P, _P, _P, _P, _I64, _I64, _INT] + [_P] * 7, _INT),

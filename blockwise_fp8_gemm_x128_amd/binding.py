@@ -8,6 +8,7 @@ computation runs in libpuro's HIP kernels; there is no other code path.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -19,11 +20,22 @@ from ._lib import (GATE_CHANNEL, GATE_FULL, GATE_NONE, GATE_TOKEN, OPT_WORKSPACE
 FP8 = torch.uint8  # E4M3 codes travel as raw bytes
 
 
+# torch's current stream as its raw handle, without the Stream object around it where torch offers
+# that (1.8 us less per call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev: torch.device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape, dev) -> None:
+    # the whole check at once first: it is what nearly every call passes, a dozen times a call
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.device == dev):
+        return
     if not isinstance(t, torch.Tensor):
         raise PuroError(f"{name}: expected a torch.Tensor")
     if t.dtype != dtype:
@@ -251,15 +263,55 @@ def puro_adamw_step(p, g, m, v, lr, beta1, beta2, eps, weight_decay, step, p_bf1
 
 # ---------------------------------------------------------------- between the GEMMs
 # 8-bit checkpoints are pairs (codes uint8 [rows, cols], scales fp32 [ceil(cols/128), rows]).
+#
+# These operators take up to fifteen tensors, and small calls are launch-bound, so their checks and
+# addresses come from one native call (csrc/args.cpp) per operator call; where it finds a tensor
+# that is not as specified, _need says what is wrong with it.
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_FP32}
+_DTYPES = {"b": torch.bfloat16, "f": torch.float32, "q": FP8}
+_LETTERS = {torch.bfloat16: "b", torch.float32: "f"}
+
+
+class _Spec:
+    """Expected tensors of a call, "name:tfij" each: t the type (b bf16, f fp32, q codes), f whether
+    it is required (!) or may be None (?), i and j which of the call's sizes d0, d1, d2 and 1 (3)
+    its sizes are (- for a vector)."""
+
+    def __init__(self, text: str):
+        pairs = [item.split(":") for item in text.split()]
+        self.names = [n for n, _ in pairs]
+        self.code = "".join(c for _, c in pairs).encode()
+
+    def pointers(self, dev, d0, d1, d2, *tensors):
+        p = _args().ptrs(self.code, dev.index, d0, d1, d2, *tensors)
+        if type(p) is not int:
+            return p
+        kind, need, *dims = self.code[4 * p:4 * p + 4].decode()
+        name = self.names[p]
+        if tensors[p] is None:
+            raise PuroError(f"{name}: required")
+        shape = tuple((d0, d1, d2, 1)[int(i)] for i in dims if i != "-")
+        _need(tensors[p], name, _DTYPES[kind], shape, dev)
+        raise PuroError(f"{name}: not as expected")
+
+
+_args_module = None
+
+
+def _args():
+    global _args_module
+    if _args_module is None:
+        try:
+            from . import _args as module
+        except ImportError as e:
+            raise PuroError("the binding's native checks are not built (%s); run `python -m "
+                            "blockwise_fp8_gemm_x128_amd.build`" % e) from e
+        _args_module = module
+    return _args_module
 
 
 def _groups(n: int) -> int:
     return (n + 127) // 128
-
-
-def _ptr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
 
 
 def _new_codes(rows, cols, dev):
@@ -267,9 +319,10 @@ def _new_codes(rows, cols, dev):
             torch.empty((_groups(cols), rows), dtype=torch.float32, device=dev))
 
 
-def _need_codes(q, s, name, rows, cols, dev, groups=None) -> None:
-    _need(q, name + " codes", FP8, (rows, cols), dev)
-    _need(s, name + " scales", torch.float32, (groups or _groups(cols), rows), dev)
+def _matrix(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise PuroError(f"{name}: expected a matrix")
+    return t.shape
 
 
 def _need_rows(x, name, dev):
@@ -279,10 +332,16 @@ def _need_rows(x, name, dev):
     if x.device != dev:
         raise PuroError(f"{name}: on {x.device}, expected {dev}")
     rows, cols = x.shape
-    ld = x.stride(0) if rows > 1 else cols
-    if (cols > 1 and x.stride(1) != 1) or ld < cols:
+    ld, unit = x.stride()
+    if rows <= 1:
+        ld = cols
+    if (cols > 1 and unit != 1) or ld < cols:
         raise PuroError(f"{name}: columns must be adjacent and rows must not overlap")
     return _TYPES[x.dtype], ld
+
+
+_PACK = _Spec("q:q!01 s:f!20")
+_TRANSPOSE = _Spec("checkpoint:q!01 scales:f!20 qt:q!10")
 
 
 def puro_ckpt_pack(x: torch.Tensor, q=None, s=None, pow2: bool = False):
@@ -291,10 +350,11 @@ def puro_ckpt_pack(x: torch.Tensor, q=None, s=None, pow2: bool = False):
     dev = _dev(x)
     kind, ld = _need_rows(x, "x", dev)
     rows, cols = x.shape
-    q = _out(q, "q", FP8, (rows, cols), dev)
-    s = _out(s, "s", torch.float32, (_groups(cols), rows), dev)
-    check(lib().puro_ckpt_pack(x.data_ptr(), kind, rows, cols, ld, bool(pow2), q.data_ptr(),
-                               s.data_ptr(), _stream(dev)))
+    if q is None or s is None:
+        new = _new_codes(rows, cols, dev)
+        q, s = new[0] if q is None else q, new[1] if s is None else s
+    p = _PACK.pointers(dev, rows, cols, _groups(cols), q, s)
+    check(lib().puro_ckpt_pack(x.data_ptr(), kind, rows, cols, ld, bool(pow2), *p, _stream(dev)))
     return q, s
 
 
@@ -302,15 +362,14 @@ def puro_ckpt_unpack(q, s, x=None, dtype=torch.bfloat16):
     """The values a checkpoint stands for, as `dtype` (bf16 or fp32) or into x (rows may be
     strided)."""
     dev = _dev(q)
-    rows, cols = q.shape
-    _need_codes(q, s, "checkpoint", rows, cols, dev)
+    rows, cols = _matrix(q, "checkpoint")
     if x is None:
         x = torch.empty((rows, cols), dtype=dtype, device=dev)
     kind, ld = _need_rows(x, "x", dev)
-    if tuple(x.shape) != (rows, cols):
+    if x.shape != (rows, cols):
         raise PuroError(f"x: shape {tuple(x.shape)}, expected {(rows, cols)}")
-    check(lib().puro_ckpt_unpack(q.data_ptr(), s.data_ptr(), rows, cols, x.data_ptr(), kind, ld,
-                                 _stream(dev)))
+    p = _PACK.pointers(dev, rows, cols, _groups(cols), q, s)
+    check(lib().puro_ckpt_unpack(*p, rows, cols, x.data_ptr(), kind, ld, _stream(dev)))
     return x
 
 
@@ -318,12 +377,14 @@ def puro_ckpt_transpose(q, s, qt=None, st=None, pow2: bool = False):
     """Checkpoint [rows, cols] -> checkpoint of its transpose (qt uint8 [cols, rows], st fp32
     [ceil(rows/128), cols]): a forward GEMM operand becomes the weight gradient's."""
     dev = _dev(q)
-    rows, cols = q.shape
-    _need_codes(q, s, "checkpoint", rows, cols, dev)
-    qt = _out(qt, "qt", FP8, (cols, rows), dev)
-    st = _out(st, "st", torch.float32, (_groups(rows), cols), dev)
-    check(lib().puro_ckpt_transpose(q.data_ptr(), s.data_ptr(), rows, cols, bool(pow2),
-                                    qt.data_ptr(), st.data_ptr(), _stream(dev)))
+    rows, cols = _matrix(q, "checkpoint")
+    if qt is None or st is None:
+        new = _new_codes(cols, rows, dev)
+        qt, st = new[0] if qt is None else qt, new[1] if st is None else st
+    p = _TRANSPOSE.pointers(dev, rows, cols, _groups(cols), q, s, qt)
+    _need(st, "st", torch.float32, (_groups(rows), cols), dev)
+    check(lib().puro_ckpt_transpose(p[0], p[1], rows, cols, bool(pow2), p[2], st.data_ptr(),
+                                    _stream(dev)))
     return qt, st
 
 
@@ -350,19 +411,35 @@ class BlockNormGrads(NamedTuple):
     dgate: Optional[torch.Tensor]
 
 
-def _gate(gate, rows, cols, dev, name="gate"):
+# puro_block_norm and puro_block_norm_grad packed as bytes, a third of the time of filling a ctypes
+# structure field by field.
+_NORM = struct.Struct("@qqiiifff15P")
+_NORM_GRAD = struct.Struct("@qqiiiff18P")
+assert _NORM.size == ctypes.sizeof(PuroBlockNorm)
+assert _NORM_GRAD.size == ctypes.sizeof(PuroBlockNormGrad)
+
+# How a gate is specified, by its kind.
+_GATES = {GATE_NONE: "f?1-", GATE_CHANNEL: "f!1-", GATE_TOKEN: "f!03", GATE_FULL: "b!01"}
+_NORM_FWD = {(dtype, kind): _Spec(
+    f"y:b?01 r:{r}!01 w_post:f?1- w_pre:f?1- gate:{g} r_out:{r}?01 n:b?01 nq:q?01 ns:f?20 "
+    "rstd_y:f?0- rstd_r:f?0- yq:q?01 ys:f?20 rq:q?01 rs:f?20")
+    for dtype, r in _LETTERS.items() for kind, g in _GATES.items()}
+_NORM_BWD = {(dtype, kind): _Spec(
+    f"dr_out:{r}?01 dn:b?01 y:b?01 y:q?01 y:f?20 r_out:{r}?01 r_out:q?01 r_out:f?20 rstd_y:f?0- "
+    f"rstd_r:f?0- w_post:f?1- w_pre:f?1- gate:{g} dr:{r}?01 dy:b?01 dw_post:f?1- dw_pre:f?1- "
+    f"dgate:{g}") for dtype, r in _LETTERS.items() for kind, g in _GATES.items()}
+
+
+def _gate_kind(gate) -> int:
     """fp32 [cols] is a gate per channel, fp32 [rows, 1] one per token, bf16 [rows, cols] one per
-    element. Returns (kind, pointer)."""
+    element."""
     if gate is None:
-        return GATE_NONE, None
+        return GATE_NONE
+    if not isinstance(gate, torch.Tensor):
+        raise PuroError("gate: expected a torch.Tensor")
     if gate.dim() == 1:
-        kind, dtype, shape = GATE_CHANNEL, torch.float32, (cols,)
-    elif gate.dtype == torch.float32:
-        kind, dtype, shape = GATE_TOKEN, torch.float32, (rows, 1)
-    else:
-        kind, dtype, shape = GATE_FULL, torch.bfloat16, (rows, cols)
-    _need(gate, name, dtype, shape, dev)
-    return kind, gate.data_ptr()
+        return GATE_CHANNEL
+    return GATE_TOKEN if gate.dtype is torch.float32 else GATE_FULL
 
 
 def puro_block_norm_fwd(y, r, w_post, w_pre, gate=None, alpha: float = 1.0, beta: float = 1.0,
@@ -377,60 +454,46 @@ def puro_block_norm_fwd(y, r, w_post, w_pre, gate=None, alpha: float = 1.0, beta
     ten outputs to write (a BlockNorm or a tuple in its order, None to leave one out) instead of
     new ones; out.r_out may be r."""
     dev = _dev(r)
-    if r.dim() != 2 or r.dtype not in _TYPES:
-        raise PuroError("r: expected a bf16 or fp32 matrix")
-    rows, cols = shape = tuple(r.shape)
-    f32, bf16 = torch.float32, torch.bfloat16
-    _need(r, "r", r.dtype, shape, dev)
-    post, pre = y is not None, w_pre is not None
-    if post:
-        _need(y, "y", bf16, shape, dev)
-        _need(w_post, "w_post", f32, (cols,), dev)
-    if pre:
-        _need(w_pre, "w_pre", f32, (cols,), dev)
-    kind, gp = _gate(gate, rows, cols, dev)
+    rows, cols = _matrix(r, "r")
+    dtype = r.dtype
+    if dtype not in _TYPES:
+        raise PuroError("r: expected bf16 or fp32")
+    kind = _gate_kind(gate)
     if out is None:
         if n not in ("fp8", "bf16", "both"):
             raise PuroError("n: expected 'fp8', 'bf16' or 'both'")
-        none = (None, None)
+        post, pre, none, f32 = y is not None, w_pre is not None, (None, None), torch.float32
         out = BlockNorm(
             torch.empty_like(r) if post or beta != 1.0 else None,
-            torch.empty(shape, dtype=bf16, device=dev) if pre and n != "fp8" else None,
+            torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+            if pre and n != "fp8" else None,
             *(_new_codes(rows, cols, dev) if pre and n != "bf16" else none),
             torch.empty((rows,), dtype=f32, device=dev) if post else None,
             torch.empty((rows,), dtype=f32, device=dev) if pre else None,
             *(_new_codes(rows, cols, dev) if post and ckpt else none),
             *(_new_codes(rows, cols, dev) if ckpt else none))
-    else:
+    elif type(out) is not BlockNorm:
         out = BlockNorm(*out)
-        for t, name, dtype, want in ((out.r_out, "r_out", r.dtype, shape),
-                                     (out.n, "n", bf16, shape),
-                                     (out.rstd_y, "rstd_y", f32, (rows,)),
-                                     (out.rstd_r, "rstd_r", f32, (rows,))):
-            if t is not None:
-                _need(t, name, dtype, want, dev)
-        for q, s, name in ((out.nq, out.ns, "n"), (out.yq, out.ys, "y"), (out.rq, out.rs, "r")):
-            if q is not None or s is not None:
-                _need_codes(q, s, name, rows, cols, dev)
-    d = PuroBlockNorm(rows, cols, _TYPES[r.dtype], kind, bool(pow2), alpha, beta, eps, _ptr(y),
-                      r.data_ptr(), _ptr(w_post) if post else None, _ptr(w_pre), gp,
-                      *map(_ptr, out))
-    check(lib().puro_block_norm_fwd(ctypes.byref(d), _stream(dev)))
+    p = _NORM_FWD[dtype, kind].pointers(dev, rows, cols, (cols + 127) // 128, y, r,
+                                        None if y is None else w_post, w_pre, gate, *out)
+    st = lib().puro_block_norm_fwd(_NORM.pack(rows, cols, _TYPES[dtype], kind, bool(pow2), alpha,
+                                              beta, eps, *p), _stream(dev))
+    if st:
+        check(st)
     return out
 
 
-def _saved(x, name, dtype, shape, dev, where):
-    """A saved activation, as it was or as its checkpoint (codes, scales): (x, q, s) pointers."""
-    if x is None:
-        if where:
-            raise PuroError(f"{name}: required")
+def _saved(x, name, wanted):
+    """A saved activation, as it was or as its checkpoint (codes, scales): (x, q, s)."""
+    if not wanted:
         return None, None, None
     if isinstance(x, (tuple, list)):
-        q, s = x
-        _need_codes(q, s, name, *shape, dev)
-        return None, q.data_ptr(), s.data_ptr()
-    _need(x, name, dtype, shape, dev)
-    return x.data_ptr(), None, None
+        if len(x) != 2:
+            raise PuroError(f"{name}: expected a (codes, scales) pair")
+        return None, x[0], x[1]
+    if x is None:
+        raise PuroError(f"{name}: required")
+    return x, None, None
 
 
 def block_norm_workspace(rows: int, cols: int, dev) -> torch.Tensor:
@@ -443,61 +506,47 @@ def puro_block_norm_bwd(dr_out, dn, y, r_out, rstd_y, rstd_r, w_post, w_pre, gat
                         alpha: float = 1.0, beta: float = 1.0, accumulate: bool = False,
                         workspace=None, out=None) -> BlockNormGrads:
     """Gradients of puro_block_norm_fwd from those of r_out (dr_out, None for zero) and n (dn
-    bf16, None if w_pre was). y and r_out: the saved tensors, or their checkpoints as (codes,
-    scales) pairs; rstd_y None: the norm after the block was left out. accumulate adds dw_post,
-    dw_pre and a channel gate's gradient to `out`'s. `out`: the five outputs to write (None to
-    skip; out.dr may be dr_out)."""
-    f32, bf16 = torch.float32, torch.bfloat16
+    bf16, None if w_pre was). y and r_out: the saved tensors, or both as their checkpoints,
+    (codes, scales) pairs; rstd_y None: the norm after the block was left out. accumulate adds
+    dw_post, dw_pre and a channel gate's gradient to `out`'s. `out`: the five outputs to write
+    (None to skip; out.dr may be dr_out)."""
     post, pre = rstd_y is not None, dn is not None
     lead = dr_out if dr_out is not None else dn
     if lead is None:
         raise PuroError("dr_out and dn: at least one is required")
     dev = _dev(lead)
-    rows, cols = shape = tuple(lead.shape)
+    rows, cols = _matrix(lead, "dr_out")
     res = (dr_out.dtype if dr_out is not None else
            r_out.dtype if isinstance(r_out, torch.Tensor) else
-           out[0].dtype if out is not None and out[0] is not None else bf16)
+           out[0].dtype if out is not None and out[0] is not None else torch.bfloat16)
     if res not in _TYPES:
         raise PuroError("dr_out: expected bf16 or fp32")
-    if dr_out is not None:
-        _need(dr_out, "dr_out", res, shape, dev)
-    if post:
-        _need(rstd_y, "rstd_y", f32, (rows,), dev)
-        _need(w_post, "w_post", f32, (cols,), dev)
-    if pre:
-        _need(dn, "dn", bf16, shape, dev)
-        _need(rstd_r, "rstd_r", f32, (rows,), dev)
-        _need(w_pre, "w_pre", f32, (cols,), dev)
-    ys = _saved(y if post else None, "y", bf16, shape, dev, post)
-    rs = _saved(r_out if pre else None, "r_out", res, shape, dev, pre)
-    kind, gp = _gate(gate, rows, cols, dev)
+    kind = _gate_kind(gate)
+    saved = *_saved(y, "y", post), *_saved(r_out, "r_out", pre)
     if out is None:
         if accumulate:
             raise PuroError("accumulate=True needs existing gradients in out")
-        vec = lambda: torch.empty((cols,), dtype=f32, device=dev)  # noqa: E731
-        out = BlockNormGrads(torch.empty(shape, dtype=res, device=dev),
-                             torch.empty(shape, dtype=bf16, device=dev) if post else None,
-                             vec() if post else None, vec() if pre else None,
+        vec = lambda: torch.empty((cols,), dtype=torch.float32, device=dev)  # noqa: E731
+        out = BlockNormGrads(torch.empty((rows, cols), dtype=res, device=dev),
+                             torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+                             if post else None, vec() if post else None, vec() if pre else None,
                              torch.empty_like(gate) if gate is not None else None)
-    else:
+    elif type(out) is not BlockNormGrads:
         out = BlockNormGrads(*out)
-        for t, name, dtype, want in ((out.dr, "dr", res, shape), (out.dy, "dy", bf16, shape),
-                                     (out.dw_post, "dw_post", f32, (cols,)),
-                                     (out.dw_pre, "dw_pre", f32, (cols,))):
-            if t is not None:
-                _need(t, name, dtype, want, dev)
-        if gate is not None:
-            _need(out.dgate, "dgate", gate.dtype, tuple(gate.shape), dev)
-    need = lib().puro_block_norm_workspace(rows, cols)
+    p = _NORM_BWD[res, kind].pointers(
+        dev, rows, cols, (cols + 127) // 128, dr_out, dn, *saved, rstd_y, rstd_r if pre else None,
+        w_post if post else None, w_pre if pre else None, gate, *out)
+    L = lib()
+    need = L.puro_block_norm_workspace(rows, cols)
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or workspace.numel() * workspace.element_size() < need:
         raise PuroError(f"workspace: {need} bytes on {dev} needed")
-    d = PuroBlockNormGrad(rows, cols, _TYPES[res], kind, bool(accumulate), alpha, beta,
-                          _ptr(dr_out), _ptr(dn), *ys, *rs, _ptr(rstd_y),
-                          rstd_r.data_ptr() if pre else None, w_post.data_ptr() if post else None,
-                          w_pre.data_ptr() if pre else None, gp, *map(_ptr, out))
-    check(lib().puro_block_norm_bwd(ctypes.byref(d), workspace.data_ptr(), _stream(dev)))
+    st = L.puro_block_norm_bwd(_NORM_GRAD.pack(rows, cols, _TYPES[res], kind, bool(accumulate),
+                                               alpha, beta, *p), workspace.data_ptr(),
+                               _stream(dev))
+    if st:
+        check(st)
     return out
 
 
@@ -520,10 +569,13 @@ class SwiGLUOperands(NamedTuple):
     hts: torch.Tensor
 
 
-def _half(cols, name):
-    if cols % 2:
-        raise PuroError(f"{name}: {cols} columns, expected an even number (g and u)")
-    return cols // 2
+# Sizes d0 rows, d1 f, d2 2f for the tensors; the scales' first sizes are checked apart.
+_SWIGLU_FWD = _Spec("gu:b!02 h:b?01 hq:q?01 guq:q?02")
+_SWIGLU_BWD = _Spec("dh:b!01 gu:b?02 gu:q?02 dgu:b?02")
+_SWIGLU_FP8 = _Spec("dh:b!01 gu:b?02 gu:q?02 dguq:q!02 dgutq:q!20 htq:q!10")
+_GU_SCALES = _Spec("hs:f?10 gus:f?20")
+_FP8_SCALES = _Spec("gus:f?20 dgus:f!20")
+_FP8_T_SCALES = _Spec("dguts:f!01 hts:f!02")
 
 
 def puro_swiglu_fwd(gu, h: bool = False, fp8: bool = True, ckpt: bool = True, pow2: bool = False,
@@ -532,47 +584,39 @@ def puro_swiglu_fwd(gu, h: bool = False, fp8: bool = True, ckpt: bool = True, po
     projection's operand; `ckpt`: an 8-bit checkpoint of gu. `out`: the five outputs to write
     (None to leave one out) instead of new ones."""
     dev = _dev(gu)
-    rows, cols = gu.shape
-    f = _half(cols, "gu")
-    _need(gu, "gu", torch.bfloat16, (rows, cols), dev)
+    rows, cols = _matrix(gu, "gu")
+    if cols % 2:
+        raise PuroError(f"gu: {cols} columns, expected an even number (g and u)")
+    f, k = cols // 2, (cols // 2 + 127) // 128
     if out is None:
         none = (None, None)
         out = SwiGLU(torch.empty((rows, f), dtype=torch.bfloat16, device=dev) if h else None,
                      *(_new_codes(rows, f, dev) if fp8 else none),
                      *((torch.empty((rows, cols), dtype=FP8, device=dev),
-                        torch.empty((2 * _groups(f), rows), dtype=torch.float32, device=dev))
+                        torch.empty((2 * k, rows), dtype=torch.float32, device=dev))
                        if ckpt else none))
-    else:
+    elif type(out) is not SwiGLU:
         out = SwiGLU(*out)
-        if out.h is not None:
-            _need(out.h, "h", torch.bfloat16, (rows, f), dev)
-        if out.hq is not None or out.hs is not None:
-            _need_codes(out.hq, out.hs, "h", rows, f, dev)
-        if out.guq is not None or out.gus is not None:
-            _need_codes(out.guq, out.gus, "gu", rows, cols, dev, 2 * _groups(f))
-    check(lib().puro_swiglu_fwd(gu.data_ptr(), rows, f, *map(_ptr, out), bool(pow2),
-                                _stream(dev)))
+    p, ph, hq, guq = _SWIGLU_FWD.pointers(dev, rows, f, cols, gu, out[0], out[1], out[3])
+    hs, gus = _GU_SCALES.pointers(dev, rows, k, 2 * k, out[2], out[4])
+    check(lib().puro_swiglu_fwd(p, rows, f, ph, hq, hs, guq, gus, bool(pow2), _stream(dev)))
     return out
-
-
-def _swiglu_saved(dh, gu):
-    dev = _dev(dh)
-    rows, f = dh.shape
-    _need(dh, "dh", torch.bfloat16, (rows, f), dev)
-    if isinstance(gu, (tuple, list)):
-        q, s = gu
-        _need_codes(q, s, "gu", rows, 2 * f, dev, 2 * _groups(f))
-        return dev, rows, f, (None, q.data_ptr(), s.data_ptr())
-    _need(gu, "gu", torch.bfloat16, (rows, 2 * f), dev)
-    return dev, rows, f, (gu.data_ptr(), None, None)
 
 
 def puro_swiglu_bwd(dh, gu, dgu=None):
     """dgu bf16 [rows, 2f] from dh bf16 [rows, f] and gu: bf16 [rows, 2f], or its checkpoint as a
     (codes, scales) pair."""
-    dev, rows, f, src = _swiglu_saved(dh, gu)
-    dgu = _out(dgu, "dgu", torch.bfloat16, (rows, 2 * f), dev)
-    check(lib().puro_swiglu_bwd(dh.data_ptr(), *src, rows, f, dgu.data_ptr(), _stream(dev)))
+    dev = _dev(dh)
+    rows, f = _matrix(dh, "dh")
+    if dgu is None:
+        dgu = torch.empty((rows, 2 * f), dtype=torch.bfloat16, device=dev)
+    x, q, s = _saved(gu, "gu", True)
+    p = _SWIGLU_BWD.pointers(dev, rows, f, 2 * f, dh, x, q, dgu)
+    ps = 0
+    if s is not None:
+        _need(s, "gu", torch.float32, (2 * ((f + 127) // 128), rows), dev)
+        ps = s.data_ptr()
+    check(lib().puro_swiglu_bwd(p[0], p[1], p[2], ps, rows, f, p[3], _stream(dev)))
     return dgu
 
 
@@ -580,17 +624,21 @@ def puro_swiglu_bwd_fp8(dh, gu, pow2: bool = False, out=None) -> SwiGLUOperands:
     """puro_swiglu_bwd straight to the FP8 operands of gate_up's data and weight gradients, and
     h's transposed copy for down's weight gradient. rows and f: multiples of 128. `out`: the six
     outputs to write instead of new ones."""
-    dev, rows, f, src = _swiglu_saved(dh, gu)
+    dev = _dev(dh)
+    rows, f = _matrix(dh, "dh")
+    if rows % 128 or f % 128:
+        raise PuroError(f"dh: shape {(rows, f)}, expected multiples of 128")
     if out is None:
         out = SwiGLUOperands(*_new_codes(rows, 2 * f, dev), *_new_codes(2 * f, rows, dev),
                              *_new_codes(f, rows, dev))
-    else:
+    elif type(out) is not SwiGLUOperands:
         out = SwiGLUOperands(*out)
-        _need_codes(out.dguq, out.dgus, "dgu", rows, 2 * f, dev)
-        _need_codes(out.dgutq, out.dguts, "dgut", 2 * f, rows, dev)
-        _need_codes(out.htq, out.hts, "ht", f, rows, dev)
-    check(lib().puro_swiglu_bwd_fp8(dh.data_ptr(), *src, rows, f, bool(pow2), *map(_ptr, out),
-                                    _stream(dev)))
+    x, q, s = _saved(gu, "gu", True)
+    p = _SWIGLU_FP8.pointers(dev, rows, f, 2 * f, dh, x, q, out[0], out[2], out[4])
+    gus, dgus = _FP8_SCALES.pointers(dev, rows, f, f // 64, s, out[1])
+    dguts, hts = _FP8_T_SCALES.pointers(dev, rows // 128, 2 * f, f, out[3], out[5])
+    check(lib().puro_swiglu_bwd_fp8(p[0], p[1], p[2], gus, rows, f, bool(pow2), p[3], dgus, p[4],
+                                    dguts, p[5], hts, _stream(dev)))
     return out
 
 

@@ -19,6 +19,8 @@ SOURCES = ["abi.hip", "quant.hip", "gemm.hip", "optim.hip", "debug.hip", "norm.h
 # GEMM path.
 PROBE_PATH = os.path.join(PKG_DIR, "libpuro_probe.so")
 PROBE_SOURCES = ["ceiling.hip"]
+# The Python binding's native argument checks: host code against torch's headers.
+ARGS_PATH = os.path.join(PKG_DIR, "_args.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -53,7 +55,27 @@ def _hipcc(sources, out: str, verbose: bool) -> str:
     return out
 
 
+def _args(verbose: bool) -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
+    tmp = ARGS_PATH + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           *("-I" + p for p in cpp_extension.include_paths("cpu")),
+           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "args.cpp"), "-L" + lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, ARGS_PATH)
+    return ARGS_PATH
+
+
 def build(verbose: bool = True) -> str:
+    _args(verbose)
     _hipcc(PROBE_SOURCES, PROBE_PATH, verbose)
     return _hipcc(SOURCES, LIB_PATH, verbose)
 

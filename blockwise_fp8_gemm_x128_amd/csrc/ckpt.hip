@@ -76,10 +76,10 @@ __global__ __launch_bounds__(kTileThreads) void ckpt_transpose_kernel(
     const uint8_t* __restrict__ q, const float* __restrict__ s, int64_t rows, int64_t cols,
     int pow2, uint8_t* __restrict__ qt, float* __restrict__ st) {
   __shared__ ColTile<1> sh;
-  const uint32_t chunks = static_cast<uint32_t>((cols + 127) >> 7);
+  const uint32_t bands = static_cast<uint32_t>((rows + 127) >> 7);
   const uint32_t b = off_lines(cols) || off_lines(rows) ? xcd_range(blockIdx.x, gridDim.x)
                                                         : blockIdx.x;
-  const int64_t cb = b % chunks, mb = b / chunks;
+  const int64_t cb = b / bands, mb = b % bands;
   const Span<kShort> sp(cb * 128 + (threadIdx.x & 15) * kVec, cols, off_lines(cols));
   const int64_t r0 = mb * 128 + (threadIdx.x >> 4) * kTileRows;
   Fp8x8 raw[kTileRows];

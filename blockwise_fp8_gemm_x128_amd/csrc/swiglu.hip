@@ -148,10 +148,9 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(const BwdArgs a) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const float sg = sigmoid(g[i]);
-      const float w = dh[i] * sg;
-      const float gi = g[i];
-      g[i] = w * u[i] * fmaf(gi, 1.0f - sg, 1.0f);
-      u[i] = w * gi;
+      const float silu = g[i] * sg;
+      g[i] = dh[i] * u[i] * fmaf(silu, 1.0f - sg, sg);
+      u[i] = dh[i] * silu;
     }
     uint16_t* o = a.dgu + row * 2 * a.f + col;
     store8(o, sp.n, g);
@@ -173,82 +172,142 @@ struct BwdFp8Args {
   int pow2;
 };
 
+// A thread's part of a 128 x 128 tile: rows r4 .. r4 + 3 and eight columns. Addresses are one
+// 32-bit offset per lane (at most 127 (2 f) + 128 < 2^32 for f <= 2^24) on top of a uniform pointer
+// per row.
+struct TilePart {
+  int64_t chunks, c, mb;
+  uint32_t r4, at1, at2;   // element offsets in tensors of f and of 2f columns
+  int64_t base1, base2;
+  __device__ __forceinline__ TilePart(int64_t rows, int64_t f) {
+    const uint32_t bands = static_cast<uint32_t>(rows >> 7);
+    chunks = f >> 7;
+    c = blockIdx.x / bands, mb = blockIdx.x % bands;
+    r4 = (threadIdx.x >> 4) * kTileRows;
+    at1 = r4 * static_cast<uint32_t>(f) + (threadIdx.x & 15) * kVec;
+    at2 = r4 * 2 * static_cast<uint32_t>(f) + (threadIdx.x & 15) * kVec;
+    base1 = mb * 128 * f + c * 128;
+    base2 = mb * 256 * f + c * 128;
+  }
+};
+
+template <bool kCodes>
+struct TileRaw {
+  GuRaw<kCodes> gu[kTileRows];
+  Bf16x8 dh[kTileRows];
+};
+template <bool kCodes>
+__device__ __forceinline__ void load_tile(TileRaw<kCodes>& w, const BwdFp8Args& a,
+                                          const TilePart& t, const Span<false>& sp) {
+  constexpr bool kShort = false;
+#pragma unroll
+  for (int p = 0; p < kTileRows; ++p) {
+    const int64_t g = t.base2 + p * 2 * a.f;
+    if constexpr (kCodes) {
+      load<true, kShort>(w.gu[p].g, a.src.q + g + t.at2, sp);
+      load<true, kShort>(w.gu[p].u, a.src.q + g + a.f + t.at2, sp);
+    } else {
+      load<true, kShort>(w.gu[p].g, a.src.gu + g + t.at2, sp);
+      load<true, kShort>(w.gu[p].u, a.src.gu + g + a.f + t.at2, sp);
+    }
+    load<true, kShort>(w.dh[p], a.dh + t.base1 + p * a.f + t.at1, sp);
+  }
+  if constexpr (kCodes) {
+    const float* s = a.src.s + t.c * a.rows + t.mb * 128;
+    const float4 sg = *reinterpret_cast<const float4*>(s + t.r4);
+    const float4 su = *reinterpret_cast<const float4*>(s + t.chunks * a.rows + t.r4);
+    w.gu[0].sg = sg.x, w.gu[1].sg = sg.y, w.gu[2].sg = sg.z, w.gu[3].sg = sg.w;
+    w.gu[0].su = su.x, w.gu[1].su = su.y, w.gu[2].su = su.z, w.gu[3].su = su.w;
+  }
+}
+
+// Codes of dg (t = 0) or du (t = 1) in the row orientation.
+__device__ __forceinline__ void store_rows(const float (&v)[kTileRows][kVec], const BwdFp8Args& a,
+                                           const TilePart& t, int which) {
+  const RowGroups<kTileRows> rg = row_groups<false, kTileRows>(v, a.pow2 != 0);
+#pragma unroll
+  for (int p = 0; p < kTileRows; ++p)
+    store8(a.dguq + t.base2 + p * 2 * a.f + which * a.f + t.at2, kVec, encode8(v[p], rg.r[p]));
+  const uint32_t l16 = threadIdx.x & 15;
+  if (l16 < kTileRows)
+    a.dgus[(which * t.chunks + t.c) * a.rows + t.mb * 128 + t.r4 + l16] = rg.s;
+}
+
 // Four waves per SIMD, two blocks per CU, so that one block's loads and stores run under the
 // other's arithmetic: that caps the registers at 128, of which the three tensors' values take 96.
-// Addresses are therefore one 32-bit offset per lane on top of a uniform pointer per row.
 template <bool kCodes>
 __global__ __launch_bounds__(kTileThreads, 4) void swiglu_bwd_fp8_kernel(const BwdFp8Args a) {
   __shared__ ColTile<3> sh;
-  const int64_t chunks = a.f >> 7;
-  const uint32_t across = static_cast<uint32_t>(chunks);
-  const int64_t c = blockIdx.x % across, mb = blockIdx.x / across;
-  const int l16 = threadIdx.x & 15;
-  const uint32_t f = static_cast<uint32_t>(a.f);
-  const uint32_t r4 = (threadIdx.x >> 4) * kTileRows;  // first of the thread's rows in the tile
-  // at most 127 (2 f) + 128 < 2^32 for f <= 2^24
-  const uint32_t at1 = r4 * f + l16 * kVec, at2 = r4 * 2 * f + l16 * kVec;
-  const int64_t base1 = mb * 128 * a.f + c * 128, base2 = mb * 256 * a.f + c * 128;
+  const TilePart t(a.rows, a.f);
+  Span<false> sp;  // whole groups: never cut short
+  sp.at = 0, sp.n = kVec, sp.cut = false;
   float v[3][kTileRows][kVec];  // dg, du, h
   {
-    GuRaw<kCodes> raw[kTileRows];
-    Bf16x8 dhr[kTileRows];
-    constexpr bool kShort = false;
-    Span<kShort> sp;  // whole groups: never cut short
-    sp.at = 0, sp.n = kVec, sp.cut = false;
-#pragma unroll
-    for (int p = 0; p < kTileRows; ++p) {
-      if constexpr (kCodes) {
-        load<true, kShort>(raw[p].g, a.src.q + base2 + p * 2 * a.f + at2, sp);
-        load<true, kShort>(raw[p].u, a.src.q + base2 + p * 2 * a.f + a.f + at2, sp);
-      } else {
-        load<true, kShort>(raw[p].g, a.src.gu + base2 + p * 2 * a.f + at2, sp);
-        load<true, kShort>(raw[p].u, a.src.gu + base2 + p * 2 * a.f + a.f + at2, sp);
-      }
-      load<true, kShort>(dhr[p], a.dh + base1 + p * a.f + at1, sp);
-    }
-    if constexpr (kCodes) {
-      const float4 sg = *reinterpret_cast<const float4*>(a.src.s + c * a.rows + mb * 128 + r4);
-      const float4 su =
-          *reinterpret_cast<const float4*>(a.src.s + (chunks + c) * a.rows + mb * 128 + r4);
-      raw[0].sg = sg.x, raw[1].sg = sg.y, raw[2].sg = sg.z, raw[3].sg = sg.w;
-      raw[0].su = su.x, raw[1].su = su.y, raw[2].su = su.z, raw[3].su = su.w;
-    }
+    TileRaw<kCodes> raw;
+    load_tile(raw, a, t, sp);
 #pragma unroll
     for (int p = 0; p < kTileRows; ++p) {
       float g[kVec], u[kVec], dh[kVec];
-      gu_values<kCodes, kShort>(raw[p], sp, g, u);
-      values(dhr[p], sp, dh);
+      gu_values<kCodes, false>(raw.gu[p], sp, g, u);
+      values(raw.dh[p], sp, dh);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
         const float sg = sigmoid(g[i]);
-        const float t = dh[i] * sg;
-        v[0][p][i] = t * u[i] * fmaf(g[i], 1.0f - sg, 1.0f);
-        v[1][p][i] = t * g[i];
-        v[2][p][i] = g[i] * sg * u[i];
+        const float silu = g[i] * sg;
+        v[0][p][i] = dh[i] * u[i] * fmaf(silu, 1.0f - sg, sg);
+        v[1][p][i] = dh[i] * silu;
+        v[2][p][i] = silu * u[i];
       }
       // The compiler would rather keep the inputs and work the values out where they are used,
       // which takes more registers than there are: the empty statements pin the values here.
 #pragma unroll
-      for (int t = 0; t < 3; ++t)
+      for (int k = 0; k < 3; ++k)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) asm volatile("" : "+v"(v[t][p][i]));
+        for (int i = 0; i < kVec; ++i) asm volatile("" : "+v"(v[k][p][i]));
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  const bool pow2 = a.pow2 != 0;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const RowGroups<kTileRows> rg = row_groups<false, kTileRows>(v[t], pow2);
-#pragma unroll
-    for (int p = 0; p < kTileRows; ++p)
-      store8(a.dguq + base2 + p * 2 * a.f + t * a.f + at2, kVec, encode8(v[t][p], rg.r[p]));
-    if (l16 < kTileRows) a.dgus[(t * chunks + c) * a.rows + mb * 128 + r4 + l16] = rg.s;
+  for (int k = 0; k < 2; ++k) {
+    store_rows(v[k], a, t, k);
     __builtin_amdgcn_sched_barrier(0);
   }
-  const ColOut out[3] = {{a.dgutq, a.dguts, 2 * a.f, c * 128},
-                         {a.dgutq, a.dguts, 2 * a.f, a.f + c * 128},
-                         {a.htq, a.hts, a.f, c * 128}};
-  col_codes<3>(sh, v, out, a.rows, mb, pow2);
+  const ColOut out[3] = {{a.dgutq, a.dguts, 2 * a.f, t.c * 128},
+                         {a.dgutq, a.dguts, 2 * a.f, a.f + t.c * 128},
+                         {a.htq, a.hts, a.f, t.c * 128}};
+  col_codes<3>(sh, v, out, a.rows, t.mb, a.pow2 != 0);
+}
+
+// The same with one block per tile and tensor (grid y: dg, du, h), which reads the inputs again and
+// works the sigmoid out again but has three times the blocks and a third of the work in each.
+template <bool kCodes>
+__global__ __launch_bounds__(kTileThreads) void swiglu_bwd_fp8_split_kernel(const BwdFp8Args a) {
+  __shared__ ColTile<1> sh;
+  const TilePart t(a.rows, a.f);
+  const int which = blockIdx.y;
+  Span<false> sp;
+  sp.at = 0, sp.n = kVec, sp.cut = false;
+  float v[1][kTileRows][kVec];
+  TileRaw<kCodes> raw;
+  load_tile(raw, a, t, sp);
+#pragma unroll
+  for (int p = 0; p < kTileRows; ++p) {
+    float g[kVec], u[kVec], dh[kVec];
+    gu_values<kCodes, false>(raw.gu[p], sp, g, u);
+    values(raw.dh[p], sp, dh);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const float sg = sigmoid(g[i]);
+      const float silu = g[i] * sg;
+      v[0][p][i] = which == 0   ? dh[i] * u[i] * fmaf(silu, 1.0f - sg, sg)
+                   : which == 1 ? dh[i] * silu
+                                : silu * u[i];
+    }
+  }
+  if (which < 2) store_rows(v[0], a, t, which);
+  const ColOut out[1] = {{which < 2 ? a.dgutq : a.htq, which < 2 ? a.dguts : a.hts,
+                          which < 2 ? 2 * a.f : a.f, (which == 1 ? a.f : 0) + t.c * 128}};
+  col_codes<1>(sh, v, out, a.rows, t.mb, a.pow2 != 0);
 }
 
 puro_status check_gu(const void* gu, const void* guq, const float* gus, bool empty) {
@@ -332,12 +391,14 @@ extern "C" puro_status puro_swiglu_bwd_fp8(const void* dh, const void* gu, const
                         {static_cast<const uint16_t*>(gu), static_cast<const uint8_t*>(guq), gus},
                         rows, f, static_cast<uint8_t*>(dguq), dgus, static_cast<uint8_t*>(dgutq),
                         dguts, static_cast<uint8_t*>(htq), hts, pow2};
-  const dim3 grid(static_cast<uint32_t>(blocks));
-  if (gu != nullptr)
-    hipLaunchKernelGGL(swiglu_bwd_fp8_kernel<false>, grid, dim3(kTileThreads), 0,
-                       static_cast<hipStream_t>(stream), a);
-  else
-    hipLaunchKernelGGL(swiglu_bwd_fp8_kernel<true>, grid, dim3(kTileThreads), 0,
-                       static_cast<hipStream_t>(stream), a);
+  // Tiles that leave two thirds of the CUs idle are split by tensor: 128 x 6144 (48 tiles) in 7.2 us
+  // against 8.2, 1024 x 1024 (64) in 7.4 against 8.4; but 1024 x 2048 (128) in 10.3 against 9.4.
+  const bool split = 3 * blocks <= 256;
+  const auto k = gu != nullptr ? (split ? swiglu_bwd_fp8_split_kernel<false>
+                                        : swiglu_bwd_fp8_kernel<false>)
+                               : (split ? swiglu_bwd_fp8_split_kernel<true>
+                                        : swiglu_bwd_fp8_kernel<true>);
+  hipLaunchKernelGGL(k, dim3(static_cast<uint32_t>(blocks), split ? 3 : 1), dim3(kTileThreads), 0,
+                     static_cast<hipStream_t>(stream), a);
   return launch_status();
 }
