@@ -49,7 +49,7 @@ def _need(t: torch.Tensor, name: str, dtype, shape, dev) -> None:
 
 
 def _dev(t: torch.Tensor) -> torch.device:
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise PuroError("inputs must be torch tensors on a HIP device")
     return t.device
 
@@ -283,7 +283,7 @@ class _Spec:
         self.code = "".join(c for _, c in pairs).encode()
 
     def pointers(self, dev, d0, d1, d2, *tensors):
-        p = _args().ptrs(self.code, dev.index, d0, d1, d2, *tensors)
+        p = (_native or _load_native())(self.code, dev.index, d0, d1, d2, *tensors)
         if type(p) is not int:
             return p
         kind, need, *dims = self.code[4 * p:4 * p + 4].decode()
@@ -295,19 +295,33 @@ class _Spec:
         raise PuroError(f"{name}: not as expected")
 
 
-_args_module = None
+_native = None  # ptrs() of the native checks
 
 
-def _args():
-    global _args_module
-    if _args_module is None:
-        try:
-            from . import _args as module
-        except ImportError as e:
-            raise PuroError("the binding's native checks are not built (%s); run `python -m "
-                            "blockwise_fp8_gemm_x128_amd.build`" % e) from e
-        _args_module = module
-    return _args_module
+def _load_native():
+    global _native
+    try:
+        from ._args import ptrs
+    except ImportError as e:
+        raise PuroError("the binding's native checks are not built (%s); run `python -m "
+                        "blockwise_fp8_gemm_x128_amd.build`" % e) from e
+    _native = ptrs
+    return ptrs
+
+
+def _call(name, *args) -> None:
+    """A C entry point of these operators, its status checked."""
+    st = (_entry.get(name) or _load_entry(name))(*args)
+    if st:
+        check(st)
+
+
+_entry = {}  # the C entry points by name
+
+
+def _load_entry(name):
+    fn = _entry[name] = getattr(lib(), name)
+    return fn
 
 
 def _groups(n: int) -> int:
@@ -354,7 +368,7 @@ def puro_ckpt_pack(x: torch.Tensor, q=None, s=None, pow2: bool = False):
         new = _new_codes(rows, cols, dev)
         q, s = new[0] if q is None else q, new[1] if s is None else s
     p = _PACK.pointers(dev, rows, cols, _groups(cols), q, s)
-    check(lib().puro_ckpt_pack(x.data_ptr(), kind, rows, cols, ld, bool(pow2), *p, _stream(dev)))
+    _call("puro_ckpt_pack", x.data_ptr(), kind, rows, cols, ld, bool(pow2), *p, _stream(dev))
     return q, s
 
 
@@ -369,7 +383,7 @@ def puro_ckpt_unpack(q, s, x=None, dtype=torch.bfloat16):
     if x.shape != (rows, cols):
         raise PuroError(f"x: shape {tuple(x.shape)}, expected {(rows, cols)}")
     p = _PACK.pointers(dev, rows, cols, _groups(cols), q, s)
-    check(lib().puro_ckpt_unpack(*p, rows, cols, x.data_ptr(), kind, ld, _stream(dev)))
+    _call("puro_ckpt_unpack", *p, rows, cols, x.data_ptr(), kind, ld, _stream(dev))
     return x
 
 
@@ -383,8 +397,8 @@ def puro_ckpt_transpose(q, s, qt=None, st=None, pow2: bool = False):
         qt, st = new[0] if qt is None else qt, new[1] if st is None else st
     p = _TRANSPOSE.pointers(dev, rows, cols, _groups(cols), q, s, qt)
     _need(st, "st", torch.float32, (_groups(rows), cols), dev)
-    check(lib().puro_ckpt_transpose(p[0], p[1], rows, cols, bool(pow2), p[2], st.data_ptr(),
-                                    _stream(dev)))
+    _call("puro_ckpt_transpose", p[0], p[1], rows, cols, bool(pow2), p[2], st.data_ptr(),
+          _stream(dev))
     return qt, st
 
 
@@ -476,10 +490,8 @@ def puro_block_norm_fwd(y, r, w_post, w_pre, gate=None, alpha: float = 1.0, beta
         out = BlockNorm(*out)
     p = _NORM_FWD[dtype, kind].pointers(dev, rows, cols, (cols + 127) // 128, y, r,
                                         None if y is None else w_post, w_pre, gate, *out)
-    st = lib().puro_block_norm_fwd(_NORM.pack(rows, cols, _TYPES[dtype], kind, bool(pow2), alpha,
-                                              beta, eps, *p), _stream(dev))
-    if st:
-        check(st)
+    _call("puro_block_norm_fwd", _NORM.pack(rows, cols, _TYPES[dtype], kind, bool(pow2), alpha,
+                                            beta, eps, *p), _stream(dev))
     return out
 
 
@@ -536,17 +548,14 @@ def puro_block_norm_bwd(dr_out, dn, y, r_out, rstd_y, rstd_r, w_post, w_pre, gat
     p = _NORM_BWD[res, kind].pointers(
         dev, rows, cols, (cols + 127) // 128, dr_out, dn, *saved, rstd_y, rstd_r if pre else None,
         w_post if post else None, w_pre if pre else None, gate, *out)
-    L = lib()
-    need = L.puro_block_norm_workspace(rows, cols)
+    need = lib().puro_block_norm_workspace(rows, cols)
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or workspace.numel() * workspace.element_size() < need:
         raise PuroError(f"workspace: {need} bytes on {dev} needed")
-    st = L.puro_block_norm_bwd(_NORM_GRAD.pack(rows, cols, _TYPES[res], kind, bool(accumulate),
-                                               alpha, beta, *p), workspace.data_ptr(),
-                               _stream(dev))
-    if st:
-        check(st)
+    _call("puro_block_norm_bwd", _NORM_GRAD.pack(rows, cols, _TYPES[res], kind, bool(accumulate),
+                                                 alpha, beta, *p), workspace.data_ptr(),
+          _stream(dev))
     return out
 
 
@@ -599,7 +608,7 @@ def puro_swiglu_fwd(gu, h: bool = False, fp8: bool = True, ckpt: bool = True, po
         out = SwiGLU(*out)
     p, ph, hq, guq = _SWIGLU_FWD.pointers(dev, rows, f, cols, gu, out[0], out[1], out[3])
     hs, gus = _GU_SCALES.pointers(dev, rows, k, 2 * k, out[2], out[4])
-    check(lib().puro_swiglu_fwd(p, rows, f, ph, hq, hs, guq, gus, bool(pow2), _stream(dev)))
+    _call("puro_swiglu_fwd", p, rows, f, ph, hq, hs, guq, gus, bool(pow2), _stream(dev))
     return out
 
 
@@ -616,7 +625,7 @@ def puro_swiglu_bwd(dh, gu, dgu=None):
     if s is not None:
         _need(s, "gu", torch.float32, (2 * ((f + 127) // 128), rows), dev)
         ps = s.data_ptr()
-    check(lib().puro_swiglu_bwd(p[0], p[1], p[2], ps, rows, f, p[3], _stream(dev)))
+    _call("puro_swiglu_bwd", p[0], p[1], p[2], ps, rows, f, p[3], _stream(dev))
     return dgu
 
 
@@ -637,8 +646,8 @@ def puro_swiglu_bwd_fp8(dh, gu, pow2: bool = False, out=None) -> SwiGLUOperands:
     p = _SWIGLU_FP8.pointers(dev, rows, f, 2 * f, dh, x, q, out[0], out[2], out[4])
     gus, dgus = _FP8_SCALES.pointers(dev, rows, f, f // 64, s, out[1])
     dguts, hts = _FP8_T_SCALES.pointers(dev, rows // 128, 2 * f, f, out[3], out[5])
-    check(lib().puro_swiglu_bwd_fp8(p[0], p[1], p[2], gus, rows, f, bool(pow2), p[3], dgus, p[4],
-                                    dguts, p[5], hts, _stream(dev)))
+    _call("puro_swiglu_bwd_fp8", p[0], p[1], p[2], gus, rows, f, bool(pow2), p[3], dgus, p[4],
+          dguts, p[5], hts, _stream(dev))
     return out
 
 

@@ -96,7 +96,7 @@ __global__ __launch_bounds__(kTileThreads) void ckpt_transpose_kernel(
 #pragma unroll
   for (int p = 0; p < kTileRows; ++p) values(raw[p], sp, sc[p], v[0][p]);
   const ColOut out[1] = {{qt, st, cols, cb * 128}};
-  col_codes<1>(sh, v, out, rows, mb, pow2 != 0);
+  col_codes<false>(sh, v, out, rows, mb, pow2 != 0);
 }
 
 puro_status check_rows(int64_t rows, int64_t cols, int64_t* blocks) {

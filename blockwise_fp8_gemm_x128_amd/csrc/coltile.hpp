@@ -8,6 +8,10 @@
 // divisions. Only codes are transposed through LDS, one byte
 // per element: four rows of a column are one dword, and a column's 128 bytes leave as one line.
 //
+// Maxima and reciprocal scales of column 8 l + i stand at 64 (i / 4) + 4 l + i mod 4, so that a lane's
+// eight are two 16 B accesses, each contiguous over the lanes (as 8 l + i they were half of the
+// kernels' bank conflicts).
+//
 // Dword of column 8 l + i, rows 4 g .. 4 g + 3: codes[(16 i + l) * kPitch + g]. With a pitch of 36
 // dwords the 16 lanes of a row start 16 different multiples of 4 banks and the wave's four row
 // groups fill the banks between, so the writes are free of conflicts and the reads are 16 B.
@@ -28,11 +32,11 @@ constexpr int kTileRows = 4;   // rows per thread
 template <int kN>
 struct ColTile {
   static constexpr int kPitch = 36;
-  union {  // the maxima are read for the last time a barrier before the first code is written
+  union __attribute__((aligned(16))) {  // the maxima are read for the last time a barrier before the first code is written
     uint32_t codes[kN][128 * kPitch];
     float maxima[kN][32][128];
   };
-  float r[kN][128];
+  alignas(16) float r[kN][128];
   int odd;
 };
 
@@ -63,9 +67,9 @@ __device__ __forceinline__ void col_maxima(ColTile<kN>& sh, const float (&v)[kN]
         for (int p = 1; p < kTileRows; ++p) m[i] = fmaxf(m[i], __builtin_fabsf(v[t][p][i]));
       }
     }
-    float4* dst = reinterpret_cast<float4*>(&sh.maxima[t][seg][8 * l16]);
+    float4* dst = reinterpret_cast<float4*>(&sh.maxima[t][seg][4 * l16]);
     dst[0] = make_float4(m[0], m[1], m[2], m[3]);
-    dst[1] = make_float4(m[4], m[5], m[6], m[7]);
+    dst[16] = make_float4(m[4], m[5], m[6], m[7]);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
@@ -75,15 +79,16 @@ __device__ __forceinline__ void col_scales(ColTile<kN>& sh, const ColOut (&out)[
                                            bool pow2) {
   const int t = threadIdx.x;
   if (t < kN * 128) {
-    const int k = __builtin_amdgcn_readfirstlane(t >> 7), c = t & 127;  // one tensor per wave
-    float x = sh.maxima[k][0][c];
+    const int k = __builtin_amdgcn_readfirstlane(t >> 7), pos = t & 127;  // one tensor per wave
+    const int c = 2 * (pos & 60) + (pos >> 6) * 4 + (pos & 3);
+    float x = sh.maxima[k][0][pos];
 #pragma unroll
-    for (int w = 1; w < 32; ++w) x = fmaxf(x, sh.maxima[k][w][c]);
+    for (int w = 1; w < 32; ++w) x = fmaxf(x, sh.maxima[k][w][pos]);
     const uint32_t m = mag(x);
     if (kMark && m >= kInfBits) sh.odd = 1;  // every writer writes the same value
     float s, r;
     ckpt_scale(m, pow2, s, r);
-    sh.r[k][c] = r;
+    sh.r[k][pos] = r;
 #pragma unroll
     for (int j = 0; j < kN; ++j)
       if (k == j && out[j].c0 + c < out[j].cols)
@@ -94,7 +99,7 @@ __device__ __forceinline__ void col_scales(ColTile<kN>& sh, const ColOut (&out)[
 // All 512 threads call it once; v[t][p][i] is element (row m0 + 4 (thread/16) + p, column
 // c0 + 8 (thread mod 16) + i) of tensor t; columns past the end are zero, rows past the end repeat
 // the last one (which changes no maximum; their codes are not stored).
-template <int kN>
+template <bool kLater, int kN>
 __device__ __forceinline__ void col_codes(ColTile<kN>& sh, const float (&v)[kN][kTileRows][kVec],
                                           const ColOut (&out)[kN], int64_t rows, int64_t mb,
                                           bool pow2) {
@@ -115,9 +120,12 @@ __device__ __forceinline__ void col_codes(ColTile<kN>& sh, const float (&v)[kN][
   }
 #pragma unroll
   for (int k = 0; k < kN; ++k) {
+    const float4 r0 = *reinterpret_cast<const float4*>(&sh.r[k][4 * l16]);
+    const float4 r1 = *reinterpret_cast<const float4*>(&sh.r[k][64 + 4 * l16]);
+    const float rs[kVec] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const float r = sh.r[k][8 * l16 + i];
+      const float r = rs[i];
       const float a = v[k][0][i], b = v[k][1][i], c = v[k][2][i], d = v[k][3][i];
       sh.codes[k][(16 * i + l16) * ColTile<kN>::kPitch + seg] =
           codes4(a * r, b * r, c * r, d * r);
@@ -138,7 +146,7 @@ __device__ __forceinline__ void col_codes(ColTile<kN>& sh, const float (&v)[kN][
       if (col >= out[k].cols) continue;
       uint8_t* p = out[k].qt + col * rows + row;
       if (left >= 16) {
-        *reinterpret_cast<u32x4_by*>(p) = u32x4_by{w.x, w.y, w.z, w.w};
+        put<kLater>(reinterpret_cast<u32x4_by*>(p), u32x4_by{w.x, w.y, w.z, w.w});
       } else {
         const uint32_t b[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll

@@ -222,12 +222,14 @@ __device__ __forceinline__ void load_tile(TileRaw<kCodes>& w, const BwdFp8Args& 
 }
 
 // Codes of dg (t = 0) or du (t = 1) in the row orientation.
+template <bool kLater>
 __device__ __forceinline__ void store_rows(const float (&v)[kTileRows][kVec], const BwdFp8Args& a,
                                            const TilePart& t, int which) {
   const RowGroups<kTileRows> rg = row_groups<false, kTileRows>(v, a.pow2 != 0);
 #pragma unroll
   for (int p = 0; p < kTileRows; ++p)
-    store8(a.dguq + t.base2 + p * 2 * a.f + which * a.f + t.at2, kVec, encode8(v[p], rg.r[p]));
+    store8<kLater>(a.dguq + t.base2 + p * 2 * a.f + which * a.f + t.at2, kVec,
+                   encode8(v[p], rg.r[p]));
   const uint32_t l16 = threadIdx.x & 15;
   if (l16 < kTileRows)
     a.dgus[(which * t.chunks + t.c) * a.rows + t.mb * 128 + t.r4 + l16] = rg.s;
@@ -235,7 +237,8 @@ __device__ __forceinline__ void store_rows(const float (&v)[kTileRows][kVec], co
 
 // Four waves per SIMD, two blocks per CU, so that one block's loads and stores run under the
 // other's arithmetic: that caps the registers at 128, of which the three tensors' values take 96.
-template <bool kCodes>
+// kLater: the codes go past the caches, for outputs larger than these (see the launch).
+template <bool kCodes, bool kLater>
 __global__ __launch_bounds__(kTileThreads, 4) void swiglu_bwd_fp8_kernel(const BwdFp8Args a) {
   __shared__ ColTile<3> sh;
   const TilePart t(a.rows, a.f);
@@ -269,13 +272,13 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_bwd_fp8_kernel(const B
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    store_rows(v[k], a, t, k);
+    store_rows<kLater>(v[k], a, t, k);
     __builtin_amdgcn_sched_barrier(0);
   }
   const ColOut out[3] = {{a.dgutq, a.dguts, 2 * a.f, t.c * 128},
                          {a.dgutq, a.dguts, 2 * a.f, a.f + t.c * 128},
                          {a.htq, a.hts, a.f, t.c * 128}};
-  col_codes<3>(sh, v, out, a.rows, t.mb, a.pow2 != 0);
+  col_codes<kLater>(sh, v, out, a.rows, t.mb, a.pow2 != 0);
 }
 
 // The same with one block per tile and tensor (grid y: dg, du, h), which reads the inputs again and
@@ -304,10 +307,10 @@ __global__ __launch_bounds__(kTileThreads) void swiglu_bwd_fp8_split_kernel(cons
                                 : silu * u[i];
     }
   }
-  if (which < 2) store_rows(v[0], a, t, which);
+  if (which < 2) store_rows<false>(v[0], a, t, which);
   const ColOut out[1] = {{which < 2 ? a.dgutq : a.htq, which < 2 ? a.dguts : a.hts,
                           which < 2 ? 2 * a.f : a.f, (which == 1 ? a.f : 0) + t.c * 128}};
-  col_codes<1>(sh, v, out, a.rows, t.mb, a.pow2 != 0);
+  col_codes<false>(sh, v, out, a.rows, t.mb, a.pow2 != 0);
 }
 
 puro_status check_gu(const void* gu, const void* guq, const float* gus, bool empty) {
@@ -394,10 +397,16 @@ extern "C" puro_status puro_swiglu_bwd_fp8(const void* dh, const void* gu, const
   // Tiles that leave two thirds of the CUs idle are split by tensor: 128 x 6144 (48 tiles) in 7.2 us
   // against 8.2, 1024 x 1024 (64) in 7.4 against 8.4; but 1024 x 2048 (128) in 10.3 against 9.4.
   const bool split = 3 * blocks <= 256;
-  const auto k = gu != nullptr ? (split ? swiglu_bwd_fp8_split_kernel<false>
-                                        : swiglu_bwd_fp8_kernel<false>)
-                               : (split ? swiglu_bwd_fp8_split_kernel<true>
-                                        : swiglu_bwd_fp8_kernel<true>);
+  // Codes of more bytes than the memory-side cache has (5 per element of h, 256 MiB) cannot all wait
+  // there for the GEMMs that read them, and go past it: 16384 x 6144 in 186 us against 198. Smaller
+  // ones stay: 4096 x 2048 in 17.7 us against 18.3, and their readers find them.
+  const bool later = 5 * rows * f > (int64_t(256) << 20);
+  const auto k = gu != nullptr ? (split   ? swiglu_bwd_fp8_split_kernel<false>
+                                  : later ? swiglu_bwd_fp8_kernel<false, true>
+                                          : swiglu_bwd_fp8_kernel<false, false>)
+                               : (split   ? swiglu_bwd_fp8_split_kernel<true>
+                                  : later ? swiglu_bwd_fp8_kernel<true, true>
+                                          : swiglu_bwd_fp8_kernel<true, false>);
   hipLaunchKernelGGL(k, dim3(static_cast<uint32_t>(blocks), split ? 3 : 1), dim3(kTileThreads), 0,
                      static_cast<hipStream_t>(stream), a);
   return launch_status();
