@@ -136,12 +136,14 @@ __device__ __forceinline__ void shift_in(Bf16x8& r, int shift) {
 }
 __device__ __forceinline__ void shift_in(Fp8x8& r, int shift) {
   asm volatile("" : "+v"(shift));
+  if (shift == 0) return;
   const uint64_t w = r.v[0] | uint64_t(r.v[1]) << 32;
   const uint64_t t = shift < kVec ? w >> (8 * shift) : 0;
   r.v = u32x2_el{static_cast<uint32_t>(t), static_cast<uint32_t>(t >> 32)};
 }
 __device__ __forceinline__ void shift_in(F8& r, int shift) {
   asm volatile("" : "+v"(shift));
+  if (shift == 0) return;
 #pragma unroll
   for (int s = kVec; s > 0; s >>= 1)
     if (shift & s) {
