@@ -212,6 +212,7 @@ def test_norm_fwd_refusals(L, status, kw):
     (SHAPE, dict(rows=-1)), (SHAPE, dict(cols=16385)), (ARG, dict(gate_kind=9)),
     (ARG, dict(accumulate=2)), (ARG, dict(residual_type=-1)), (ARG, dict(alpha=float("nan"))),
     (ARG, dict(yq=P, ys=P)), (ARG, dict(rq=P, rs=P)),          # both forms of an activation
+    (ARG, dict(y=None, yq=P, ys=P)), (ARG, dict(r=None, rq=P, rs=P)),   # one of each form
     (ARG, dict(w_post=None)), (ARG, dict(w_pre=None)),
     (NULL, dict(y=None)), (NULL, dict(y=None, yq=P)), (NULL, dict(y=None, ys=P)),
     (NULL, dict(r=None)), (NULL, dict(r=None, rq=P)), (NULL, dict(dn=None)), (NULL, dict(dy=None)),

@@ -308,6 +308,26 @@ def test_norm_empty(puro):
     assert puro.puro_swiglu_bwd(e, torch.empty((5, 0), dtype=BF16, device=DEV)).shape == (5, 0)
 
 
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+def test_norm_infinite_residual_stays_in_its_row(puro, value):
+    """An infinity in the residual stream: its row's statistics fail, no other row changes, and the
+    checkpoints keep their finite elements."""
+    rows, cols = 9, 1000
+    y, r = acts(rows, cols, 1), acts(rows, cols, 2, F32)
+    w = rnd((cols,), 3)
+    a = puro.puro_block_norm_fwd(y, r, w, w)
+    r2 = r.clone()
+    r2[3, 500] = value
+    b = puro.puro_block_norm_fwd(y, r2, w, w)
+    keep = [i for i in range(rows) if i != 3]
+    for k in ("r_out", "nq", "yq", "rq", "rstd_y", "rstd_r"):
+        assert same(getattr(a, k)[keep], getattr(b, k)[keep]), k
+    assert same(a.yq, b.yq) and same(a.ys, b.ys)
+    other = [i for i in range(cols) if i // 128 != 500 // 128]
+    assert same(a.rq[3, other], b.rq[3, other]) and torch.isfinite(b.rs).all()
+    assert (b.rq[3, 500].item() & 0x7F) == 0x7F
+
+
 def test_norm_nonfinite_row_stays_in_its_row(puro):
     """A NaN in one row of y makes that row's outputs NaN and changes no other row."""
     rows, cols = 40, 2048
@@ -388,22 +408,29 @@ def test_swiglu_bwd_fp8(puro, rows, f, saved, pow2):
     ref.check_codes(o.htq, o.hts, h.T, e.T, pow2, "h transposed")
 
 
-def test_swiglu_bwd_fp8_nonfinite(puro):
-    """A NaN gradient element: NaN codes at its own places only, in both orientations."""
-    gu, dh = gu_of(256, 256), acts(256, 256, 43, BF16, 1e-3)
+@pytest.mark.parametrize("rows,f", [(256, 256), (1664, 1024)])    # split by tensor, and whole
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_swiglu_bwd_fp8_nonfinite(puro, rows, f, value):
+    """A NaN or infinite gradient element: NaN codes at its own places only, in both orientations,
+    and scales that leave it out."""
+    gu, dh = gu_of(rows, f), acts(rows, f, 43, BF16, 1e-3)
+    gu[130, 9], gu[130, f + 9] = 0.75, -1.5      # du = dh silu(g) and dg = dh u silu'(g) both not 0
     a = puro.puro_swiglu_bwd_fp8(dh, gu)
     dh2 = dh.clone()
-    dh2[130, 9] = float("nan")
+    dh2[130, 9] = value
     b = puro.puro_swiglu_bwd_fp8(dh2, gu)
-    bad = torch.zeros((256, 512), dtype=torch.bool, device=DEV)
-    bad[130, 9] = bad[130, 265] = True
+    bad = torch.zeros((rows, 2 * f), dtype=torch.bool, device=DEV)
+    bad[130, 9] = bad[130, f + 9] = True
     for x, m in ((b.dguq, bad), (b.dgutq, bad.t())):
         assert torch.all((x[m] & 0x7F) == 0x7F) and torch.all((x[~m] & 0x7F) != 0x7F)
     assert same(a.htq, b.htq) and same(a.hts, b.hts)
-    keep = torch.ones(256, dtype=torch.bool, device=DEV)
+    keep = torch.ones(rows, dtype=torch.bool, device=DEV)
     keep[130] = False
-    assert same(a.dguq[keep], b.dguq[keep]) and torch.isfinite(b.dgus).all()
-    assert torch.isfinite(b.dguts).all()
+    assert same(a.dguq[keep], b.dguq[keep])
+    zero = dh.clone()           # the scales are those without the element
+    zero[130, 9] = 0.0
+    z = puro.puro_swiglu_bwd_fp8(zero, gu)
+    assert same(b.dgus, z.dgus) and same(b.dguts, z.dguts)
 
 
 # ------------------------------------------------------------------ how they are called
