@@ -34,7 +34,7 @@ def _stream(dev: torch.device) -> int:
 def _need(t: torch.Tensor, name: str, dtype, shape, dev) -> None:
     # the whole check at once first: it is what nearly every call passes, a dozen times a call
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous() and t.device == dev):
+            and t.layout is torch.strided and t.is_contiguous() and t.device == dev):
         return
     if not isinstance(t, torch.Tensor):
         raise PuroError(f"{name}: expected a torch.Tensor")
@@ -42,7 +42,7 @@ def _need(t: torch.Tensor, name: str, dtype, shape, dev) -> None:
         raise PuroError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if tuple(t.shape) != tuple(shape):
         raise PuroError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
+    if t.layout is not torch.strided or not t.is_contiguous():
         raise PuroError(f"{name}: must be contiguous")
     if t.device != dev:
         raise PuroError(f"{name}: on {t.device}, expected {dev}")
@@ -341,7 +341,8 @@ def _matrix(t, name):
 
 def _need_rows(x, name, dev):
     """A 2-D bf16 or fp32 matrix with unit column stride; returns (type, row stride)."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _TYPES:
+    if (not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _TYPES
+            or x.layout is not torch.strided):
         raise PuroError(f"{name}: expected a bf16 or fp32 matrix")
     if x.device != dev:
         raise PuroError(f"{name}: on {x.device}, expected {dev}")

@@ -2,8 +2,8 @@
 // their expected types, shapes, contiguity and device, and their addresses, in a microsecond
 // instead of the five that the same questions take through the interpreter.
 //
-//   ptrs(spec, device, d0, d1, d2, *tensors) -> tuple of addresses, or the index of the first tensor
-//                                               that is not as the specification says
+//   ptrs(spec, device, d0, d1, d2, *tensors) -> tuple of addresses, or the index of the first
+//                                               tensor that is not as the specification says
 //
 // spec: four bytes per tensor: its type (b bf16, f fp32, q uint8), ! or ? (may be None, address 0),
 // and the indices of its one or two sizes among d0, d1, d2 and the number 1 (3), - for none.
@@ -11,6 +11,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <exception>
 
 namespace {
 
@@ -43,9 +45,13 @@ PyObject* ptrs(PyObject*, PyObject* const* args, Py_ssize_t n) {
     uint64_t address = 0;
     bool ok = o == Py_None ? spec[1] == '?' : false;
     if (!ok && THPVariable_Check(o)) {
-      const at::Tensor& t = THPVariable_Unpack(o);
-      ok = as_specified(t, spec, v[0], dims);
-      if (ok) address = reinterpret_cast<uint64_t>(t.const_data_ptr());
+      try {
+        const at::Tensor& t = THPVariable_Unpack(o);
+        ok = as_specified(t, spec, v[0], dims);
+        if (ok) address = reinterpret_cast<uint64_t>(t.const_data_ptr());
+      } catch (const std::exception&) {  // a layout without strides or storage (sparse, nested)
+        ok = false;
+      }
     }
     PyObject* item = ok ? PyLong_FromUnsignedLongLong(address) : nullptr;
     if (item == nullptr) {

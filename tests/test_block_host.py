@@ -256,3 +256,16 @@ def test_binding_refuses_host_tensors():
                  lambda: puro.puro_block_norm_bwd(None, None, x, x, w, w, w, w)):
         with pytest.raises(PuroError):
             call()
+
+
+def test_binding_refuses_sparse_tensors():
+    """A tensor without strides has no answer to "is it contiguous": torch's exception for that must
+    not leave the native checks as one of C++."""
+    from blockwise_fp8_gemm_x128_amd import PuroError
+    from blockwise_fp8_gemm_x128_amd import binding as puro
+    dev = torch.device("cuda", 0)
+    q = torch.zeros((4, 8), dtype=torch.uint8).to_sparse_csr()
+    with pytest.raises(PuroError, match="q: must be contiguous"):
+        puro._PACK.pointers(dev, 4, 8, 1, q, None)
+    with pytest.raises(PuroError, match="x: expected a bf16 or fp32 matrix"):
+        puro._need_rows(torch.zeros((4, 8)).to_sparse_csr(), "x", dev)
