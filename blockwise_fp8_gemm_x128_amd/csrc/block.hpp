@@ -63,7 +63,7 @@ __host__ __device__ inline bool off_lines(int64_t cols) { return cols % 128 != 0
 // ---------------------------------------------------------------- vectors of eight
 // Rows of any length start at any element, so vectors are only element-aligned; the global
 // memory instructions take any address, and an aligned vector costs what it always did.
-typedef uint32_t u32x4_el __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_el __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x2_el __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t u32_el __attribute__((aligned(1)));
 typedef uint16_t u16_el __attribute__((aligned(1)));
@@ -248,8 +248,23 @@ __device__ __forceinline__ void values(Fp8x8 r, const Span<kShort>& s, float sca
 // next kernel reads. Measured on MI355X over rotating buffers: the activation of 8192 x 6144 with
 // its checkpoint 63.8 -> 55.4 us, the block norm of 4096 x 8192 72 -> 66.5 us forward and 78 -> 69
 // backward, of 8192 x 2048 33.3 -> 32.2 and 37.6 -> 38.2.
-template <bool kLater, typename V>
-__device__ __forceinline__ void put(V* p, V v) {
+// (One function per type: a template parameter would lose the pointer's weak alignment.)
+template <bool kLater>
+__device__ __forceinline__ void put(u32x4_el* p, u32x4_el v) {
+  if constexpr (kLater)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+template <bool kLater>
+__device__ __forceinline__ void put(u32x2_el* p, u32x2_el v) {
+  if constexpr (kLater)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+template <bool kLater>
+__device__ __forceinline__ void put(f32x4_el* p, f32x4_el v) {
   if constexpr (kLater)
     __builtin_nontemporal_store(v, p);
   else

@@ -5,12 +5,12 @@
 // (16 lanes cover a row, each wave 16 rows). A column's largest magnitude is a register maximum
 // over 4 rows, and then 32 words of LDS over the block, which one thread per column reads (lane
 // swaps within the wave first cost more instructions than the reads); that thread also does the
-// divisions. Only codes are transposed through LDS, one byte
-// per element: four rows of a column are one dword, and a column's 128 bytes leave as one line.
+// divisions. Only codes are transposed through LDS, one byte per element: four rows of a column
+// are one dword, and a column's 128 bytes leave as one line.
 //
-// Maxima and reciprocal scales of column 8 l + i stand at 64 (i / 4) + 4 l + i mod 4, so that a lane's
-// eight are two 16 B accesses, each contiguous over the lanes (as 8 l + i they were half of the
-// kernels' bank conflicts).
+// Maxima and reciprocal scales of column 8 l + i stand at 64 (i / 4) + 4 l + i mod 4, so that a
+// lane's eight are two 16 B accesses, each contiguous over the lanes (as 8 l + i they were half of
+// the kernels' bank conflicts).
 //
 // Dword of column 8 l + i, rows 4 g .. 4 g + 3: codes[(16 i + l) * kPitch + g]. With a pitch of 36
 // dwords the 16 lanes of a row start 16 different multiples of 4 banks and the wave's four row
@@ -24,15 +24,14 @@
 
 namespace puro {
 
-typedef uint32_t u32x4_by __attribute__((ext_vector_type(4), aligned(1)));
-
 constexpr int kTileThreads = 512;
 constexpr int kTileRows = 4;   // rows per thread
 
 template <int kN>
 struct ColTile {
   static constexpr int kPitch = 36;
-  union __attribute__((aligned(16))) {  // the maxima are read for the last time a barrier before the first code is written
+  // The maxima are read for the last time a barrier before the first code is written.
+  union __attribute__((aligned(16))) {
     uint32_t codes[kN][128 * kPitch];
     float maxima[kN][32][128];
   };
@@ -146,7 +145,7 @@ __device__ __forceinline__ void col_codes(ColTile<kN>& sh, const float (&v)[kN][
       if (col >= out[k].cols) continue;
       uint8_t* p = out[k].qt + col * rows + row;
       if (left >= 16) {
-        put<kLater>(reinterpret_cast<u32x4_by*>(p), u32x4_by{w.x, w.y, w.z, w.w});
+        put<kLater>(reinterpret_cast<u32x4_el*>(p), u32x4_el{w.x, w.y, w.z, w.w});
       } else {
         const uint32_t b[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll

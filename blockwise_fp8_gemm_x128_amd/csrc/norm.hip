@@ -76,7 +76,7 @@ struct Team {
   __device__ __forceinline__ explicit Team(int wpt) {
     lanes = kLanes == 1 ? 16 : kLanes ? kLanes : wpt * 64;
     team = threadIdx.x / lanes;
-    // teams of whole waves: the row is the same in all lanes of a wave, and its addresses are scalar
+    // teams of whole waves: the row is the same in all lanes of a wave, its addresses scalar
     if (kLanes == 0 || kLanes == 64) team = __builtin_amdgcn_readfirstlane(team);
     lane = threadIdx.x - team * lanes;
     teams = blockDim.x / lanes;
@@ -93,7 +93,7 @@ __device__ __forceinline__ void row_vector(const float* w, const Span<kShort>& s
     return;
   }
   F8 r;
-  load<false, kShort>(r, w, sp);
+  load<false, kShort>(r, row_ptr<true>(w, 0), sp);
   values(r, sp, f);
 }
 
@@ -233,22 +233,27 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_fwd_kernel(const Fwd
       const int n = in ? sp[j].n : 0;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) ss[0] = fmaf(t[j][i], t[j][i], ss[0]);
-      if (a.r_out) store8<true>(row_ptr<kUniform>(static_cast<R*>(a.r_out), at) + sp[j].col, n, t[j]);
+      if (a.r_out)
+        store8<true>(row_ptr<kUniform>(static_cast<R*>(a.r_out), at) + sp[j].col, n, t[j]);
       if (a.yq && a.rq) {  // both scales from one pair of divisions
         float both[2][kVec];
 #pragma unroll
         for (int i = 0; i < kVec; ++i) both[0][i] = y[j][i], both[1][i] = t[j][i];
         const uint32_t m[2] = {ymax[j], max8<false>(t[j])};
         const RowGroups<2> g = row_groups<2>(m, both, pow2);
-        store_codes<kUniform, true>({a.yq, a.ys}, row, a.rows, a.cols, sp[j].col, n, in, y[j], g.r[0], g.s, 0);
-        store_codes<kUniform, true>({a.rq, a.rs}, row, a.rows, a.cols, sp[j].col, n, in, t[j], g.r[1], g.s, 1);
+        store_codes<kUniform, true>({a.yq, a.ys}, row, a.rows, a.cols, sp[j].col, n, in,
+                                    y[j], g.r[0], g.s, 0);
+        store_codes<kUniform, true>({a.rq, a.rs}, row, a.rows, a.cols, sp[j].col, n, in,
+                                    t[j], g.r[1], g.s, 1);
       } else if (a.yq) {
         const uint32_t m[1] = {ymax[j]};
         const RowGroups<1> g = row_groups<1>(m, &y[j], pow2);
-        store_codes<kUniform, true>({a.yq, a.ys}, row, a.rows, a.cols, sp[j].col, n, in, y[j], g.r[0], g.s, 0);
+        store_codes<kUniform, true>({a.yq, a.ys}, row, a.rows, a.cols, sp[j].col, n, in,
+                                    y[j], g.r[0], g.s, 0);
       } else if (a.rq) {
         const RowGroups<1> g = row_groups<false, 1>(&t[j], pow2);
-        store_codes<kUniform, true>({a.rq, a.rs}, row, a.rows, a.cols, sp[j].col, n, in, t[j], g.r[0], g.s, 0);
+        store_codes<kUniform, true>({a.rq, a.rs}, row, a.rows, a.cols, sp[j].col, n, in,
+                                    t[j], g.r[0], g.s, 0);
       }
     }
     if (!a.w_pre) {
@@ -267,7 +272,8 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_fwd_kernel(const Fwd
       if (a.n) store8(row_ptr<kUniform>(a.n, at) + sp[j].col, n, o);
       if (a.nq) {
         const RowGroups<1> g = row_groups<false, 1>(&o, pow2);
-        store_codes<kUniform, false>({a.nq, a.ns}, row, a.rows, a.cols, sp[j].col, n, in, o, g.r[0], g.s, 0);
+        store_codes<kUniform, false>({a.nq, a.ns}, row, a.rows, a.cols, sp[j].col, n, in,
+                                     o, g.r[0], g.s, 0);
       }
     }
     if (kLanes == 0 && !a.y) __syncthreads();  // before sh[1] is written again
@@ -312,6 +318,13 @@ struct BwdRow<R, kNV, true> {
   float ry, rr, gt;
 };
 
+template <bool kUniform, bool kShort>
+__device__ __forceinline__ void load_gate(Bf16x8& g, const BwdArgs& a, int64_t row,
+                                          const Span<kShort>& sp) {
+  load<true, kShort>(
+      g, row_ptr<kUniform>(static_cast<const uint16_t*>(a.gate), row * a.cols), sp);
+}
+
 template <bool kUniform, typename R, int kNV, bool kCodes, bool kShort>
 __device__ __forceinline__ void load_row(BwdRow<R, kNV, kCodes>& w, const BwdArgs& a, int64_t row,
                                          const Span<kShort> (&sp)[kNV]) {
@@ -341,63 +354,87 @@ __device__ __forceinline__ void load_row(BwdRow<R, kNV, kCodes>& w, const BwdArg
         load<true, kShort>(w.y[j], row_ptr<kUniform>(a.y, at), sp[j]);
       }
     }
-    if (a.gate_kind == PURO_GATE_FULL)
-      load<true, kShort>(w.gate[j],
-                         row_ptr<kUniform>(static_cast<const uint16_t*>(a.gate), at), sp[j]);
+    if (kNV == 1 && a.gate_kind == PURO_GATE_FULL) load_gate<kUniform>(w.gate[j], a, row, sp[j]);
   }
 }
 
-// With two vectors per lane the weights are read again for each row (from the caches) and nothing is
-// loaded ahead: there are no registers for either.
+// The weight after the block times a channel gate, which is how both directions use it.
+template <bool kShort>
+__device__ __forceinline__ void post_weight(const BwdArgs& a, const Span<kShort>& sp, float* f) {
+  row_vector(a.w_post, sp, 0.0f, f);
+  float g[kVec];
+  row_vector(a.gate_kind == PURO_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr, sp,
+             1.0f, g);
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) f[i] *= g[i];
+}
+
+// Eight sums of a lane in LDS, its own: no other lane reads or writes them.
+__device__ __forceinline__ void lds_add(float4* lo, float4* hi, const float* f) {
+  float4 a = *lo, b = *hi;
+  a.x += f[0], a.y += f[1], a.z += f[2], a.w += f[3];
+  b.x += f[4], b.y += f[5], b.z += f[6], b.w += f[7];
+  *lo = a, *hi = b;
+}
+
+// Two vectors per lane (kWide: rows of more than 8192 columns, one per block of up to 1024 threads)
+// would take 190 registers where 128 are to be had: there the column sums stand in LDS (128 KB, one
+// block per CU as before), and the weights and a gate per element are read again where they are
+// used, from the caches. 4096 x 16384 in 182 us instead of 504, which were spills.
 template <typename R, int kLanes, int kNV, bool kCodes>
-__global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(
-    const BwdArgs a) {
+__global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(const BwdArgs a) {
   __shared__ float sh[2][3][kMaxWaves];
+  constexpr bool kWide = kNV == 2;
   constexpr bool kShort = kLanes == 1;  // rows of fewer than eight columns, in one lane of 16
   constexpr bool kUniform = kLanes == 0 || kLanes == 64;
   const Team<kLanes> tm(a.wpt);
   const float inv_d = 1.0f / static_cast<float>(a.cols);
-  const bool channel = a.gate_kind == PURO_GATE_CHANNEL, full = a.gate_kind == PURO_GATE_FULL;
+  const bool full = a.gate_kind == PURO_GATE_FULL;
   const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
 
   float wg[kNV][kVec], wp[kNV][kVec];  // w_post (times a channel gate); w_pre
+  __shared__ float4 own[kWide ? 2 : 1][kWide ? 2 * kNV : 1][kWide ? 1024 : 1];
   float acc[2][kNV][kVec] = {};
   Span<kShort> sp[kNV];
 #pragma unroll
   for (int j = 0; j < kNV; ++j) {
     sp[j] = Span<kShort>((j * tm.lanes + tm.lane) * kVec, a.cols,
                          a.cols != tm.lanes * kVec * kNV);
-    row_vector(a.w_post, sp[j], 0.0f, wg[j]);
-    float g[kVec];
-    row_vector(channel ? static_cast<const float*>(a.gate) : nullptr, sp[j], 1.0f, g);
+    if constexpr (kWide) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) wg[j][i] *= g[i];
-    row_vector(a.w_pre, sp[j], 0.0f, wp[j]);
+      for (int k = 0; k < 2; ++k)
+        own[k][2 * j][threadIdx.x] = own[k][2 * j + 1][threadIdx.x] = make_float4(0, 0, 0, 0);
+    } else {
+      post_weight(a, sp[j], wg[j]);
+      row_vector(a.w_pre, sp[j], 0.0f, wp[j]);
+    }
   }
 
   const int64_t first = int64_t(blockIdx.x) * a.rows_per_block;
   const int64_t end = min(a.rows, first + a.rows_per_block);
+  const int t = threadIdx.x;
   int buf = 0;
   BwdRow<R, kNV, kCodes> w;
   load_row<kUniform>(w, a, min(first + tm.team, end - 1), sp);
   for (int64_t base = first; base < end; base += tm.teams, buf ^= 1) {
-    // A team past the end works on the last row again, with its statistics taken as zero, so that
-    // it adds nothing to a column sum, and stores nothing.
+    // A team past the end has loaded the last row again; it takes its values as zero, whatever they
+    // are (that row may be changing in place), and stores nothing.
     const int64_t row = min(base + tm.team, end - 1);
     const bool in = base + tm.team < end;
-    const float ry = in ? w.ry : 0.0f, rr = in ? w.rr : 0.0f, gt = w.gt;
+    const float ry = in ? w.ry : 0.0f, rr = in ? w.rr : 0.0f, gt = in ? w.gt : 0.0f;
     float A[kNV][kVec], yh[kNV][kVec], rh[kNV][kVec];
     Bf16x8 graw[kNV];
     float sums[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < kNV; ++j) {
-      if (a.dr_out) {
+      if (a.dr_out && in) {
         values(w.d[j], sp[j], A[j]);
       } else {
 #pragma unroll
         for (int i = 0; i < kVec; ++i) A[j][i] = 0.0f;
       }
-      if (pre) {
+      if (pre && in) {
+        if constexpr (kWide) row_vector(a.w_pre, sp[j], 0.0f, wp[j]);
         float dn[kVec];
         values(w.dn[j], sp[j], dn);
         if constexpr (kCodes)
@@ -410,13 +447,18 @@ __global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(
           const float x = wp[j][i] * dn[i];
           A[j][i] = fmaf(rr, x, A[j][i]);
           sums[0] = fmaf(rh[j][i], x, sums[0]);
-          acc[1][j][i] = fmaf(dn[i], rh[j][i], acc[1][j][i]);
+          if constexpr (kWide)
+            dn[i] *= rh[j][i];
+          else
+            acc[1][j][i] = fmaf(dn[i], rh[j][i], acc[1][j][i]);
         }
+        if constexpr (kWide) lds_add(&own[1][2 * j][t], &own[1][2 * j + 1][t], dn);
       } else {
 #pragma unroll
         for (int i = 0; i < kVec; ++i) rh[j][i] = 0.0f;
       }
-      if (post) {
+      if (post && in) {
+        if constexpr (kWide) post_weight(a, sp[j], wg[j]);
         if constexpr (kCodes)
           values(w.y[j], sp[j], w.ys[j], yh[j]);
         else
@@ -429,7 +471,10 @@ __global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(
         }
         if (full) {
           float g[kVec];
-          graw[j] = w.gate[j];
+          if constexpr (kWide)
+            load_gate<kUniform>(graw[j], a, row, sp[j]);
+          else
+            graw[j] = w.gate[j];
           values(graw[j], sp[j], g);
 #pragma unroll
           for (int i = 0; i < kVec; ++i) q[i] *= g[i];
@@ -467,8 +512,10 @@ __global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(
       }
       if (a.dr) store8<true>(row_ptr<kUniform>(static_cast<R*>(a.dr), at) + col, n, o);
       if (post) {
-        if (full) {
+        if constexpr (kWide) post_weight(a, sp[j], wg[j]);
+        if (full && in) {
           float g[kVec];
+          if constexpr (kWide) load_gate<kUniform>(graw[j], a, row, sp[j]);
           values(graw[j], sp[j], g);
 #pragma unroll
           for (int i = 0; i < kVec; ++i) o[i] = a.alpha * yh[j][i] * wg[j][i] * G[i];
@@ -480,14 +527,30 @@ __global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
           G[i] *= gt;
-          acc[0][j][i] = fmaf(yh[j][i], G[i], acc[0][j][i]);
+          if constexpr (!kWide) acc[0][j][i] = fmaf(yh[j][i], G[i], acc[0][j][i]);
           o[i] = fmaf(wg[j][i] * ag, G[i], k2 * yh[j][i]);
         }
         store8(row_ptr<kUniform>(a.dy, at) + col, n, o);
+        if constexpr (kWide) {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) G[i] *= yh[j][i];
+          lds_add(&own[0][2 * j][t], &own[0][2 * j + 1][t], G);
+        }
       }
     }
   }
 
+  if constexpr (kWide) {
+#pragma unroll
+    for (int j = 0; j < kNV; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 lo = own[k][2 * j][t], hi = own[k][2 * j + 1][t];
+        const float f[kVec] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        store8(a.partials + (int64_t(blockIdx.x) * 2 + k) * a.cols + sp[j].col, sp[j].n, f);
+      }
+    return;
+  }
   // Column sums of the block: over the teams of a wave in registers, over the others through LDS,
   // where each thread then sums whole columns; one partial per block.
   extern __shared__ float red[];
@@ -730,7 +793,8 @@ extern "C" puro_status puro_block_norm_fwd(const puro_block_norm* d, void* strea
 extern "C" int64_t puro_block_norm_workspace(int64_t rows, int64_t cols) {
   if (!norm_dims_ok(rows, cols) || rows == 0 || cols == 0) return 0;
   const Shape s = shape_of(cols, kBwdThreads);
-  return int64_t(split_rows(rows, s, kBwdWaves, PURO_NORM_MAX_BLOCKS).blocks) * 2 * cols * sizeof(float);
+  const Split p = split_rows(rows, s, kBwdWaves, PURO_NORM_MAX_BLOCKS);
+  return int64_t(p.blocks) * 2 * cols * sizeof(float);
 }
 
 extern "C" puro_status puro_block_norm_bwd(const puro_block_norm_grad* d, void* workspace,

@@ -394,12 +394,12 @@ extern "C" puro_status puro_swiglu_bwd_fp8(const void* dh, const void* gu, const
                         {static_cast<const uint16_t*>(gu), static_cast<const uint8_t*>(guq), gus},
                         rows, f, static_cast<uint8_t*>(dguq), dgus, static_cast<uint8_t*>(dgutq),
                         dguts, static_cast<uint8_t*>(htq), hts, pow2};
-  // Tiles that leave two thirds of the CUs idle are split by tensor: 128 x 6144 (48 tiles) in 7.2 us
-  // against 8.2, 1024 x 1024 (64) in 7.4 against 8.4; but 1024 x 2048 (128) in 10.3 against 9.4.
+  // Tiles that leave two thirds of the CUs idle are split by tensor: 128 x 6144 (48 tiles) in 7.2
+  // us against 8.2, 1024 x 1024 (64) in 7.4 against 8.4; but 1024 x 2048 (128) in 10.3 against 9.4.
   const bool split = 3 * blocks <= 256;
-  // Codes of more bytes than the memory-side cache has (5 per element of h, 256 MiB) cannot all wait
-  // there for the GEMMs that read them, and go past it: 16384 x 6144 in 186 us against 198. Smaller
-  // ones stay: 4096 x 2048 in 17.7 us against 18.3, and their readers find them.
+  // Codes of more bytes than the memory-side cache has (5 per element of h, 256 MiB) cannot all
+  // wait there for the GEMMs that read them, and go past it: 16384 x 6144 in 186 us against 198.
+  // Smaller ones stay: 4096 x 2048 in 17.7 us against 18.3, and their readers find them.
   const bool later = 5 * rows * f > (int64_t(256) << 20);
   const auto k = gu != nullptr ? (split   ? swiglu_bwd_fp8_split_kernel<false>
                                   : later ? swiglu_bwd_fp8_kernel<false, true>

@@ -289,9 +289,8 @@ puro_status puro_ckpt_transpose(const void* q, const float* s, int64_t rows, int
  *   p = y * rstd_y * w_post,            rstd_y = 1/sqrt(mean(y^2) + eps)
  *   r_out = beta * r + alpha * gate * p
  *   n = r_out * rstd_r * w_pre,         rstd_r = 1/sqrt(mean(r_out^2) + eps)
- * n is formed from the unrounded r_out. Either half may be left out: w_post and y NULL
- * for the norm before a block alone (then r_out = beta * r), w_pre NULL for the norm after a block
- * alone.
+ * n is formed from the unrounded r_out. Either half may be left out: w_post and y NULL for the norm
+ * before a block alone (then r_out = beta * r), w_pre NULL for the norm after a block alone.
  * cols <= PURO_NORM_MAX_COLS. Sums of squares must fit fp32. */
 #define PURO_NORM_MAX_COLS 16384
 #define PURO_GATE_NONE 0
@@ -322,8 +321,9 @@ typedef struct {
 } puro_block_norm;
 puro_status puro_block_norm_fwd(const puro_block_norm* desc, void* stream);
 
-/* Block norm, backward. From the gradients of r_out (dr_out, NULL for zero) and n (dn) and from y and r_out as stored -- as they were, or
- * as checkpoints -- with their rstd_y and rstd_r, and with yh = y rstd_y, rh = r_out rstd_r:
+/* Block norm, backward. From the gradients of r_out (dr_out, NULL for zero) and n (dn) and from y
+ * and r_out as stored -- as they were, or as checkpoints -- with their rstd_y and rstd_r, and with
+ * yh = y rstd_y, rh = r_out rstd_r:
  *   G  = dr_out + rstd_r (w_pre dn - rh mean(rh w_pre dn))
  *   dr = beta G                                (may be dr_out itself; NULL to skip)
  *   dp = alpha gate G,  dy = rstd_y (w_post dp - yh mean(yh w_post dp))
@@ -331,10 +331,11 @@ puro_status puro_block_norm_fwd(const puro_block_norm* desc, void* stream);
  *   dgate = alpha w_post yh G, summed over rows (PURO_GATE_CHANNEL), over columns
  *           (PURO_GATE_TOKEN) or as it is (PURO_GATE_FULL), in the gate's type
  * accumulate = 1 adds dw_post, dw_pre and a channel gate's gradient to what is there. w_post NULL:
- * the norm after the block was left out; w_pre NULL: the norm before the next one. workspace: puro_block_norm_workspace(rows, cols) bytes
- * of caller-owned device memory, 16-byte aligned, used by one call at a time (at most
- * PURO_NORM_MAX_BLOCKS partial sums of 8 bytes per column). y and r are both as they were or both
- * checkpoints. */
+ * the norm after the block was left out; w_pre NULL: the norm before the next one. y and r are both
+ * as they were or both checkpoints.
+ * workspace: puro_block_norm_workspace(rows, cols) bytes of caller-owned device memory, 16-byte
+ * aligned, used by one call at a time (at most PURO_NORM_MAX_BLOCKS partial sums of 8 bytes per
+ * column). */
 #define PURO_NORM_MAX_BLOCKS 512
 typedef struct {
   int64_t rows, cols;

@@ -308,6 +308,30 @@ def test_norm_empty(puro):
     assert puro.puro_swiglu_bwd(e, torch.empty((5, 0), dtype=BF16, device=DEV)).shape == (5, 0)
 
 
+@pytest.mark.parametrize("kind", ["none", "channel", "token", "full"])
+@pytest.mark.parametrize("res,saved", [(BF16, "fp8"), (F32, "asis")])
+def test_norm_bwd_wide_rows(puro, kind, res, saved):
+    """More than 8192 columns, and several rows to a block."""
+    rows, cols = 520, 8328
+    say("norm bwd wide", kind, res, saved)
+    d = bwd_inputs(puro, rows, cols, res, kind, saved)
+    v, e = bwd_ref(d, kind, 0.75, 0.9375)
+    check_bwd(bwd_call(puro, d, 0.75, 0.9375), v, e, res, kind)
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 256), (1, 100), (5, 5), (3, 600)])
+def test_norm_bwd_infinite_gradient_in_the_last_row(puro, rows, cols):
+    """An infinite element of dn in the last row makes its column of dw_pre infinite, with the sign
+    of its normalised activation, not NaN, and no other column: lanes without a row of their own,
+    which there are at these sizes, add nothing."""
+    d = bwd_inputs(puro, rows, cols, F32, "none", "asis", half="pre")
+    d["t"][-1] = rnd((cols,), 3).abs() + 0.5
+    d["dn"][-1, 1] = float("inf")
+    o = bwd_call(puro, d, 1.0, 1.0)
+    assert o.dw_pre[1].item() == float("inf")
+    assert torch.isfinite(o.dw_pre[torch.arange(cols, device=DEV) != 1]).all()
+
+
 @pytest.mark.parametrize("value", [float("inf"), -float("inf")])
 def test_norm_infinite_residual_stays_in_its_row(puro, value):
     """An infinity in the residual stream: its row's statistics fail, no other row changes, and the
