@@ -262,7 +262,7 @@ def test_norm_bwd_gates(puro, kind, rows, cols, res, saved):
 
 
 @pytest.mark.parametrize("half", ["post", "pre"])
-@pytest.mark.parametrize("rows,cols", [(1, 64), (50, 520), (1100, 2048)])
+@pytest.mark.parametrize("rows,cols", [(1, 64), (50, 520), (1100, 2048), (300, 9000)])
 def test_norm_bwd_halves(puro, half, rows, cols):
     d = bwd_inputs(puro, rows, cols, BF16, "channel", "fp8", half)
     v, e = bwd_ref(d, "channel", 1.5, 1.0)
