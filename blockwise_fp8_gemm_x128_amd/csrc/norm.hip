@@ -14,8 +14,9 @@
 //
 // HBM-bound: every element of every input is read once into registers, where the row stays until
 // its last output is written; a row belongs to one team of lanes (16, 32 or 64 lanes of a wave for
-// short rows, whole waves for longer ones), 8 columns per lane and vector. All statistics and
-// sums are fp32; r' is normalised unrounded, so n does not see the residual stream's rounding.
+// short rows, whole waves or groups of 16 lanes for longer ones), 8 columns per lane and vector.
+// All statistics and sums are fp32; r' is normalised unrounded, so n does not see the residual
+// stream's rounding.
 #include <algorithm>
 #include <cmath>
 
@@ -25,15 +26,31 @@ namespace puro {
 namespace {
 
 constexpr int kMaxWaves = 16;  // of a block
+// How a row lies over lanes (kLanes): 16, 32 or 64 lanes of a wave, one lane of 16 (kOne: rows of
+// fewer than eight columns), whole waves (kWaves) or groups of 16 lanes (kGroups), `wpt` of them.
+constexpr int kWaves = 0, kOne = 1, kGroups = 2;
 
-// Sum over the team of each of kN values. Teams of whole waves go through LDS with one barrier;
-// `buf` alternates between calls, so a wave that is already writing the next call's values never
-// meets one still reading this call's. kLanes = 0: a team of `wpt` waves.
-template <int kLanes, int kN>
-__device__ __forceinline__ void team_sum(float (&v)[kN], float (*sh)[kMaxWaves], int wpt) {
-  if constexpr (kLanes != 0) {
+// Sum over the team of each of kN values. Teams across waves go through LDS with one barrier;
+// `sh` alternates between calls, so a wave that is already writing the next call's values never
+// meets one still reading this call's.
+template <int kLanes, int kN, int kMax>
+__device__ __forceinline__ void team_sum(float (&v)[kN], float (*sh)[kMax], int wpt) {
+  if constexpr (kLanes == kGroups) {
+    const int g = threadIdx.x >> 4, l = threadIdx.x & 15, g0 = g - g % wpt;
 #pragma unroll
-    for (int k = 0; k < kN; ++k) v[k] = lanes_sum<kLanes == 1 ? 16 : kLanes>(v[k]);
+    for (int k = 0; k < kN; ++k) {
+      v[k] = lanes_sum<16>(v[k]);
+      if (l == 0) sh[k][g] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const float t = sh[k][min(g0 + l, kMax - 1)];
+      v[k] = lanes_sum<16>(l < wpt ? t : 0.0f);
+    }
+  } else if constexpr (kLanes != 0) {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) v[k] = lanes_sum<kLanes == kOne ? 16 : kLanes>(v[k]);
   } else {
     const int wave = threadIdx.x >> 6, w0 = wave - wave % wpt;
 #pragma unroll
@@ -56,12 +73,12 @@ __device__ __forceinline__ void team_sum(float (&v)[kN], float (*sh)[kMaxWaves],
 // Sum over a wave's teams of kLanes lanes, lane by lane.
 template <int kLanes>
 __device__ __forceinline__ float teams_sum(float v) {
-  if constexpr (kLanes == 1 || kLanes == 16) {
+  if constexpr (kLanes == kOne || kLanes == 16) {
     const uint32_t u = __float_as_uint(v);
     const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
     v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
   }
-  if constexpr (kLanes == 1 || kLanes == 16 || kLanes == 32) {
+  if constexpr (kLanes == kOne || kLanes == 16 || kLanes == 32) {
     const uint32_t u = __float_as_uint(v);
     const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
     v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
@@ -74,14 +91,29 @@ template <int kLanes>
 struct Team {
   int lanes, lane, team, teams;
   __device__ __forceinline__ explicit Team(int wpt) {
-    lanes = kLanes == 1 ? 16 : kLanes ? kLanes : wpt * 64;
+    lanes = kLanes == kWaves    ? wpt * 64
+            : kLanes == kGroups ? wpt * 16
+            : kLanes == kOne    ? 16
+                                : kLanes;
     team = threadIdx.x / lanes;
     // teams of whole waves: the row is the same in all lanes of a wave, its addresses scalar
-    if (kLanes == 0 || kLanes == 64) team = __builtin_amdgcn_readfirstlane(team);
+    if (kLanes == kWaves || kLanes == 64) team = __builtin_amdgcn_readfirstlane(team);
     lane = threadIdx.x - team * lanes;
     teams = blockDim.x / lanes;
   }
+  // Lanes of a block of groups that make no whole team (team == teams) have no row.
+  __device__ __forceinline__ bool has_row(int base, int end) const {
+    return base + team < end && (kLanes != kGroups || team < teams);
+  }
 };
+
+// The rows of a block: `teams` a step, in steps dealt out evenly.
+template <typename Args>
+__device__ __forceinline__ void block_rows(const Args& a, int teams, int& first, int& end) {
+  const int b = blockIdx.x;
+  first = (b * a.steps + min(b, a.more)) * teams;   // of at most 2^24 rows
+  end = min(static_cast<int>(a.rows), first + (a.steps + (b < a.more)) * teams);
+}
 
 // Eight of a vector over the columns (a weight, a gate), or `none` where there is none.
 template <bool kShort>
@@ -105,7 +137,7 @@ struct FwdArgs {
   const void* gate;
   int gate_kind, pow2;
   int64_t rows;
-  int cols, wpt, rows_per_block;
+  int cols, wpt, steps, more;   // steps of a block; of the first `more` blocks one more
   float alpha, beta, eps;
   void* r_out;
   uint16_t* n;
@@ -156,10 +188,12 @@ __device__ __forceinline__ void load_row(FwdRow<R, kNV>& w, const FwdArgs& a, in
 }
 
 template <typename R, int kLanes, int kNV>
-__global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_fwd_kernel(const FwdArgs a) {
-  __shared__ float sh[2][1][kMaxWaves];
-  constexpr bool kShort = kLanes == 1;  // rows of fewer than eight columns, in one lane of 16
-  constexpr bool kUniform = kLanes == 0 || kLanes == 64;
+__global__ __launch_bounds__(kLanes == kWaves ? 1024 : kLanes == kGroups ? 320 : 256)
+void norm_fwd_kernel(const FwdArgs a) {
+  constexpr bool kCross = kLanes == kWaves || kLanes == kGroups;  // teams across waves
+  __shared__ float sh[2][1][kLanes == kGroups ? 32 : kMaxWaves];
+  constexpr bool kShort = kLanes == kOne;  // rows of fewer than eight columns, in one lane of 16
+  constexpr bool kUniform = kLanes == kWaves || kLanes == 64;
   const Team<kLanes> tm(a.wpt);
   const float inv_d = 1.0f / static_cast<float>(a.cols);
   const bool channel = a.gate_kind == PURO_GATE_CHANNEL, full = a.gate_kind == PURO_GATE_FULL;
@@ -179,13 +213,13 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_fwd_kernel(const Fwd
     row_vector(a.w_pre, sp[j], 0.0f, pw[j]);
   }
 
-  const int64_t first = int64_t(blockIdx.x) * a.rows_per_block;
-  const int64_t end = min(a.rows, first + a.rows_per_block);
-  // A team past the end works on the last row again and stores nothing.
+  int first, end;
+  block_rows(a, tm.teams, first, end);
+  // A team without a row works on the last one again and stores nothing.
   FwdRow<R, kNV> w;
-  for (int64_t base = first; base < end; base += tm.teams) {  // the same count for every team
+  for (int base = first; base < end; base += tm.teams) {  // the same count for every team
     const int64_t row = min(base + tm.team, end - 1);
-    const bool in = base + tm.team < end;
+    const bool in = tm.has_row(base, end);
     load_row<kUniform>(w, a, row, sp);
     const int64_t at = row * a.cols;
     float y[kNV][kVec], t[kNV][kVec];
@@ -201,7 +235,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_fwd_kernel(const Fwd
 #pragma unroll
         for (int i = 0; i < kVec; ++i) ss[0] = fmaf(y[j][i], y[j][i], ss[0]);
       }
-      team_sum<kLanes, 1>(ss, sh[0], a.wpt);
+      team_sum<kLanes>(ss, sh[0], a.wpt);
       ry = rsqrtf(fmaf(ss[0], inv_d, a.eps));
       if (in && tm.lane == 0) a.rstd_y[row] = ry;
     }
@@ -257,10 +291,10 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_fwd_kernel(const Fwd
       }
     }
     if (!a.w_pre) {
-      if constexpr (kLanes == 0) __syncthreads();  // before sh[0] is written again
+      if constexpr (kCross) __syncthreads();  // before sh[0] is written again
       continue;
     }
-    team_sum<kLanes, 1>(ss, sh[1], a.wpt);
+    team_sum<kLanes>(ss, sh[1], a.wpt);
     const float rr = rsqrtf(fmaf(ss[0], inv_d, a.eps));
     if (in && tm.lane == 0) a.rstd_r[row] = rr;
 #pragma unroll
@@ -276,7 +310,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_fwd_kernel(const Fwd
                                      o, g.r[0], g.s, 0);
       }
     }
-    if (kLanes == 0 && !a.y) __syncthreads();  // before sh[1] is written again
+    if (kCross && !a.y) __syncthreads();  // before sh[1] is written again
   }
 }
 
@@ -294,7 +328,7 @@ struct BwdArgs {
   const void* gate;
   int gate_kind;
   int64_t rows;
-  int cols, wpt, rows_per_block;
+  int cols, wpt, steps, more;   // steps of a block; of the first `more` blocks one more
   float alpha, beta;
   void* dr;
   uint16_t* dy;
@@ -382,11 +416,13 @@ __device__ __forceinline__ void lds_add(float4* lo, float4* hi, const float* f) 
 // block per CU as before), and the weights and a gate per element are read again where they are
 // used, from the caches. 4096 x 16384 in 182 us instead of 504, which were spills.
 template <typename R, int kLanes, int kNV, bool kCodes>
-__global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(const BwdArgs a) {
-  __shared__ float sh[2][3][kMaxWaves];
+__global__ __launch_bounds__(kLanes == kWaves ? 1024 : 512, kLanes == kGroups ? 4 : 1)
+void norm_bwd_kernel(const BwdArgs a) {
+  constexpr bool kCross = kLanes == kWaves || kLanes == kGroups;  // teams across waves
+  __shared__ float sh[2][3][kLanes == kGroups ? 32 : kMaxWaves];
   constexpr bool kWide = kNV == 2;
-  constexpr bool kShort = kLanes == 1;  // rows of fewer than eight columns, in one lane of 16
-  constexpr bool kUniform = kLanes == 0 || kLanes == 64;
+  constexpr bool kShort = kLanes == kOne;  // rows of fewer than eight columns, in one lane of 16
+  constexpr bool kUniform = kLanes == kWaves || kLanes == 64;
   const Team<kLanes> tm(a.wpt);
   const float inv_d = 1.0f / static_cast<float>(a.cols);
   const bool full = a.gate_kind == PURO_GATE_FULL;
@@ -410,17 +446,17 @@ __global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(const Bwd
     }
   }
 
-  const int64_t first = int64_t(blockIdx.x) * a.rows_per_block;
-  const int64_t end = min(a.rows, first + a.rows_per_block);
+  int first, end;
+  block_rows(a, tm.teams, first, end);
   const int t = threadIdx.x;
   int buf = 0;
   BwdRow<R, kNV, kCodes> w;
   load_row<kUniform>(w, a, min(first + tm.team, end - 1), sp);
-  for (int64_t base = first; base < end; base += tm.teams, buf ^= 1) {
-    // A team past the end has loaded the last row again; it takes its values as zero, whatever they
-    // are (that row may be changing in place), and stores nothing.
+  for (int base = first; base < end; base += tm.teams, buf ^= 1) {
+    // A team without a row has loaded the last one again; it takes its values as zero, whatever
+    // they are (that row may be changing in place), and stores nothing.
     const int64_t row = min(base + tm.team, end - 1);
-    const bool in = base + tm.team < end;
+    const bool in = tm.has_row(base, end);
     const float ry = in ? w.ry : 0.0f, rr = in ? w.rr : 0.0f, gt = in ? w.gt : 0.0f;
     float A[kNV][kVec], yh[kNV][kVec], rh[kNV][kVec];
     Bf16x8 graw[kNV];
@@ -492,7 +528,7 @@ __global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(const Bwd
     // the next row's loads go out before this one's sums and stores
     if (base + tm.teams < end)
       load_row<kUniform>(w, a, min(base + tm.teams + tm.team, end - 1), sp);
-    team_sum<kLanes, 3>(sums, sh[buf], a.wpt);
+    team_sum<kLanes>(sums, sh[buf], a.wpt);
     const float k1 = rr * sums[0] * inv_d;
     const float qg = sums[1] - k1 * sums[2];  // sum of q G
     const float ag = a.alpha * ry;
@@ -554,9 +590,9 @@ __global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(const Bwd
   // Column sums of the block: over the teams of a wave in registers, over the others through LDS,
   // where each thread then sums whole columns; one partial per block.
   extern __shared__ float red[];
-  const int lanes = kLanes == 0 ? tm.lanes : kLanes == 1 ? 16 : kLanes;
-  const int rows = kLanes == 0 ? tm.teams : static_cast<int>(blockDim.x >> 6);
-  const int at = kLanes == 0 ? threadIdx.x
+  const int lanes = tm.lanes;
+  const int rows = kCross ? tm.teams : static_cast<int>(blockDim.x >> 6);
+  const int at = kCross ? threadIdx.x
                              : (threadIdx.x >> 6) * lanes + (threadIdx.x & 63);  // of kLanes lanes
   const int width = lanes * kVec;
 #pragma unroll
@@ -569,12 +605,12 @@ __global__ __launch_bounds__(kLanes ? 512 : 1024) void norm_bwd_kernel(const Bwd
     if (rows == 1) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        store8(a.partials + (int64_t(blockIdx.x) * 2 + k) * a.cols + sp[j].col, sp[j].n,
-               acc[k][j]);
+        store8(a.partials + (int64_t(blockIdx.x) * 2 + k) * a.cols + sp[j].col,
+               tm.team < tm.teams ? sp[j].n : 0, acc[k][j]);
       continue;
     }
     __syncthreads();
-    if (kLanes == 0 || kLanes == 64 || (threadIdx.x & 63) < lanes)
+    if (kCross ? tm.team < tm.teams : kLanes == 64 || (threadIdx.x & 63) < lanes)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float4* dst = reinterpret_cast<float4*>(red + k * rows * width + at * kVec);
@@ -648,26 +684,49 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const ReduceArgs a) {
 
 // ------------------------------------------------------------------ host side
 // How a row is laid over lanes: 16, 32 or 64 lanes of 8 columns up to 512 columns, then whole
-// waves, one vector per lane up to 8192 columns and two beyond.
+// waves, one vector per lane up to 8192 columns and two beyond; or, up to 2048 columns, groups of
+// 16 lanes in a block of `least` to `most` threads.
 struct Shape {
-  int lanes;     // 16, 32, 64, 1 (16 of which one has the row), or 0 for whole waves
+  int lanes;     // 16, 32, 64, kOne, kGroups or kWaves
   int nv;        // vectors of 8 columns per lane
-  int wpt;       // waves per team (whole waves)
+  int wpt;       // waves or groups per team
   int threads;   // per block
   int teams;     // per block
 };
+struct Blocks {
+  int threads, least, most;   // of several teams; of groups
+};
+constexpr Blocks kFwdBlocks = {256, 192, 320}, kBwdBlocks = {512, 256, 448};
 
-Shape shape_of(int64_t cols, int most_threads) {
-  Shape s = {0, 1, 0, most_threads, 0};
+// Groups are taken where they leave fewer lanes idle, and at most one in twelve. They cost vector
+// registers for addresses and a reduction across waves. In 16.8 M elements with checkpoints rows of
+// 384 columns (3 groups in 4 groups' lanes before) take 33.6 us forward against 35.7 with whole
+// waves, of 640 33.8 against 38.5, 768 33.5 against 36.0, 1280 33.4 against 35.2; backward 384 37.2
+// against 40.4, 640 38.8 against 44.1, 896 37.0 against 39.0, 1152 37.1 against 45.1. Where a block
+// does not come out even they lose: 1408 columns forward, 35.6 against 34.0.
+Shape shape_of(int64_t cols, const Blocks& b) {
   const int64_t vecs = ceil_div(cols, kVec);
+  const int m = static_cast<int>(ceil_div(cols, 128));
+  const int in_waves = m <= 4 ? (m == 3 ? 4 : m) : static_cast<int>(ceil_div(m, 4)) * 4;
+  if (m < in_waves && m <= 16) {
+    Shape s = {kGroups, 1, m, 0, 0};
+    double most = 0;  // part of the lanes in use
+    for (int t = b.least; t <= b.most; t += 64) {
+      const int groups = t / 16, teams = groups / m;
+      const double used = double(teams * m) / groups;
+      if (used > most) most = used, s.threads = t, s.teams = teams;
+    }
+    if (most > double(m) / in_waves && most > 0.91) return s;
+  }
+  Shape s = {kWaves, 1, 0, b.threads, 0};
   if (vecs <= 64) {
-    s.lanes = cols < kVec ? 1 : vecs <= 16 ? 16 : vecs <= 32 ? 32 : 64;
+    s.lanes = cols < kVec ? kOne : vecs <= 16 ? 16 : vecs <= 32 ? 32 : 64;
     s.teams = s.threads / std::max(s.lanes, 16);
     return s;
   }
   s.nv = vecs <= 1024 ? 1 : 2;
   s.wpt = static_cast<int>(ceil_div(vecs, 64 * s.nv));
-  s.teams = std::max(1, most_threads / (64 * s.wpt));
+  s.teams = std::max(1, b.threads / (64 * s.wpt));
   s.threads = 64 * s.wpt * s.teams;
   return s;
 }
@@ -678,40 +737,47 @@ bool norm_dims_ok(int64_t rows, int64_t cols) {
   return any_dim_ok(rows) && cols >= 0 && cols <= PURO_NORM_MAX_COLS;
 }
 
-// Blocks and rows per block. A block keeps its weights (and column sums) over consecutive rows, so
-// the grid is at most what the chip holds at once: `waves` per CU, which the kernel's registers
-// allow, in a whole number of blocks per CU, at least half as many. Of these numbers the one whose
-// busiest CU gets the fewest row steps is taken, the larger of equals: for 8192 rows of 2048
-// columns forward 4 blocks per CU of 8 rows each (33 us) and not 5 or 6 of 7 or 6 (34 to 36 us);
-// for 5120 columns 2 blocks of ten waves (44 us) and not 4 (53 us).
+// Blocks, and steps of one row per team for each. A block keeps its weights (and column sums) over
+// consecutive rows, so the grid is what the chip holds at once: `waves` per CU, which the kernel's
+// registers allow, in whole blocks. Steps are dealt out evenly, the first `more` blocks taking one
+// more, so that the CUs, which get every 256th block, differ by a step at most (blocks of equal
+// length left some CUs a block's length ahead of others: 896 columns forward 42.5 -> 34.3 us, 1152
+// backward 55.9 -> 45.1); and only as many CUs are used as the busiest one's steps ask for, which
+// saves partial sums.
 constexpr int kCus = 256;
 struct Split {
-  int blocks, rows_per_block;
+  int blocks, steps, more;
 };
 Split split_rows(int64_t rows, const Shape& s, int waves, int most_blocks) {
-  const int64_t steps = ceil_div(rows, s.teams);  // of one row per team
-  const int most = std::min(most_blocks / kCus, std::max(1, waves / (s.threads / 64)));
-  int64_t per = 0, busiest = INT64_MAX;
-  for (int k = most; 2 * k >= most && k > 0; --k) {
-    const int64_t n = std::max<int64_t>(1, ceil_div(steps, int64_t(kCus) * k));
-    if (n * k < busiest) busiest = n * k, per = n;
-  }
+  const int64_t steps = ceil_div(rows, s.teams);
+  const int per_cu = std::min(most_blocks / kCus, std::max(1, waves / (s.threads / 64)));
+  const int64_t cus = ceil_div(steps, ceil_div(steps, kCus));
   Split p;
-  p.rows_per_block = static_cast<int>(per * s.teams);
-  p.blocks = static_cast<int>(ceil_div(rows, p.rows_per_block));
+  p.blocks = static_cast<int>(std::min(steps, per_cu * cus));
+  p.steps = static_cast<int>(steps / p.blocks);
+  p.more = static_cast<int>(steps % p.blocks);
   return p;
 }
-constexpr int kFwdThreads = 256, kFwdWaves = 24;  // threads of blocks of several teams
-constexpr int kBwdThreads = 512, kBwdWaves = 16;
+constexpr int kBwdWaves = 16;
+// Forward: as many waves as the registers allow, but 16 (where blocks make 16) for rows of a
+// multiple of 4 KB in bf16, whose blocks seem to meet on the same memory channels: 8192 x 2048 32.2
+// us against 33.5 with 24, in fp32 47.9 against 50.9, 4096 x 4096 31.6 against 33.4; but 1792
+// columns 35.6 against 34.3, and 6144 columns, where it would be 12 waves, 55.8 against 47.6.
+int fwd_waves(const Shape& s, int64_t cols) {
+  if (s.nv == 2 || s.lanes == kGroups) return 16;
+  if (cols % 2048 == 0 && 16 % (s.threads / 64) == 0) return 16;
+  return s.lanes == kWaves || s.lanes == 64 ? 24 : 20;
+}
 
 template <typename R>
 void launch_fwd(const FwdArgs& a, const Shape& s, int blocks, hipStream_t st) {
-  const auto k = s.lanes == 1    ? norm_fwd_kernel<R, 1, 1>
-                 : s.lanes == 16 ? norm_fwd_kernel<R, 16, 1>
-                 : s.lanes == 32 ? norm_fwd_kernel<R, 32, 1>
-                 : s.lanes == 64 ? norm_fwd_kernel<R, 64, 1>
-                 : s.nv == 1     ? norm_fwd_kernel<R, 0, 1>
-                                 : norm_fwd_kernel<R, 0, 2>;
+  const auto k = s.lanes == kOne      ? norm_fwd_kernel<R, kOne, 1>
+                 : s.lanes == kGroups ? norm_fwd_kernel<R, kGroups, 1>
+                 : s.lanes == 16      ? norm_fwd_kernel<R, 16, 1>
+                 : s.lanes == 32      ? norm_fwd_kernel<R, 32, 1>
+                 : s.lanes == 64      ? norm_fwd_kernel<R, 64, 1>
+                 : s.nv == 1          ? norm_fwd_kernel<R, kWaves, 1>
+                                      : norm_fwd_kernel<R, kWaves, 2>;
   hipLaunchKernelGGL(k, dim3(blocks), dim3(s.threads), 0, st, a);
 }
 
@@ -719,15 +785,19 @@ template <typename R, bool kCodes>
 void launch_bwd(const BwdArgs& a, const Shape& s, int blocks, hipStream_t st) {
   const dim3 grid(blocks), block(s.threads);
   // two accumulators of the teams (of the waves, for teams within one) as whole rows
-  const int rows = s.lanes ? s.threads / 64 : s.teams;
-  const int lanes = s.lanes ? std::max(s.lanes, 16) : s.wpt * 64;
+  const bool cross = s.lanes == kWaves || s.lanes == kGroups;
+  const int rows = cross ? s.teams : s.threads / 64;
+  const int lanes = s.lanes == kWaves    ? s.wpt * 64
+                    : s.lanes == kGroups ? s.wpt * 16
+                                         : std::max(s.lanes, 16);
   const size_t lds = rows > 1 ? size_t(2) * rows * lanes * kVec * sizeof(float) : 0;
-  const auto k = s.lanes == 1    ? norm_bwd_kernel<R, 1, 1, kCodes>
-                 : s.lanes == 16 ? norm_bwd_kernel<R, 16, 1, kCodes>
-                 : s.lanes == 32 ? norm_bwd_kernel<R, 32, 1, kCodes>
-                 : s.lanes == 64 ? norm_bwd_kernel<R, 64, 1, kCodes>
-                 : s.nv == 1     ? norm_bwd_kernel<R, 0, 1, kCodes>
-                                 : norm_bwd_kernel<R, 0, 2, kCodes>;
+  const auto k = s.lanes == kOne      ? norm_bwd_kernel<R, kOne, 1, kCodes>
+                 : s.lanes == kGroups ? norm_bwd_kernel<R, kGroups, 1, kCodes>
+                 : s.lanes == 16      ? norm_bwd_kernel<R, 16, 1, kCodes>
+                 : s.lanes == 32      ? norm_bwd_kernel<R, 32, 1, kCodes>
+                 : s.lanes == 64      ? norm_bwd_kernel<R, 64, 1, kCodes>
+                 : s.nv == 1          ? norm_bwd_kernel<R, kWaves, 1, kCodes>
+                                      : norm_bwd_kernel<R, kWaves, 2, kCodes>;
   hipLaunchKernelGGL(k, grid, block, lds, st, a);
 }
 
@@ -775,14 +845,14 @@ extern "C" puro_status puro_block_norm_fwd(const puro_block_norm* d, void* strea
   PURO_TRY(check_pair(d->yq, d->ys));
   PURO_TRY(check_pair(d->rq, d->rs));
 
-  const Shape s = shape_of(d->cols, kFwdThreads);
+  const Shape s = shape_of(d->cols, kFwdBlocks);
   FwdArgs a = {static_cast<const uint16_t*>(d->y), d->r, d->w_post, d->w_pre, d->gate,
-               d->gate_kind, d->pow2, d->rows, static_cast<int>(d->cols), s.wpt, 0, d->alpha,
+               d->gate_kind, d->pow2, d->rows, static_cast<int>(d->cols), s.wpt, 0, 0, d->alpha,
                d->beta, d->eps, d->r_out, static_cast<uint16_t*>(d->n),
                static_cast<uint8_t*>(d->nq), d->ns, d->rstd_y, d->rstd_r,
                static_cast<uint8_t*>(d->yq), d->ys, static_cast<uint8_t*>(d->rq), d->rs};
-  const Split p = split_rows(d->rows, s, kFwdWaves, INT32_MAX);
-  a.rows_per_block = p.rows_per_block;
+  const Split p = split_rows(d->rows, s, fwd_waves(s, d->cols), INT32_MAX);
+  a.steps = p.steps, a.more = p.more;
   if (d->residual_type == PURO_TYPE_BF16)
     launch_fwd<uint16_t>(a, s, p.blocks, static_cast<hipStream_t>(stream));
   else
@@ -792,7 +862,7 @@ extern "C" puro_status puro_block_norm_fwd(const puro_block_norm* d, void* strea
 
 extern "C" int64_t puro_block_norm_workspace(int64_t rows, int64_t cols) {
   if (!norm_dims_ok(rows, cols) || rows == 0 || cols == 0) return 0;
-  const Shape s = shape_of(cols, kBwdThreads);
+  const Shape s = shape_of(cols, kBwdBlocks);
   const Split p = split_rows(rows, s, kBwdWaves, PURO_NORM_MAX_BLOCKS);
   return int64_t(p.blocks) * 2 * cols * sizeof(float);
 }
@@ -845,17 +915,17 @@ extern "C" puro_status puro_block_norm_bwd(const puro_block_norm_grad* d, void* 
   PURO_TRY(check_optional(d->dw_pre));
 
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const Shape s = shape_of(d->cols, kBwdThreads);
+  const Shape s = shape_of(d->cols, kBwdBlocks);
   int blocks = 0;
   if (!empty) {
     BwdArgs a = {d->dr_out, static_cast<const uint16_t*>(d->dn),
                  static_cast<const uint16_t*>(d->y), static_cast<const uint8_t*>(d->yq), d->ys,
                  d->r, static_cast<const uint8_t*>(d->rq), d->rs, d->rstd_y, d->rstd_r, d->w_post,
                  d->w_pre, d->gate, d->gate_kind, d->rows, static_cast<int>(d->cols), s.wpt, 0,
-                 d->alpha, d->beta, d->dr, static_cast<uint16_t*>(d->dy), d->dgate,
+                 0, d->alpha, d->beta, d->dr, static_cast<uint16_t*>(d->dy), d->dgate,
                  static_cast<float*>(workspace)};
     const Split p = split_rows(d->rows, s, kBwdWaves, PURO_NORM_MAX_BLOCKS);
-    a.rows_per_block = p.rows_per_block;
+    a.steps = p.steps, a.more = p.more;
     blocks = p.blocks;
     const bool codes = d->yq != nullptr || d->rq != nullptr;
     const auto launch = d->residual_type == PURO_TYPE_BF16

@@ -49,6 +49,9 @@ def gate_of(kind, rows, cols, seed):
 AXES = {"none": None, "channel": 0, "token": 1, "full": ()}
 SIZES = [(1, 1), (1, 2048), (3, 7), (37, 100), (5, 128), (130, 129), (33, 256), (9, 500),
          (17, 1000), (70, 2051), (261, 2048), (6, 5120), (4, 8191), (3, 8200), (2, 16384)]
+# rows of three to fourteen groups of columns, several to a block, and blocks of unequal length
+GROUPED = [(5, 300), (9001, 384), (2500, 600), (3777, 768), (1700, 896), (2311, 1152), (1, 1200),
+           (1303, 1280), (1111, 1600), (1040, 1792)]
 
 
 # ------------------------------------------------------------------ 8-bit checkpoints
@@ -175,7 +178,7 @@ def check_fwd(puro, rows, cols, res, kind, n, ckpt, pow2, half="both", inplace=F
     return o
 
 
-@pytest.mark.parametrize("rows,cols", SIZES)
+@pytest.mark.parametrize("rows,cols", SIZES + GROUPED)
 @pytest.mark.parametrize("res", [BF16, F32])
 def test_norm_fwd_sizes(puro, rows, cols, res):
     check_fwd(puro, rows, cols, res, "channel", "both", True, False)
@@ -242,7 +245,7 @@ def check_bwd(o, v, e, res, kind):
         ref.close(o.dgate, v["dgate"], e["dgate"] + extra, "dgate")
 
 
-@pytest.mark.parametrize("rows,cols", SIZES + [(3000, 64), (2100, 2048)])
+@pytest.mark.parametrize("rows,cols", SIZES + GROUPED + [(3000, 64), (2100, 2048)])
 @pytest.mark.parametrize("res,saved", [(BF16, "fp8"), (F32, "asis")])
 def test_norm_bwd_sizes(puro, rows, cols, res, saved):
     say("norm bwd", rows, cols, res, saved)
