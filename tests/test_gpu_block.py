@@ -107,6 +107,29 @@ def test_special_values(puro, dtype, pow2):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_both_ends_of_the_range(puro, dtype, pow2):
+    """Groups up to the largest finite values and down to subnormal ones, by themselves and mixed."""
+    x = rnd((130, 260), 12).cpu()
+    x[0] *= 2.0 ** 125
+    x[1] = torch.finfo(dtype).max
+    x[2, ::2], x[2, 1::2] = torch.finfo(dtype).max, 2.0 ** -130
+    x[3] *= 2.0 ** -127
+    x[4] = 2.0 ** -133
+    x[5] *= 2.0 ** -119
+    x[6, 7] = -torch.finfo(dtype).max
+    x = x.to(dtype).to(DEV)
+    q, s = puro.puro_ckpt_pack(x, pow2=pow2)
+    rq, rs = ref.encode(x, pow2)
+    assert same(s, rs) and same(q, rq)
+    qt, st = puro.puro_ckpt_transpose(q, s, pow2=pow2)
+    tq, ts = ref.encode(ref.decode32(q, s).t().contiguous(), pow2)
+    assert same(st, ts)
+    m = (tq & 0x7F) == 0x7F
+    assert torch.equal(qt.cpu()[~m], tq[~m]) and torch.equal(qt.cpu()[m] & 0x7F, tq[m] & 0x7F)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("off", [0, 1, 3, 8])
 def test_strided_rows(puro, dtype, off):
     """Rows inside a wider matrix at any element offset; what lies around them stays."""
@@ -458,6 +481,41 @@ def test_swiglu_bwd_fp8_nonfinite(puro, rows, f, value):
     zero[130, 9] = 0.0
     z = puro.puro_swiglu_bwd_fp8(zero, gu)
     assert same(b.dgus, z.dgus) and same(b.dguts, z.dguts)
+
+
+# ------------------------------------------------------------------ large offsets
+def test_rows_past_32_bits(puro):
+    """2.2e9 elements a tensor: the last rows come out as those of a small matrix."""
+    rows, cols, n = (1 << 20) + 5, 2100, 300
+
+    def big(small):
+        x = torch.empty((rows, cols), dtype=small.dtype, device=DEV)
+        x.fill_(0.5)
+        x[-n:] = small
+        return x
+
+    y, r, dn = acts(n, cols, 1), acts(n, cols, 2), acts(n, cols, 3, BF16, 1e-3)
+    wo, wp = rnd((cols,), 4), rnd((cols,), 5)
+    a = puro.puro_block_norm_fwd(y, r, wo, wp)
+    b = puro.puro_block_norm_fwd(big(y), big(r), wo, wp)
+    for k in ("r_out", "nq", "rstd_y", "rstd_r", "yq", "rq"):
+        assert same(getattr(a, k), getattr(b, k)[-n:]), k
+    for k in ("ns", "ys", "rs"):
+        assert same(getattr(a, k), getattr(b, k)[:, -n:]), k
+    ga = puro.puro_block_norm_bwd(r, dn, (a.yq, a.ys), (a.rq, a.rs), a.rstd_y, a.rstd_r, wo, wp)
+    gb = puro.puro_block_norm_bwd(big(r), big(dn), (b.yq, b.ys), (b.rq, b.rs), b.rstd_y, b.rstd_r,
+                                  wo, wp)
+    assert same(ga.dr, gb.dr[-n:]) and same(ga.dy, gb.dy[-n:])
+    del b, gb
+    torch.cuda.empty_cache()
+    gu, dh = y, dn[:, :cols // 2].contiguous()
+    wide = torch.empty((rows, cols // 2), dtype=BF16, device=DEV)
+    wide.fill_(0.5)
+    wide[-n:] = dh
+    ha, hb = puro.puro_swiglu_fwd(gu), puro.puro_swiglu_fwd(big(gu))
+    assert same(ha.hq, hb.hq[-n:]) and same(ha.guq, hb.guq[-n:]) and same(ha.gus, hb.gus[:, -n:])
+    assert same(puro.puro_swiglu_bwd(dh, (ha.guq, ha.gus)),
+                puro.puro_swiglu_bwd(wide, (hb.guq, hb.gus))[-n:])
 
 
 # ------------------------------------------------------------------ how they are called
