@@ -283,7 +283,7 @@ class _Spec:
         self.code = "".join(c for _, c in pairs).encode()
 
     def pointers(self, dev, d0, d1, d2, *tensors):
-        p = (_native or _load_native())(self.code, dev.index, d0, d1, d2, *tensors)
+        p = (_native or _load_native()).ptrs(self.code, dev.index, d0, d1, d2, *tensors)
         if type(p) is not int:
             return p
         kind, need, *dims = self.code[4 * p:4 * p + 4].decode()
@@ -295,18 +295,32 @@ class _Spec:
         raise PuroError(f"{name}: not as expected")
 
 
-_native = None  # ptrs() of the native checks
+# The module of native checks and calls. Its calls return the entry point's status, or None for
+# arguments that are not as they must be: then the binding's own checks say which.
+_native = None
 
 
 def _load_native():
     global _native
     try:
-        from ._args import ptrs
+        from . import _args
     except ImportError as e:
         raise PuroError("the binding's native checks are not built (%s); run `python -m "
                         "blockwise_fp8_gemm_x128_amd.build`" % e) from e
-    _native = ptrs
-    return ptrs
+    _args.bind(_raw_stream or (lambda i: torch.cuda.current_stream(i).cuda_stream),
+               *(ctypes.cast(getattr(lib(), "puro_" + name), ctypes.c_void_p).value
+                 for name in ("ckpt_pack", "ckpt_unpack", "ckpt_transpose", "block_norm_fwd",
+                              "block_norm_workspace", "block_norm_bwd", "swiglu_fwd", "swiglu_bwd",
+                              "swiglu_bwd_fp8")))
+    _native = _args
+    return _args
+
+
+def _done(st) -> bool:
+    """Whether a native call was made; raises its error."""
+    if st:
+        check(st)
+    return st is not None
 
 
 def _call(name, *args) -> None:
@@ -362,12 +376,14 @@ _TRANSPOSE = _Spec("checkpoint:q!01 scales:f!20 qt:q!10")
 def puro_ckpt_pack(x: torch.Tensor, q=None, s=None, pow2: bool = False):
     """8-bit checkpoint of x, bf16 or fp32 [rows, cols] (any sizes, rows may be strided) ->
     (q uint8 E4M3 [rows, cols], s fp32 [ceil(cols/128), rows])."""
+    if q is None or s is None:
+        new = _new_codes(*_matrix(x, "x"), _dev(x))
+        q, s = new[0] if q is None else q, new[1] if s is None else s
+    if _done((_native or _load_native()).ckpt_pack(x, q, s, pow2)):
+        return q, s
     dev = _dev(x)
     kind, ld = _need_rows(x, "x", dev)
     rows, cols = x.shape
-    if q is None or s is None:
-        new = _new_codes(rows, cols, dev)
-        q, s = new[0] if q is None else q, new[1] if s is None else s
     p = _PACK.pointers(dev, rows, cols, _groups(cols), q, s)
     _call("puro_ckpt_pack", x.data_ptr(), kind, rows, cols, ld, bool(pow2), *p, _stream(dev))
     return q, s
@@ -376,10 +392,12 @@ def puro_ckpt_pack(x: torch.Tensor, q=None, s=None, pow2: bool = False):
 def puro_ckpt_unpack(q, s, x=None, dtype=torch.bfloat16):
     """The values a checkpoint stands for, as `dtype` (bf16 or fp32) or into x (rows may be
     strided)."""
+    if x is None:
+        x = torch.empty(_matrix(q, "checkpoint"), dtype=dtype, device=_dev(q))
+    if _done((_native or _load_native()).ckpt_unpack(q, s, x)):
+        return x
     dev = _dev(q)
     rows, cols = _matrix(q, "checkpoint")
-    if x is None:
-        x = torch.empty((rows, cols), dtype=dtype, device=dev)
     kind, ld = _need_rows(x, "x", dev)
     if x.shape != (rows, cols):
         raise PuroError(f"x: shape {tuple(x.shape)}, expected {(rows, cols)}")
@@ -391,11 +409,14 @@ def puro_ckpt_unpack(q, s, x=None, dtype=torch.bfloat16):
 def puro_ckpt_transpose(q, s, qt=None, st=None, pow2: bool = False):
     """Checkpoint [rows, cols] -> checkpoint of its transpose (qt uint8 [cols, rows], st fp32
     [ceil(rows/128), cols]): a forward GEMM operand becomes the weight gradient's."""
+    if qt is None or st is None:
+        rows, cols = _matrix(q, "checkpoint")
+        new = _new_codes(cols, rows, _dev(q))
+        qt, st = new[0] if qt is None else qt, new[1] if st is None else st
+    if _done((_native or _load_native()).ckpt_transpose(q, s, qt, st, pow2)):
+        return qt, st
     dev = _dev(q)
     rows, cols = _matrix(q, "checkpoint")
-    if qt is None or st is None:
-        new = _new_codes(cols, rows, dev)
-        qt, st = new[0] if qt is None else qt, new[1] if st is None else st
     p = _TRANSPOSE.pointers(dev, rows, cols, _groups(cols), q, s, qt)
     _need(st, "st", torch.float32, (_groups(rows), cols), dev)
     _call("puro_ckpt_transpose", p[0], p[1], rows, cols, bool(pow2), p[2], st.data_ptr(),
@@ -468,15 +489,11 @@ def puro_block_norm_fwd(y, r, w_post, w_pre, gate=None, alpha: float = 1.0, beta
     GEMM's operand), "bf16" or "both"; `ckpt`: also 8-bit checkpoints of y and r_out. `out`: the
     ten outputs to write (a BlockNorm or a tuple in its order, None to leave one out) instead of
     new ones; out.r_out may be r."""
-    dev = _dev(r)
-    rows, cols = _matrix(r, "r")
-    dtype = r.dtype
-    if dtype not in _TYPES:
-        raise PuroError("r: expected bf16 or fp32")
-    kind = _gate_kind(gate)
     if out is None:
         if n not in ("fp8", "bf16", "both"):
             raise PuroError("n: expected 'fp8', 'bf16' or 'both'")
+        dev = _dev(r)
+        rows, cols = _matrix(r, "r")
         post, pre, none, f32 = y is not None, w_pre is not None, (None, None), torch.float32
         out = BlockNorm(
             torch.empty_like(r) if post or beta != 1.0 else None,
@@ -489,6 +506,15 @@ def puro_block_norm_fwd(y, r, w_post, w_pre, gate=None, alpha: float = 1.0, beta
             *(_new_codes(rows, cols, dev) if ckpt else none))
     elif type(out) is not BlockNorm:
         out = BlockNorm(*out)
+    if _done((_native or _load_native()).norm_fwd(y, r, w_post, w_pre, gate, alpha, beta, eps,
+                                                  pow2, out)):
+        return out
+    dev = _dev(r)
+    rows, cols = _matrix(r, "r")
+    dtype = r.dtype
+    if dtype not in _TYPES:
+        raise PuroError("r: expected bf16 or fp32")
+    kind = _gate_kind(gate)
     p = _NORM_FWD[dtype, kind].pointers(dev, rows, cols, (cols + 127) // 128, y, r,
                                         None if y is None else w_post, w_pre, gate, *out)
     _call("puro_block_norm_fwd", _NORM.pack(rows, cols, _TYPES[dtype], kind, bool(pow2), alpha,
@@ -515,6 +541,14 @@ def block_norm_workspace(rows: int, cols: int, dev) -> torch.Tensor:
     return torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
 
 
+def _residual(dr_out, r_out, dr):
+    """The residual stream's type in a backward call."""
+    for t in (dr_out, r_out, dr):
+        if isinstance(t, torch.Tensor):
+            return t.dtype
+    return torch.bfloat16
+
+
 def puro_block_norm_bwd(dr_out, dn, y, r_out, rstd_y, rstd_r, w_post, w_pre, gate=None,
                         alpha: float = 1.0, beta: float = 1.0, accumulate: bool = False,
                         workspace=None, out=None) -> BlockNormGrads:
@@ -523,29 +557,34 @@ def puro_block_norm_bwd(dr_out, dn, y, r_out, rstd_y, rstd_r, w_post, w_pre, gat
     (codes, scales) pairs; rstd_y None: the norm after the block was left out. accumulate adds
     dw_post, dw_pre and a channel gate's gradient to `out`'s. `out`: the five outputs to write
     (None to skip; out.dr may be dr_out)."""
-    post, pre = rstd_y is not None, dn is not None
     lead = dr_out if dr_out is not None else dn
     if lead is None:
         raise PuroError("dr_out and dn: at least one is required")
-    dev = _dev(lead)
-    rows, cols = _matrix(lead, "dr_out")
-    res = (dr_out.dtype if dr_out is not None else
-           r_out.dtype if isinstance(r_out, torch.Tensor) else
-           out[0].dtype if out is not None and out[0] is not None else torch.bfloat16)
-    if res not in _TYPES:
-        raise PuroError("dr_out: expected bf16 or fp32")
-    kind = _gate_kind(gate)
-    saved = *_saved(y, "y", post), *_saved(r_out, "r_out", pre)
+    post, pre = rstd_y is not None, dn is not None
     if out is None:
         if accumulate:
             raise PuroError("accumulate=True needs existing gradients in out")
+        dev = _dev(lead)
+        rows, cols = _matrix(lead, "dr_out")
         vec = lambda: torch.empty((cols,), dtype=torch.float32, device=dev)  # noqa: E731
-        out = BlockNormGrads(torch.empty((rows, cols), dtype=res, device=dev),
+        out = BlockNormGrads(torch.empty((rows, cols), dtype=_residual(dr_out, r_out, None),
+                                         device=dev),
                              torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
                              if post else None, vec() if post else None, vec() if pre else None,
                              torch.empty_like(gate) if gate is not None else None)
     elif type(out) is not BlockNormGrads:
         out = BlockNormGrads(*out)
+    if _done((_native or _load_native()).norm_bwd(dr_out, dn, y, r_out, rstd_y, rstd_r, w_post,
+                                                  w_pre, gate, alpha, beta, accumulate, workspace,
+                                                  out)):
+        return out
+    dev = _dev(lead)
+    rows, cols = _matrix(lead, "dr_out")
+    res = _residual(dr_out, r_out, out[0])
+    if res not in _TYPES:
+        raise PuroError("dr_out: expected bf16 or fp32")
+    kind = _gate_kind(gate)
+    saved = *_saved(y, "y", post), *_saved(r_out, "r_out", pre)
     p = _NORM_BWD[res, kind].pointers(
         dev, rows, cols, (cols + 127) // 128, dr_out, dn, *saved, rstd_y, rstd_r if pre else None,
         w_post if post else None, w_pre if pre else None, gate, *out)
@@ -593,13 +632,10 @@ def puro_swiglu_fwd(gu, h: bool = False, fp8: bool = True, ckpt: bool = True, po
     """h = u g sigmoid(g) from gu = [g | u], bf16 [rows, 2f]. `h`: h in bf16; `fp8`: h as the down
     projection's operand; `ckpt`: an 8-bit checkpoint of gu. `out`: the five outputs to write
     (None to leave one out) instead of new ones."""
-    dev = _dev(gu)
-    rows, cols = _matrix(gu, "gu")
-    if cols % 2:
-        raise PuroError(f"gu: {cols} columns, expected an even number (g and u)")
-    f, k = cols // 2, (cols // 2 + 127) // 128
     if out is None:
-        none = (None, None)
+        dev = _dev(gu)
+        rows, cols = _matrix(gu, "gu")
+        f, k, none = cols // 2, (cols // 2 + 127) // 128, (None, None)
         out = SwiGLU(torch.empty((rows, f), dtype=torch.bfloat16, device=dev) if h else None,
                      *(_new_codes(rows, f, dev) if fp8 else none),
                      *((torch.empty((rows, cols), dtype=FP8, device=dev),
@@ -607,6 +643,13 @@ def puro_swiglu_fwd(gu, h: bool = False, fp8: bool = True, ckpt: bool = True, po
                        if ckpt else none))
     elif type(out) is not SwiGLU:
         out = SwiGLU(*out)
+    if _done((_native or _load_native()).swiglu_fwd(gu, pow2, out)):
+        return out
+    dev = _dev(gu)
+    rows, cols = _matrix(gu, "gu")
+    if cols % 2:
+        raise PuroError(f"gu: {cols} columns, expected an even number (g and u)")
+    f, k = cols // 2, (cols // 2 + 127) // 128
     p, ph, hq, guq = _SWIGLU_FWD.pointers(dev, rows, f, cols, gu, out[0], out[1], out[3])
     hs, gus = _GU_SCALES.pointers(dev, rows, k, 2 * k, out[2], out[4])
     _call("puro_swiglu_fwd", p, rows, f, ph, hq, hs, guq, gus, bool(pow2), _stream(dev))
@@ -616,10 +659,13 @@ def puro_swiglu_fwd(gu, h: bool = False, fp8: bool = True, ckpt: bool = True, po
 def puro_swiglu_bwd(dh, gu, dgu=None):
     """dgu bf16 [rows, 2f] from dh bf16 [rows, f] and gu: bf16 [rows, 2f], or its checkpoint as a
     (codes, scales) pair."""
+    if dgu is None:
+        rows, f = _matrix(dh, "dh")
+        dgu = torch.empty((rows, 2 * f), dtype=torch.bfloat16, device=_dev(dh))
+    if _done((_native or _load_native()).swiglu_bwd(dh, gu, dgu)):
+        return dgu
     dev = _dev(dh)
     rows, f = _matrix(dh, "dh")
-    if dgu is None:
-        dgu = torch.empty((rows, 2 * f), dtype=torch.bfloat16, device=dev)
     x, q, s = _saved(gu, "gu", True)
     p = _SWIGLU_BWD.pointers(dev, rows, f, 2 * f, dh, x, q, dgu)
     ps = 0
@@ -634,15 +680,19 @@ def puro_swiglu_bwd_fp8(dh, gu, pow2: bool = False, out=None) -> SwiGLUOperands:
     """puro_swiglu_bwd straight to the FP8 operands of gate_up's data and weight gradients, and
     h's transposed copy for down's weight gradient. rows and f: multiples of 128. `out`: the six
     outputs to write instead of new ones."""
-    dev = _dev(dh)
-    rows, f = _matrix(dh, "dh")
-    if rows % 128 or f % 128:
-        raise PuroError(f"dh: shape {(rows, f)}, expected multiples of 128")
     if out is None:
+        dev = _dev(dh)
+        rows, f = _matrix(dh, "dh")
         out = SwiGLUOperands(*_new_codes(rows, 2 * f, dev), *_new_codes(2 * f, rows, dev),
                              *_new_codes(f, rows, dev))
     elif type(out) is not SwiGLUOperands:
         out = SwiGLUOperands(*out)
+    if _done((_native or _load_native()).swiglu_bwd_fp8(dh, gu, pow2, out)):
+        return out
+    dev = _dev(dh)
+    rows, f = _matrix(dh, "dh")
+    if rows % 128 or f % 128:
+        raise PuroError(f"dh: shape {(rows, f)}, expected multiples of 128")
     x, q, s = _saved(gu, "gu", True)
     p = _SWIGLU_FP8.pointers(dev, rows, f, 2 * f, dh, x, q, out[0], out[2], out[4])
     gus, dgus = _FP8_SCALES.pointers(dev, rows, f, f // 64, s, out[1])

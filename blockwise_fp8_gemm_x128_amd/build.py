@@ -19,7 +19,7 @@ SOURCES = ["abi.hip", "quant.hip", "gemm.hip", "optim.hip", "debug.hip", "norm.h
 # GEMM path.
 PROBE_PATH = os.path.join(PKG_DIR, "libpuro_probe.so")
 PROBE_SOURCES = ["ceiling.hip"]
-# The Python binding's native argument checks: host code against torch's headers.
+# The Python binding's native half: host code against torch's headers.
 ARGS_PATH = os.path.join(PKG_DIR, "_args.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -65,8 +65,8 @@ def _args(verbose: bool) -> str:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
            *("-I" + p for p in cpp_extension.include_paths("cpu")),
-           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "args.cpp"), "-L" + lib,
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+           "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE,
+           os.path.join(CSRC, "args.cpp"), "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
