@@ -269,3 +269,25 @@ def test_binding_refuses_sparse_tensors():
         puro._PACK.pointers(dev, 4, 8, 1, q, None)
     with pytest.raises(PuroError, match="x: expected a bf16 or fp32 matrix"):
         puro._need_rows(torch.zeros((4, 8)).to_sparse_csr(), "x", dev)
+
+
+def test_native_calls_leave_what_they_do_not_take():
+    """Nothing but tensors on the device in their places is taken: the native calls return None,
+    without an exception, and the binding's own checks then say what was wrong."""
+    from blockwise_fp8_gemm_x128_amd import binding as puro
+    nat = puro._load_native()
+    x, none = torch.zeros((4, 8), dtype=torch.bfloat16), (None,)
+    csr = torch.zeros((4, 8), dtype=torch.uint8).to_sparse_csr()
+    for bad in (x, csr, None, 3, "x", (x, x)):
+        assert nat.ckpt_pack(bad, x, x, False) is None
+        assert nat.ckpt_unpack(bad, x, x) is None
+        assert nat.ckpt_transpose(bad, x, x, x, False) is None
+        assert nat.norm_fwd(x, bad, x, x, None, 1.0, 1.0, 1e-6, False, none * 10) is None
+        assert nat.norm_bwd(bad, x, x, x, x, x, x, x, None, 1.0, 1.0, False, None, none * 5) is None
+        assert nat.swiglu_fwd(bad, False, none * 5) is None
+        assert nat.swiglu_bwd(bad, (x, x), x) is None
+        assert nat.swiglu_bwd_fp8(bad, (x, x), False, none * 6) is None
+    assert nat.ckpt_pack(x) is None                      # too few arguments
+    assert nat.swiglu_fwd(x, False, none) is None        # too few outputs
+    with pytest.raises(TypeError):
+        nat.bind(None)

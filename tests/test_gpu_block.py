@@ -526,6 +526,39 @@ def test_results_repeat(puro):
         assert same(x, y)
 
 
+def test_native_calls_and_checked_calls_agree(puro, monkeypatch):
+    """The binding's one-step native call and its way around it, argument by argument, make the same
+    call: also taken for what the native one leaves alone (a list for a pair, 1 for True)."""
+    rows, f, cols = 256, 384, 1024
+    y, r, w = acts(rows, cols, 1), acts(rows, cols, 2, F32), rnd((cols,), 3)
+    gu, dh = gu_of(rows, f), acts(rows, f, 43, BF16, 1e-3)
+    d = bwd_inputs(puro, rows, cols, BF16, "token", "fp8")
+
+    def calls(as_pair, flag):
+        a = puro.puro_block_norm_fwd(y, r, w, w, rnd((rows, 1), 4), 0.5, 0.25, 1e-5, n="both",
+                                     pow2=flag)
+        h = puro.puro_swiglu_fwd(gu, h=True, pow2=flag)
+        pair = as_pair((h.guq, h.gus))
+        e = dict(d, y=as_pair(d["y"]), t=as_pair(d["t"]))
+        g = bwd_call(puro, e, 0.75, 0.9375)
+        g2 = bwd_call(puro, dict(e, dro=None), 0.75, 0.9375, accumulate=flag, out=g._replace(
+            **{k: getattr(g, k).clone() for k in g._fields}))
+        q, s = puro.puro_ckpt_pack(r[:, 5:900], pow2=flag)
+        return (*a, *h, *g, *g2, puro.puro_swiglu_bwd(dh, pair),
+                *puro.puro_swiglu_bwd_fp8(dh, pair, pow2=flag), q, s,
+                puro.puro_ckpt_unpack(q, s, dtype=F32), *puro.puro_ckpt_transpose(q, s, pow2=flag))
+
+    native = calls(tuple, True)
+    made = []
+    real = puro._call
+    monkeypatch.setattr(puro, "_call", lambda name, *a: (made.append(name), real(name, *a))[1])
+    assert len(native) == len(calls(tuple, True)) and not made
+    checked = calls(list, 1)
+    assert len(made) >= 8
+    for a, b in zip(native, checked):
+        assert same(a, b)
+
+
 def test_other_stream_and_graph(puro):
     """The calls run on torch's current stream and can be captured; replays, with eager work
     between them, give the eager bytes."""
