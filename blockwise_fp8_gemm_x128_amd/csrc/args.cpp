@@ -1,7 +1,7 @@
-// The Python binding's native half, for the operators between the GEMMs: a call's tensors (up to 18)
-// are checked against the types, shapes, contiguity and device they must have and handed to the C
-// entry point in one step. Asked through the interpreter the same questions take a forward norm's
-// host time from 7 us to 17.
+// The Python binding's native half, for the operators between the GEMMs: a call's tensors (up to
+// 18) are checked against the types, shapes, contiguity and device they must have and handed to the
+// C entry point in one step. A forward norm's host time is 5.4 us, 3 of it the launch; with the same
+// questions asked through the interpreter it was 17.
 //
 //   ptrs(spec, device, d0, d1, d2, *tensors) -> tuple of addresses, or the index of the first
 //                                               tensor that is not as the specification says
@@ -366,7 +366,8 @@ PyObject* swiglu_bwd(PyObject* const* a) {   // dh, gu, dgu
   });
 }
 
-PyObject* swiglu_bwd_fp8(PyObject* const* a) {   // dh, gu, pow2, (dguq, dgus, dgutq, dguts, htq, hts)
+PyObject* swiglu_bwd_fp8(PyObject* const* a) {
+  // dh, gu, pow2, (dguq, dgus, dgutq, dguts, htq, hts)
   Call c(a[0]);
   if (!c.ok || c.rows % 128 != 0 || c.cols % 128 != 0 || !outputs(a[3], 6)) Py_RETURN_NONE;
   const int64_t rows = c.rows, f = c.cols;

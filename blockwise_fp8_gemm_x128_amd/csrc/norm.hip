@@ -684,8 +684,8 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const ReduceArgs a) {
 
 // ------------------------------------------------------------------ host side
 // How a row is laid over lanes: 16, 32 or 64 lanes of 8 columns up to 512 columns, then whole
-// waves, one vector per lane up to 8192 columns and two beyond; or, up to 2048 columns, groups of
-// 16 lanes in a block of `least` to `most` threads.
+// waves, one vector per lane up to a number of columns and two beyond; or, up to 2048 columns,
+// groups of 16 lanes in a block of `least` to `most` threads.
 struct Shape {
   int lanes;     // 16, 32, 64, kOne, kGroups or kWaves
   int nv;        // vectors of 8 columns per lane
@@ -695,8 +695,13 @@ struct Shape {
 };
 struct Blocks {
   int threads, least, most;   // of several teams; of groups
+  int one;                    // vectors of the longest row with one per lane
 };
-constexpr Blocks kFwdBlocks = {256, 192, 320}, kBwdBlocks = {512, 256, 448};
+// Forward, rows of more than twelve waves leave room for one block per CU, whose phases nothing
+// overlaps: two vectors per lane there make two blocks, 4096 x 7168 in 57.3 us instead of 64.0, 8192
+// columns 64.1 instead of 66.0; but 5120 columns 51.4 instead of 40.3. Backward the second vector
+// does not fit the registers: 8192 columns in 117 us instead of 69.
+constexpr Blocks kFwdBlocks = {256, 192, 320, 768}, kBwdBlocks = {512, 256, 448, 1024};
 
 // Groups are taken where they leave fewer lanes idle, and at most one in twelve. They cost vector
 // registers for addresses and a reduction across waves. In 16.8 M elements with checkpoints rows of
@@ -724,7 +729,7 @@ Shape shape_of(int64_t cols, const Blocks& b) {
     s.teams = s.threads / std::max(s.lanes, 16);
     return s;
   }
-  s.nv = vecs <= 1024 ? 1 : 2;
+  s.nv = vecs <= b.one ? 1 : 2;
   s.wpt = static_cast<int>(ceil_div(vecs, 64 * s.nv));
   s.teams = std::max(1, b.threads / (64 * s.wpt));
   s.threads = 64 * s.wpt * s.teams;

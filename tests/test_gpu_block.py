@@ -49,9 +49,10 @@ def gate_of(kind, rows, cols, seed):
 AXES = {"none": None, "channel": 0, "token": 1, "full": ()}
 SIZES = [(1, 1), (1, 2048), (3, 7), (37, 100), (5, 128), (130, 129), (33, 256), (9, 500),
          (17, 1000), (70, 2051), (261, 2048), (6, 5120), (4, 8191), (3, 8200), (2, 16384)]
-# rows of three to fourteen groups of columns, several to a block, and blocks of unequal length
+# rows of three to fourteen groups of columns and of many waves, several to a block, and blocks of
+# unequal length
 GROUPED = [(5, 300), (9001, 384), (2500, 600), (3777, 768), (1700, 896), (2311, 1152), (1, 1200),
-           (1303, 1280), (1111, 1600), (1040, 1792)]
+           (1303, 1280), (1111, 1600), (1040, 1792), (600, 7100)]
 
 
 # ------------------------------------------------------------------ 8-bit checkpoints
@@ -109,7 +110,7 @@ def test_special_values(puro, dtype, pow2):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("pow2", [False, True])
 def test_both_ends_of_the_range(puro, dtype, pow2):
-    """Groups up to the largest finite values and down to subnormal ones, by themselves and mixed."""
+    """Groups up to the largest finite values and down to subnormal ones, alone and mixed."""
     x = rnd((130, 260), 12).cpu()
     x[0] *= 2.0 ** 125
     x[1] = torch.finfo(dtype).max
