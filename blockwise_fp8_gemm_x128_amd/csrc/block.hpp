@@ -35,7 +35,8 @@ __device__ __forceinline__ uint32_t xcd_range(uint32_t b, uint32_t n) {
 
 // The elementwise kernels' block of 256 threads: 16 lane groups of 16, each on one 128-column chunk
 // of a row; two chunks side by side, eight rows a pass, two passes with all their loads issued
-// first. Measured on MI355X against 1, 4, 8 and 16 chunks and 1 and 4 passes: 16384 x 2048 fp32
+// first. Measured on MI355X, all stores through the caches (past them, as now, the same calls take
+// 29.7, 55.3 and 7.0 us), against 1, 4, 8 and 16 chunks and 1 and 4 passes: 16384 x 2048 fp32
 // packed in 30.3 us (30.8 to 35.2), the activation of 8192 x 6144 in 63.9 us (67 to 74.5), 2047 x
 // 4111 unpacked in 7.1 us (7 to 9.8). Ranges per XCD: 4000 x 5003 packed in 12.4 us against 14.9,
 // but 8192 x 6144 activated in 67.5 against 63.9, so only rows off the 128 B lines take them.
@@ -246,8 +247,8 @@ __device__ __forceinline__ void values(Fp8x8 r, const Span<kShort>& s, float sca
 // and one element. kLater: nobody reads the output soon (a checkpoint waits for the backward pass,
 // the residual stream for the end of the next block): it goes past the caches, which keep what the
 // next kernel reads. Measured on MI355X over rotating buffers: the activation of 8192 x 6144 with
-// its checkpoint 63.8 -> 55.4 us, the block norm of 4096 x 8192 72 -> 66.5 us forward and 78 -> 69
-// backward, of 8192 x 2048 33.3 -> 32.2 and 37.6 -> 38.2.
+// its checkpoint 63.8 -> 55.4 us, the block norm of 4096 x 8192 72 -> 66.5 us forward (63.8 with
+// two vectors per lane) and 78 -> 69 backward, of 8192 x 2048 33.3 -> 32.2 and 37.6 -> 38.2.
 // (One function per type: a template parameter would lose the pointer's weak alignment.)
 template <bool kLater>
 __device__ __forceinline__ void put(u32x4_el* p, u32x4_el v) {
