@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kTileThreads) void ckpt_transpose_kernel(
 
 puro_status check_rows(int64_t rows, int64_t cols, int64_t* blocks) {
   *blocks = row_tiles(rows, cols);
-  return *blocks > INT32_MAX ? PURO_ERR_SHAPE : PURO_OK;
+  return grid_ok(*blocks, 256) ? PURO_OK : PURO_ERR_SHAPE;
 }
 
 // The 16- or 32-bit side of a checkpoint: any row stride from cols up, element-aligned.
@@ -182,7 +182,7 @@ extern "C" puro_status puro_ckpt_transpose(const void* q, const float* s, int64_
   PURO_TRY(check_ptr(st, empty));
   if (empty) return PURO_OK;
   const int64_t blocks = ceil_div(rows, 128) * ceil_div(cols, 128);
-  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(blocks, kTileThreads)) return PURO_ERR_SHAPE;
   const auto k = cols < kVec ? ckpt_transpose_kernel<true> : ckpt_transpose_kernel<false>;
   hipLaunchKernelGGL(k, dim3(static_cast<uint32_t>(blocks)),
                      dim3(kTileThreads), 0, static_cast<hipStream_t>(stream),

@@ -9,8 +9,8 @@ namespace puro {
 
 // ---------------------------------------------------------------- host-side validation
 constexpr int64_t kGroup = 128;
-// Largest accepted dimension; keeps every element offset far inside int64 and every grid
-// inside hipLaunchKernel's 32-bit limits.
+// Largest accepted dimension; keeps every element offset far inside int64. (A grid has a limit of
+// its own, grid_ok.)
 constexpr int64_t kMaxDim = int64_t(1) << 24;
 
 inline bool dim_ok(int64_t d) { return d >= 0 && d <= kMaxDim && d % kGroup == 0; }
@@ -22,6 +22,13 @@ inline puro_status check_ptr(const void* p, bool empty) {
   if (p == nullptr) return PURO_ERR_NULL;
   if (!aligned16(p)) return PURO_ERR_ALIGN;
   return PURO_OK;
+}
+
+// Whether a launch of `blocks` blocks along x runs all of them. The runtime counts a launch's threads
+// in 32 bits and takes a larger one for what is left of it: of 2^24 + 5 blocks of 256 threads five
+// ran on MI355X, without an error.
+inline bool grid_ok(int64_t blocks, int64_t threads) {
+  return blocks <= INT32_MAX && blocks * threads <= int64_t(UINT32_MAX);
 }
 
 inline puro_status launch_status() {

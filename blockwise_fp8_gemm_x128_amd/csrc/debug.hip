@@ -156,7 +156,7 @@ puro_status check_bf16(const void* x, int64_t rows, int64_t cols, int groups, bo
   if (rows == 0 || cols == 0 || !on()) return PURO_OK;
   std::lock_guard<std::mutex> lock(g_mutex);
   const int64_t tiles = (rows / 128) * (cols / 128);
-  if (tiles > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(tiles, 128)) return PURO_ERR_SHAPE;
   return run_check(stream, [&](hipStream_t st, uint32_t* flags) {
     hipLaunchKernelGGL(check_bf16_kernel, dim3(static_cast<uint32_t>(tiles)), dim3(128), 0, st,
                        static_cast<const uint16_t*>(x), rows, cols, groups, pow2 ? 0 : 1,

@@ -1069,7 +1069,7 @@ template <class C>
 puro_status launch(GemmKernel k, const void* A, const float* sA, const void* B, const float* sB,
                    void* Cout, int64_t I, int64_t J, int64_t L, int accumulate, void* stream) {
   const int64_t blocks = ((I + C::BM - 1) / C::BM) * ((J + C::BN - 1) / C::BN);
-  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(blocks, C::kThreads)) return PURO_ERR_SHAPE;
   hipLaunchKernelGGL(k, dim3(static_cast<uint32_t>(blocks)), dim3(C::kThreads), 0,
                      static_cast<hipStream_t>(stream), static_cast<const uint8_t*>(A), sA,
                      static_cast<const uint8_t*>(B), sB, Cout, I, J, L, accumulate);
@@ -1081,7 +1081,7 @@ puro_status launch_k2(GemmKernel k, const void* A, const float* sA, const void* 
                       const float* sB, void* Cout, int64_t I, int64_t J, int64_t L,
                       int accumulate, void* stream) {
   const int64_t blocks = ((I + C::BM - 1) / C::BM) * ((J + C::BN - 1) / C::BN);
-  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(blocks, 2 * C::kThreads)) return PURO_ERR_SHAPE;
   hipLaunchKernelGGL(k, dim3(static_cast<uint32_t>(blocks)), dim3(2 * C::kThreads), 0,
                      static_cast<hipStream_t>(stream), static_cast<const uint8_t*>(A), sA,
                      static_cast<const uint8_t*>(B), sB, Cout, I, J, L, accumulate);

@@ -278,7 +278,7 @@ puro_status quant_act_1x128(const void* x, int64_t rows, int64_t cols, void* q, 
   if (empty) return PURO_OK;
   PURO_TRY(debug::check_bf16(x, rows, cols, debug::kRowGroups, kPow2, stream));
   const int64_t blocks = (rows / kActRowsPerBlock) * (cols / 128);
-  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(blocks, 256)) return PURO_ERR_SHAPE;
   hipLaunchKernelGGL(quant_act_1x128_kernel<kPow2>, dim3(static_cast<uint32_t>(blocks)),
                      dim3(256), 0, static_cast<hipStream_t>(stream),
                      static_cast<const uint16_t*>(x), rows, cols, static_cast<uint8_t*>(q), s);
@@ -296,7 +296,7 @@ puro_status quant_w_128x128(const void* w, int64_t n, int64_t k, void* q, float*
   if (empty) return PURO_OK;
   PURO_TRY(debug::check_bf16(w, n, k, debug::kBlockGroups, kPow2, stream));
   const int64_t blocks = (n / 128) * (k / 128);
-  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(blocks, 256)) return PURO_ERR_SHAPE;
   hipLaunchKernelGGL(quant_w_128x128_kernel<kPow2>, dim3(static_cast<uint32_t>(blocks)),
                      dim3(256), 0, static_cast<hipStream_t>(stream),
                      static_cast<const uint16_t*>(w), n, k, static_cast<uint8_t*>(q), s);
@@ -314,7 +314,7 @@ puro_status quant_transpose(const void* x, int64_t rows, int64_t cols, void* qt,
   if (empty) return PURO_OK;
   PURO_TRY(debug::check_bf16(x, rows, cols, debug::kColGroups, kPow2, stream));
   const int64_t blocks = (rows / 128) * (cols / 128);
-  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(blocks, 512)) return PURO_ERR_SHAPE;
   const auto kernel = quant_dual_1x128_kernel<kPow2, false>;  // column groups only
   hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(blocks)), dim3(512), 0, static_cast<hipStream_t>(stream),
                      static_cast<const uint16_t*>(x), rows, cols, nullptr, nullptr,
@@ -336,7 +336,7 @@ puro_status quant_dual_1x128(const void* x, int64_t rows, int64_t cols, void* q,
   PURO_TRY(debug::check_bf16(x, rows, cols, debug::kRowGroups | debug::kColGroups, kPow2,
                              stream));
   const int64_t blocks = (rows / 128) * (cols / 128);
-  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(blocks, 512)) return PURO_ERR_SHAPE;
   const auto kernel = quant_dual_1x128_kernel<kPow2, true>;
   hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(blocks)), dim3(512), 0, static_cast<hipStream_t>(stream),
                      static_cast<const uint16_t*>(x), rows, cols, static_cast<uint8_t*>(q), s,
@@ -370,7 +370,7 @@ puro_status quant_w_128x128_group(const puro_w_item* items, int count, void* str
     ++used;
   }
   if (used == 0) return PURO_OK;
-  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(blocks, 256)) return PURO_ERR_SHAPE;
   for (int i = 0; i < used; ++i)
     PURO_TRY(debug::check_bf16(g.w[i], g.n[i], g.k[i], debug::kBlockGroups, kPow2, stream));
   g.first[used] = blocks;

@@ -343,7 +343,7 @@ extern "C" puro_status puro_swiglu_fwd(const void* gu, int64_t rows, int64_t f, 
     PURO_TRY(check_ptr(gus, false));
   }
   const int64_t blocks = row_tiles(rows, f);
-  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(blocks, 256)) return PURO_ERR_SHAPE;
   const FwdArgs a = {static_cast<const uint16_t*>(gu), rows, f, static_cast<uint16_t*>(h),
                      static_cast<uint8_t*>(hq), hs, static_cast<uint8_t*>(guq), gus, pow2};
   const auto k = f < kVec ? swiglu_fwd_kernel<true> : swiglu_fwd_kernel<false>;
@@ -362,7 +362,7 @@ extern "C" puro_status puro_swiglu_bwd(const void* dh, const void* gu, const voi
   PURO_TRY(check_ptr(dgu, empty));
   if (empty) return PURO_OK;
   const int64_t blocks = row_tiles(rows, f);
-  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(blocks, 256)) return PURO_ERR_SHAPE;
   const BwdArgs a = {static_cast<const uint16_t*>(dh),
                      {static_cast<const uint16_t*>(gu), static_cast<const uint8_t*>(guq), gus},
                      rows, f, static_cast<uint16_t*>(dgu)};
@@ -389,7 +389,7 @@ extern "C" puro_status puro_swiglu_bwd_fp8(const void* dh, const void* gu, const
     PURO_TRY(check_ptr(p, empty));
   if (empty) return PURO_OK;
   const int64_t blocks = (rows / 128) * (f / 128);
-  if (blocks > INT32_MAX) return PURO_ERR_SHAPE;
+  if (!grid_ok(blocks, kTileThreads)) return PURO_ERR_SHAPE;
   const BwdFp8Args a = {static_cast<const uint16_t*>(dh),
                         {static_cast<const uint16_t*>(gu), static_cast<const uint8_t*>(guq), gus},
                         rows, f, static_cast<uint8_t*>(dguq), dgus, static_cast<uint8_t*>(dgutq),

@@ -25,7 +25,9 @@
  *     synchronises nothing and keeps no state between calls (calls are thread-safe), except in
  *     debug mode (puro_set_debug below), where each call waits for its input checks.
  *   - Every tensor is dense row-major. Tensor pointers must be 16-byte aligned.
- *   - Every dimension must be a multiple of 128 (zero allowed). A call whose output is empty
+ *   - Every dimension must be a multiple of 128 (zero allowed) and at most 2^24, and a call's
+ *     launch must stay below 2^32 threads, which takes tensors of 2^36 elements or more to pass;
+ *     PURO_ERR_SHAPE otherwise. A call whose output is empty
  *     returns PURO_OK and launches nothing. A GEMM whose reduction dimension is 0 writes zeros
  *     (or leaves dW unchanged when accumulating).
  *   - `stream` is a hipStream_t (NULL = the default stream). Work is enqueued asynchronously;
@@ -250,7 +252,9 @@ puro_status puro_fp8_gemm_wgrad_pow2(const void* dytq, const float* sdyt, const 
  * activations that the backward pass reads. They take bf16 activations and gradients, fp32
  * weights and weight gradients, and a residual stream in bf16 or fp32, and write the GEMMs' FP8
  * operands directly. Conventions as above, except where stated: rows and columns here may have
- * any size from 0 to 2^24 (not only multiples of 128), and inputs may hold infinities and NaN.
+ * any size from 0 to 2^24 (not only multiples of 128), and inputs may hold infinities and NaN. The
+ * bound on a launch's threads is reached at 2^36 elements by the checkpoint's packing and unpacking
+ * and by the activation (of h), at 2^37 by the requantisation.
  * Sums and statistics are fp32 and run in an order fixed by the sizes alone, so results repeat
  * exactly.
  *
