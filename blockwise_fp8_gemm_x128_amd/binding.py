@@ -61,6 +61,16 @@ def _out(t, name, dtype, shape, dev):
     return t
 
 
+def _need_workspace(t, need: int, dev) -> None:
+    """Scratch memory of `need` bytes: of a view, the bytes of its elements are not the bytes behind
+    its address (expanded rows share theirs, a stepped view's lie apart)."""
+    if not isinstance(t, torch.Tensor):
+        raise PuroError("workspace: expected a torch.Tensor")
+    if (t.device != dev or t.layout is not torch.strided or not t.is_contiguous()
+            or t.numel() * t.element_size() < need):
+        raise PuroError(f"workspace: {need} contiguous bytes on {dev} needed")
+
+
 def puro_quant_act_1x128(x: torch.Tensor, q=None, s=None, _fn="puro_quant_act_1x128"):
     """x bf16 [rows, cols] -> (q uint8 E4M3 [rows, cols], s fp32 [cols/128, rows])."""
     dev = _dev(x)
@@ -591,8 +601,8 @@ def puro_block_norm_bwd(dr_out, dn, y, r_out, rstd_y, rstd_r, w_post, w_pre, gat
     need = lib().puro_block_norm_workspace(rows, cols)
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or workspace.numel() * workspace.element_size() < need:
-        raise PuroError(f"workspace: {need} bytes on {dev} needed")
+    else:
+        _need_workspace(workspace, need, dev)
     _call("puro_block_norm_bwd", _NORM_GRAD.pack(rows, cols, _TYPES[res], kind, bool(accumulate),
                                                  alpha, beta, *p), workspace.data_ptr(),
           _stream(dev))

@@ -330,8 +330,9 @@ PyObject* norm_bwd(PyObject* const* a) {
     own = at::empty({need > 16 ? need : 16}, c.lead->options().dtype(at::kByte));
     w = &own;
   }
-  c.ok = w != nullptr && w->is_cuda() && w->get_device() == c.device &&
-         w->numel() * w->element_size() >= need;
+  // contiguous: a view's elements may share their bytes, or lie apart
+  c.ok = w != nullptr && w->is_cuda() && w->get_device() == c.device && w->is_contiguous() &&
+         static_cast<int64_t>(w->numel() * w->element_size()) >= need;
   void* ws = c.ok ? const_cast<void*>(w->const_data_ptr()) : nullptr;
   return finish(c, [&](void* st) { return entry.norm_bwd(&d, ws, st); });
 }

@@ -1,0 +1,35 @@
+"""GPU tests of how the operators between the GEMMs are called: what their binding refuses, and
+what it takes for granted."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def rnd(shape, seed, dtype=F32, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std).to(dtype).to(DEV)
+
+
+@pytest.mark.parametrize("make", [
+    lambda n: torch.empty(n - 1, dtype=torch.uint8, device=DEV),
+    lambda n: torch.empty(1, dtype=torch.uint8, device=DEV).expand(n),
+    lambda n: torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2],
+    lambda n: torch.empty(n, dtype=torch.uint8),
+    lambda n: bytearray(n),
+])
+def test_norm_bwd_workspace_views_are_refused(puro, make):
+    """Scratch memory that has fewer bytes behind its address than the kernels write."""
+    from blockwise_fp8_gemm_x128_amd import PuroError
+    rows, cols = 64, 512
+    x, w, rstd = rnd((rows, cols), 1, BF16), rnd((cols,), 2), torch.ones(rows, device=DEV)
+    need = puro.lib().puro_block_norm_workspace(rows, cols)
+    assert need >= 2 * cols * 4
+    args = (x, x, x, x, rstd, rstd, w, w)
+    with pytest.raises(PuroError, match="workspace"):
+        puro.puro_block_norm_bwd(*args, workspace=make(need))
+    a = puro.puro_block_norm_bwd(*args)
+    b = puro.puro_block_norm_bwd(*args, workspace=torch.empty(need // 4, device=DEV))
+    assert all(torch.equal(x, y) for x, y in zip(a, b) if x is not None)
