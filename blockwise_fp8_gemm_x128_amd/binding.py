@@ -213,8 +213,11 @@ def puro_frobenius_norm(w: torch.Tensor, norm=None, workspace=None):
     dev = _dev(w)
     _need(w, "w", torch.float32, tuple(w.shape), dev)
     norm = _out(norm, "norm", torch.float32, (1,), dev)
-    ws = optim_workspace(dev) if workspace is None else workspace
-    check(lib().puro_frobenius_norm(w.data_ptr(), w.numel(), norm.data_ptr(), ws.data_ptr(),
+    if workspace is None:
+        workspace = optim_workspace(dev)
+    else:
+        _need_workspace(workspace, OPT_WORKSPACE_BYTES, dev)
+    check(lib().puro_frobenius_norm(w.data_ptr(), w.numel(), norm.data_ptr(), workspace.data_ptr(),
                                     _stream(dev)))
     return norm
 
@@ -228,9 +231,12 @@ def puro_hyperball_step(w: torch.Tensor, u: torch.Tensor, lr: float, radius: tor
     _need(u, "u", torch.float32, tuple(w.shape), dev)
     _need(radius, "radius", torch.float32, (1,), dev)
     w_bf16 = _out(w_bf16, "w_bf16", torch.bfloat16, tuple(w.shape), dev)
-    ws = optim_workspace(dev) if workspace is None else workspace
+    if workspace is None:
+        workspace = optim_workspace(dev)
+    else:
+        _need_workspace(workspace, OPT_WORKSPACE_BYTES, dev)
     check(lib().puro_hyperball_step(w.data_ptr(), u.data_ptr(), n, float(lr), radius.data_ptr(),
-                                    w_bf16.data_ptr(), ws.data_ptr(), _stream(dev)))
+                                    w_bf16.data_ptr(), workspace.data_ptr(), _stream(dev)))
     return w_bf16
 
 

@@ -33,3 +33,22 @@ def test_norm_bwd_workspace_views_are_refused(puro, make):
     a = puro.puro_block_norm_bwd(*args)
     b = puro.puro_block_norm_bwd(*args, workspace=torch.empty(need // 4, device=DEV))
     assert all(torch.equal(x, y) for x, y in zip(a, b) if x is not None)
+
+
+def test_optimizer_workspace_is_checked(puro):
+    from blockwise_fp8_gemm_x128_amd import PuroError
+    w = rnd((64, 64), 3)
+    whole = puro.optim_workspace(DEV)
+    norm = puro.puro_frobenius_norm(w, workspace=whole)
+    assert torch.equal(norm, puro.puro_frobenius_norm(w))
+    u, radius = rnd((64, 64), 4), norm.clone()
+    before = w.clone()
+    for bad in (whole[:-1], whole[:1].expand(whole.numel()), whole.cpu(), bytearray(whole.numel())):
+        with pytest.raises(PuroError, match="workspace"):
+            puro.puro_frobenius_norm(w, workspace=bad)
+        with pytest.raises(PuroError, match="workspace"):
+            puro.puro_hyperball_step(w, u, 0.1, radius, workspace=bad)
+    assert torch.equal(w, before)
+    puro.puro_hyperball_step(w, u, 0.1, radius, workspace=whole)
+    puro.puro_hyperball_step(before, u, 0.1, radius)
+    assert torch.equal(w, before)
