@@ -25,8 +25,9 @@ FP8 = torch.uint8  # E4M3 codes travel as raw bytes
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(dev: torch.device) -> int:
-    if _raw_stream is not None:
+def _stream(dev: Optional[torch.device]) -> int:
+    """torch's current stream on a tensor's device; None: on the current device."""
+    if _raw_stream is not None and dev is not None:
         return _raw_stream(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
 

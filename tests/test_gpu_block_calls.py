@@ -1,5 +1,5 @@
-"""GPU tests of how the operators between the GEMMs are called: what their binding refuses, and
-what it takes for granted."""
+"""GPU tests of how the binding makes its calls: what it refuses, which stream and which types it
+takes where the arguments leave them open."""
 import pytest
 import torch
 
@@ -52,3 +52,20 @@ def test_optimizer_workspace_is_checked(puro):
     puro.puro_hyperball_step(w, u, 0.1, radius, workspace=whole)
     puro.puro_hyperball_step(before, u, 0.1, radius)
     assert torch.equal(w, before)
+
+
+def test_prepared_group_call_without_a_tensor(puro):
+    """prepare() of a call whose tensors are inside a ctypes array, on the current stream."""
+    ws = [rnd((128, 256), 5, BF16), rnd((256, 128), 6, BF16)]
+    want_q, want_s = puro.puro_quant_w_128x128_group(ws)
+    qs, ss = [torch.zeros_like(q) for q in want_q], [torch.zeros_like(s) for s in want_s]
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for stream in (torch.cuda.current_stream(), st):
+        with torch.cuda.stream(stream):
+            call = puro.prepare("puro_quant_w_128x128_group", puro.w_group_items(ws, qs, ss), 2)
+            for t in (*qs, *ss):
+                t.zero_()
+            call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*qs, *ss), (*want_q, *want_s)))
