@@ -558,22 +558,28 @@ def block_norm_workspace(rows: int, cols: int, dev) -> torch.Tensor:
     return torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
 
 
-def _residual(dr_out, r_out, dr):
-    """The residual stream's type in a backward call."""
-    for t in (dr_out, r_out, dr):
-        if isinstance(t, torch.Tensor):
-            return t.dtype
-    return torch.bfloat16
+def _residual(dr_out, r_out, given):
+    """The residual stream's type in a backward call that makes its own dr: that of the tensors of
+    that type, or, where r_out is a checkpoint and dr_out absent, the one given. It is not guessed:
+    every earlier boundary takes its type from this dr."""
+    known = next((t.dtype for t in (dr_out, r_out) if isinstance(t, torch.Tensor)), given)
+    if known is None:
+        raise PuroError("residual_dtype: required where r_out is a checkpoint and dr_out None "
+                        "(or give out.dr)")
+    if given is not None and (given != known or given not in _TYPES):
+        raise PuroError(f"residual_dtype: {given}, expected {known} (bf16 or fp32)")
+    return known
 
 
 def puro_block_norm_bwd(dr_out, dn, y, r_out, rstd_y, rstd_r, w_post, w_pre, gate=None,
                         alpha: float = 1.0, beta: float = 1.0, accumulate: bool = False,
-                        workspace=None, out=None) -> BlockNormGrads:
+                        workspace=None, out=None, residual_dtype=None) -> BlockNormGrads:
     """Gradients of puro_block_norm_fwd from those of r_out (dr_out, None for zero) and n (dn
     bf16, None if w_pre was). y and r_out: the saved tensors, or both as their checkpoints,
     (codes, scales) pairs; rstd_y None: the norm after the block was left out. accumulate adds
     dw_post, dw_pre and a channel gate's gradient to `out`'s. `out`: the five outputs to write
-    (None to skip; out.dr may be dr_out)."""
+    (None to skip; out.dr may be dr_out). residual_dtype: the residual stream's type, for a new dr
+    where neither dr_out nor r_out as it was says it (the last boundary, from checkpoints)."""
     lead = dr_out if dr_out is not None else dn
     if lead is None:
         raise PuroError("dr_out and dn: at least one is required")
@@ -584,20 +590,26 @@ def puro_block_norm_bwd(dr_out, dn, y, r_out, rstd_y, rstd_r, w_post, w_pre, gat
         dev = _dev(lead)
         rows, cols = _matrix(lead, "dr_out")
         vec = lambda: torch.empty((cols,), dtype=torch.float32, device=dev)  # noqa: E731
-        out = BlockNormGrads(torch.empty((rows, cols), dtype=_residual(dr_out, r_out, None),
+        out = BlockNormGrads(torch.empty((rows, cols),
+                                         dtype=_residual(dr_out, r_out, residual_dtype),
                                          device=dev),
                              torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
                              if post else None, vec() if post else None, vec() if pre else None,
                              torch.empty_like(gate) if gate is not None else None)
-    elif type(out) is not BlockNormGrads:
-        out = BlockNormGrads(*out)
+    else:
+        if type(out) is not BlockNormGrads:
+            out = BlockNormGrads(*out)
+        if residual_dtype is not None:
+            _residual(out.dr, None, residual_dtype)
     if _done((_native or _load_native()).norm_bwd(dr_out, dn, y, r_out, rstd_y, rstd_r, w_post,
                                                   w_pre, gate, alpha, beta, accumulate, workspace,
                                                   out)):
         return out
     dev = _dev(lead)
     rows, cols = _matrix(lead, "dr_out")
-    res = _residual(dr_out, r_out, out[0])
+    # (of neither: nothing of the residual type is read or written)
+    res = next((t.dtype for t in (dr_out, r_out, out[0]) if isinstance(t, torch.Tensor)),
+               torch.bfloat16)
     if res not in _TYPES:
         raise PuroError("dr_out: expected bf16 or fp32")
     kind = _gate_kind(gate)

@@ -293,7 +293,8 @@ PyObject* norm_bwd(PyObject* const* a) {
   if (!c.ok || !outputs(a[13], 5)) Py_RETURN_NONE;
   PyObject* const* o = &PyTuple_GET_ITEM(a[13], 0);
   const bool post = a[4] != Py_None, pre = a[1] != Py_None;
-  // the residual type: that of dr_out, else of r_out, else of dr, else bf16
+  // the residual type: that of dr_out, else of r_out, else of dr; without any of them nothing of
+  // that type is read or written
   const at::Tensor* typed = a[0] != Py_None ? c.lead : as_tensor(a[3]);
   if (typed == nullptr) typed = as_tensor(o[0]);
   const at::ScalarType res = typed != nullptr ? typed->scalar_type() : at::kBFloat16;

@@ -70,7 +70,7 @@ class MlpStack:
                                      vector(0.5), vector(1.0)))
 
     def forward(self, r):
-        """r: the residual stream, bf16 [tokens, d] -> (n bf16 [tokens, d], kept)."""
+        """r: the residual stream, bf16 or fp32 [tokens, d] -> (n bf16 [tokens, d], kept)."""
         first = puro.puro_block_norm_fwd(None, r, None, self.w_first, eps=self.eps)
         kept, n, last = [], (first.nq, first.ns), len(self.layers) - 1
         for i, p in enumerate(self.layers):
@@ -84,17 +84,17 @@ class MlpStack:
             kept.append(Kept(n, (act.guq, act.gus), (wguq, wgus), (wdq, wds),
                              norm._replace(r_out=None)))
             r, n = norm.r_out, (norm.nq, norm.ns)
-        return norm.n, (first, kept)
+        return norm.n, (first, kept, r.dtype)
 
     def backward(self, dn, kept):
-        """dn: the gradient of forward's n, bf16 -> (dr, dw_first, [gradients of each layer's wgu,
-        wd, w_post, gate, w_pre])."""
-        first, kept = kept
+        """dn: the gradient of forward's n, bf16 -> (dr in the residual stream's type, dw_first,
+        [gradients of each layer's wgu, wd, w_post, gate, w_pre])."""
+        first, kept, stream = kept
         grads, dr = [], None
         for p, k in zip(reversed(self.layers), reversed(kept)):
             o = puro.puro_block_norm_bwd(dr, dn, (k.norm.yq, k.norm.ys), (k.norm.rq, k.norm.rs),
                                          k.norm.rstd_y, k.norm.rstd_r, p.w_post, p.w_pre, p.gate,
-                                         alpha=self.alpha, beta=self.beta)
+                                         alpha=self.alpha, beta=self.beta, residual_dtype=stream)
             dyq, dys, dytq, dyts = puro.puro_quant_dual_1x128(o.dy)
             dh = puro.puro_fp8_gemm_dgrad(dyq, dys, *k.wd)
             a = puro.puro_swiglu_bwd_fp8(dh, k.gu)
@@ -104,7 +104,7 @@ class MlpStack:
             grads.append((dwgu, dwd, o.dw_post, o.dgate, o.dw_pre))
             dr = o.dr
         o = puro.puro_block_norm_bwd(dr, dn, None, (first.rq, first.rs), None, first.rstd_r, None,
-                                     self.w_first)
+                                     self.w_first, residual_dtype=stream)
         return o.dr, o.dw_pre, grads[::-1]
 
 

@@ -69,3 +69,50 @@ def test_prepared_group_call_without_a_tensor(puro):
             call()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((*qs, *ss), (*want_q, *want_s)))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_residual_type_of_the_last_boundary(puro, dtype):
+    """From checkpoints and without a gradient of the stream nothing says the stream's type: it is
+    asked for, and dr has it. Its values are those with a gradient of zeros, and fp32 ones are
+    not rounded to bf16: against 64 bits within the bound that block_ref derives."""
+    import block_ref as ref
+    from blockwise_fp8_gemm_x128_amd import PuroError
+    rows, cols = 40, 384
+    y, r = rnd((rows, cols), 7, BF16), rnd((rows, cols), 8, dtype)
+    wo, wp, dn = rnd((cols,), 9), rnd((cols,), 10), rnd((rows, cols), 11, BF16, 1e-3)
+    o = puro.puro_block_norm_fwd(y, r, wo, wp)
+    saved = ((o.yq, o.ys), (o.rq, o.rs), o.rstd_y, o.rstd_r, wo, wp)
+    with pytest.raises(PuroError, match="residual_dtype"):
+        puro.puro_block_norm_bwd(None, dn, *saved)
+    with pytest.raises(PuroError, match="residual_dtype"):
+        puro.puro_block_norm_bwd(None, dn, *saved, residual_dtype=torch.float16)
+    with pytest.raises(PuroError, match="residual_dtype"):
+        puro.puro_block_norm_bwd(torch.zeros_like(r), dn, *saved,
+                                 residual_dtype=F32 if dtype is BF16 else BF16)
+    a = puro.puro_block_norm_bwd(None, dn, *saved, residual_dtype=dtype)
+    b = puro.puro_block_norm_bwd(torch.zeros_like(r), dn, *saved)
+    assert a.dr.dtype == b.dr.dtype == dtype
+    assert all(torch.equal(x, z) for x, z in zip(a[:4], b[:4]))
+    c = puro.puro_block_norm_bwd(None, dn, *saved, out=b, residual_dtype=dtype)
+    assert c.dr is b.dr and torch.equal(c.dr, a.dr)
+    with pytest.raises(PuroError, match="residual_dtype"):
+        puro.puro_block_norm_bwd(None, dn, *saved, out=b,
+                                 residual_dtype=F32 if dtype is BF16 else BF16)
+    v, e = ref.norm_bwd(None, ref.f64(dn), ref.f64(ref.decode32(o.yq, o.ys)),
+                        ref.f64(ref.decode32(o.rq, o.rs)), ref.f64(o.rstd_y), ref.f64(o.rstd_r),
+                        ref.f64(wo), ref.f64(wp), ref.gate64(None), 1.0, 1.0, None)
+    ref.close(a.dr, v["dr"], e["dr"] + ref.out_err(v["dr"], dtype) * 1.01, "dr")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_stack_keeps_the_streams_type(puro, dtype):
+    """The gradient of an fp32 residual stream stays in fp32 through every boundary: it has bits
+    that bf16 has not."""
+    from blockwise_fp8_gemm_x128_amd.mlp_stack import MlpStack
+    stack = MlpStack(2, 256, 128, seed=3)
+    n, kept = stack.forward(rnd((128, 256), 12, dtype))
+    dr, _, _ = stack.backward(rnd((128, 256), 13, BF16), kept)
+    assert n.dtype == BF16 and dr.dtype == dtype
+    if dtype == F32:
+        assert not torch.equal(dr, dr.to(BF16).float())
