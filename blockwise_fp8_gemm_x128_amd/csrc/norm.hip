@@ -682,6 +682,12 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const ReduceArgs a) {
     a.dgate[c] = a.alpha * a.w_post[c] * v + (a.accumulate ? a.dgate[c] : 0.0f);
 }
 
+// The gradient of a gate per row where there are no columns to sum over.
+__global__ __launch_bounds__(256) void zero_kernel(float* p, int64_t n) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) p[i] = 0.0f;
+}
+
 // ------------------------------------------------------------------ host side
 // How a row is laid over lanes: 16, 32 or 64 lanes of 8 columns up to 512 columns, then whole
 // waves, one vector per lane up to a number of columns and two beyond; or, up to 2048 columns,
@@ -826,10 +832,11 @@ extern "C" puro_status puro_block_norm_fwd(const puro_block_norm* d, void* strea
   if (!std::isfinite(d->alpha) || !std::isfinite(d->beta) || !std::isfinite(d->eps) ||
       !(d->eps > 0))
     return PURO_ERR_ARG;
+  if (d->cols == 0) return PURO_OK;  // empty tensors, whose addresses may all be NULL
   const bool post = d->w_post != nullptr, pre = d->w_pre != nullptr;
   if (!post && (d->gate_kind != PURO_GATE_NONE || d->y || d->yq || d->ys)) return PURO_ERR_ARG;
   if (!pre && (d->n || d->nq || d->ns)) return PURO_ERR_ARG;
-  if (d->rows == 0 || d->cols == 0) return PURO_OK;
+  if (d->rows == 0) return PURO_OK;
   if (!post && !pre) return PURO_ERR_NULL;
   PURO_TRY(check_ptr(d->r, false));
   PURO_TRY(check_optional(d->r_out));
@@ -880,13 +887,19 @@ extern "C" puro_status puro_block_norm_bwd(const puro_block_norm_grad* d, void* 
       (d->accumulate != 0 && d->accumulate != 1))
     return PURO_ERR_ARG;
   if (!std::isfinite(d->alpha) || !std::isfinite(d->beta)) return PURO_ERR_ARG;
+  const bool empty = d->rows == 0;
+  if (d->cols == 0) {  // empty tensors, whose addresses may all be NULL
+    if (empty || d->gate_kind != PURO_GATE_TOKEN) return PURO_OK;
+    PURO_TRY(check_ptr(d->dgate, false));
+    hipLaunchKernelGGL(zero_kernel, dim3(static_cast<uint32_t>(ceil_div(d->rows, 256))), dim3(256),
+                       0, static_cast<hipStream_t>(stream), static_cast<float*>(d->dgate), d->rows);
+    return launch_status();
+  }
   const bool post = d->w_post != nullptr, pre = d->w_pre != nullptr;
   if (!post && (d->gate_kind != PURO_GATE_NONE || d->y || d->yq || d->dy || d->dw_post))
     return PURO_ERR_ARG;
   if (!pre && (d->dn || d->r || d->rq || d->dw_pre)) return PURO_ERR_ARG;
   if ((d->y && d->yq) || (d->r && d->rq)) return PURO_ERR_ARG;
-  if (d->cols == 0) return PURO_OK;
-  const bool empty = d->rows == 0;
   if (!empty) {
     if (!post && !pre) return PURO_ERR_NULL;
     if (!pre && d->dr_out == nullptr) return PURO_ERR_NULL;

@@ -295,7 +295,8 @@ puro_status puro_ckpt_transpose(const void* q, const float* s, int64_t rows, int
  *   n = r_out * rstd_r * w_pre,         rstd_r = 1/sqrt(mean(r_out^2) + eps)
  * n is formed from the unrounded r_out. Either half may be left out: w_post and y NULL for the norm
  * before a block alone (then r_out = beta * r), w_pre NULL for the norm after a block alone.
- * cols <= PURO_NORM_MAX_COLS. Sums of squares must fit fp32. */
+ * cols <= PURO_NORM_MAX_COLS. Sums of squares must fit fp32. With cols = 0 nothing is written (the
+ * mean over no columns has no value). */
 #define PURO_NORM_MAX_COLS 16384
 #define PURO_GATE_NONE 0
 #define PURO_GATE_CHANNEL 1 /* fp32 [cols] */
@@ -334,6 +335,7 @@ puro_status puro_block_norm_fwd(const puro_block_norm* desc, void* stream);
  *   dw_post = sum over rows of dp yh,  dw_pre = sum over rows of dn rh     (NULL to skip)
  *   dgate = alpha w_post yh G, summed over rows (PURO_GATE_CHANNEL), over columns
  *           (PURO_GATE_TOKEN) or as it is (PURO_GATE_FULL), in the gate's type
+ * With cols = 0 a gate per token's gradient is zero.
  * accumulate = 1 adds dw_post, dw_pre and a channel gate's gradient to what is there. w_post NULL:
  * the norm after the block was left out; w_pre NULL: the norm before the next one. y and r are both
  * as they were or both checkpoints.

@@ -116,3 +116,26 @@ def test_stack_keeps_the_streams_type(puro, dtype):
     assert n.dtype == BF16 and dr.dtype == dtype
     if dtype == F32:
         assert not torch.equal(dr, dr.to(BF16).float())
+
+
+def test_gate_per_token_without_columns(puro):
+    """A sum over no columns: zero, and not what the memory held."""
+    e, rstd = torch.empty((5, 0), dtype=BF16, device=DEV), torch.ones(5, device=DEV)
+    w, gate = torch.empty(0, device=DEV), torch.ones((5, 1), device=DEV)
+    out = puro.BlockNormGrads(torch.empty_like(e), torch.empty_like(e), torch.empty_like(w),
+                              torch.empty_like(w), torch.full((5, 1), 7.0, device=DEV))
+    g = puro.puro_block_norm_bwd(e, e, e, e, rstd, rstd, w, w, gate, out=out)
+    assert torch.all(g.dgate == 0)
+    for other in (None, w, e):                              # no gate, one per column, per element
+        o = puro.puro_block_norm_fwd(e, e, w, w, other)
+        assert o.r_out.shape == (5, 0)
+        g = puro.puro_block_norm_bwd(e, e, e, e, rstd, rstd, w, w, other)
+        assert g.dr.shape == (5, 0) and g.dw_pre.shape == (0,)
+    big = puro.BlockNormGrads(None, torch.empty((300000, 0), dtype=BF16, device=DEV), None, None,
+                              torch.full((300001, 1), 7.0, device=DEV)[:300000])
+    e = torch.empty((300000, 0), dtype=BF16, device=DEV)
+    rstd, gate = torch.ones(300000, device=DEV), torch.ones((300000, 1), device=DEV)
+    puro.puro_block_norm_bwd(e, e, (e.view(torch.uint8), torch.empty((0, 300000), device=DEV)),
+                             (e.view(torch.uint8), torch.empty((0, 300000), device=DEV)), rstd,
+                             rstd, w, w, gate, out=big)
+    assert torch.all(big.dgate == 0)

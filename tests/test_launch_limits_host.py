@@ -63,3 +63,28 @@ def test_gemms_past_the_thread_limit(L, sfx):
     assert getattr(L, "puro_fp8_gemm_fwd" + sfx)(P, P, P, P, P, MAX, n, 128, None) == SHAPE
     assert getattr(L, "puro_fp8_gemm_dgrad" + sfx)(P, P, P, P, P, MAX, 128, n, None) == SHAPE
     assert getattr(L, "puro_fp8_gemm_wgrad" + sfx)(P, P, P, P, P, 128, MAX, n, 0, None) == SHAPE
+
+
+def test_norm_without_columns(L):
+    """Empty tensors may have no address: that of the weight after the block does not say that its
+    half was left out."""
+    import ctypes
+
+    from blockwise_fp8_gemm_x128_amd._lib import PuroBlockNorm, PuroBlockNormGrad
+    for kind in range(4):
+        sizes = dict(rows=8, cols=0, gate_kind=kind, alpha=1.0, beta=1.0, gate=P)
+        d = PuroBlockNorm(eps=1e-6, rstd_y=P, rstd_r=P, **sizes)
+        assert L.puro_block_norm_fwd(ctypes.byref(d), None) == 0
+        if kind != 2:
+            assert L.puro_block_norm_bwd(ctypes.byref(PuroBlockNormGrad(**sizes)), None, None) == 0
+
+
+def test_gate_per_token_without_columns(L):
+    """Its gradient, a sum over no columns, is zero and has to be written: its address is checked."""
+    import ctypes
+
+    from blockwise_fp8_gemm_x128_amd._lib import PuroBlockNormGrad
+    for status, dgate in ((1, None), (3, P + 1)):
+        d = PuroBlockNormGrad(rows=8, cols=0, gate_kind=2, alpha=1.0, beta=1.0, w_post=P, gate=P,
+                              dgate=dgate)
+        assert L.puro_block_norm_bwd(ctypes.byref(d), P, None) == status
