@@ -1,6 +1,8 @@
-"""Builds libpuro.so (all HIP kernels + the C ABI) for gfx950 with hipcc, in-tree.
+"""Builds libpuro.so (all HIP kernels + the C ABI) for gfx950 with hipcc, in-tree, and the Python
+binding's native half with the host compiler.
 
-Usage: ``python -m blockwise_fp8_gemm_x128_amd.build`` (also called by ``__graft_entry__.build``).
+Usage: ``python -m blockwise_fp8_gemm_x128_amd.build`` (also called by ``__graft_entry__.build``),
+with ``--library`` for the C library alone, which needs neither torch nor a host compiler.
 """
 from __future__ import annotations
 
@@ -66,7 +68,8 @@ def _args(verbose: bool) -> str:
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
            *("-I" + p for p in cpp_extension.include_paths("cpu")),
            "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE,
-           os.path.join(CSRC, "args.cpp"), "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+           os.path.join(CSRC, "args.cpp"), "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
@@ -74,11 +77,22 @@ def _args(verbose: bool) -> str:
     return ARGS_PATH
 
 
-def build(verbose: bool = True) -> str:
-    _args(verbose)
-    _hipcc(PROBE_SOURCES, PROBE_PATH, verbose)
+def build_library(verbose: bool = True) -> str:
+    """The C library alone."""
     return _hipcc(SOURCES, LIB_PATH, verbose)
 
 
+def build(verbose: bool = True) -> str:
+    """Everything, the C library first: it is in place also where the binding's half fails."""
+    build_library(verbose)
+    _hipcc(PROBE_SOURCES, PROBE_PATH, verbose)
+    try:
+        _args(verbose)
+    except (ImportError, OSError, RuntimeError, subprocess.CalledProcessError) as e:
+        raise RuntimeError("the binding's native half (%s) failed to build; %s is built" %
+                           (os.path.basename(ARGS_PATH), os.path.basename(LIB_PATH))) from e
+    return LIB_PATH
+
+
 if __name__ == "__main__":
-    print(build())
+    print(build_library() if sys.argv[1:] == ["--library"] else build())
