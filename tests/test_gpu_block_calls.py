@@ -139,3 +139,38 @@ def test_gate_per_token_without_columns(puro):
                              (e.view(torch.uint8), torch.empty((0, 300000), device=DEV)), rstd,
                              rstd, w, w, gate, out=big)
     assert torch.all(big.dgate == 0)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_operators_write_the_quantisers_bytes(puro, pow2):
+    """Where the input of a code is exact, its bytes are the quantisers': the activation's checkpoint
+    and the norm's of its input against the activation quantiser; a forward operand that stands
+    for a matrix exactly, requantised along its rows, against the transposing quantiser of that
+    matrix."""
+    sfx = "_pow2" if pow2 else ""
+    act, turn = (getattr(puro, n + sfx) for n in ("puro_quant_act_1x128", "puro_quant_transpose"))
+    same = lambda a, b: torch.equal(a.view(torch.uint8), b.view(torch.uint8))  # noqa: E731
+    rows, f = 384, 640
+    gu = rnd((rows, 2 * f), 14, BF16, 3.0)
+    gu[5] = 0.0
+    o = puro.puro_swiglu_fwd(gu, pow2=pow2)
+    for i in range(2):
+        q, s = act(gu[:, i * f:(i + 1) * f].contiguous())
+        assert same(o.guq[:, i * f:(i + 1) * f].contiguous(), q)
+        assert same(o.gus[i * f // 128:(i + 1) * f // 128].contiguous(), s)
+    y, w = gu[:, :f].contiguous(), rnd((f,), 15)
+    n = puro.puro_block_norm_fwd(y, y, w, w, pow2=pow2)
+    q, s = act(y)
+    assert same(n.yq, q) and same(n.ys, s)
+    # E4M3 values times a power of two per row, 448 among them in every group: the scale is that
+    # power, under either rule, and every value is what its code stands for
+    codes = torch.randint(0, 256, (rows, f), generator=torch.Generator().manual_seed(16))
+    codes[(codes & 0x7F) == 0x7F] = 0x38
+    codes[:, ::128] = 0x7E
+    power = torch.exp2(torch.arange(rows) % 9 - 4.0)[:, None]
+    x = (codes.to(torch.uint8).view(torch.float8_e4m3fn).float() * power).to(BF16).to(DEV)
+    q, s = act(x)
+    assert torch.equal(q.cpu().int(), codes.int())
+    assert torch.equal(s.cpu(), power.t().expand(f // 128, rows))
+    for a, b in zip(puro.puro_ckpt_transpose(q, s, pow2=pow2), turn(x)):
+        assert same(a, b)
