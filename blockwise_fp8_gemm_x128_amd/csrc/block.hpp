@@ -35,11 +35,12 @@ __device__ __forceinline__ uint32_t xcd_range(uint32_t b, uint32_t n) {
 
 // The elementwise kernels' block of 256 threads: 16 lane groups of 16, each on one 128-column chunk
 // of a row; two chunks side by side, eight rows a pass, two passes with all their loads issued
-// first. Measured on MI355X, all stores through the caches (past them, as now, the same calls take
-// 29.7, 55.3 and 7.0 us), against 1, 4, 8 and 16 chunks and 1 and 4 passes: 16384 x 2048 fp32
-// packed in 30.3 us (30.8 to 35.2), the activation of 8192 x 6144 in 63.9 us (67 to 74.5), 2047 x
-// 4111 unpacked in 7.1 us (7 to 9.8). Ranges per XCD: 4000 x 5003 packed in 12.4 us against 14.9,
-// but 8192 x 6144 activated in 67.5 against 63.9, so only rows off the 128 B lines take them.
+// first. Measured on MI355X, all stores through the caches, against 1, 4, 8 and 16 chunks and 1 and
+// 4 passes: 16384 x 2048 fp32 packed in 30.3 us (30.8 to 35.2), the activation of 8192 x 6144 in
+// 63.9 us (67 to 74.5), 2047 x 4111 unpacked in 7.1 us (7 to 9.8). (Checkpoints' codes now go past
+// the caches, which makes the first two 29.7 and 55.3 us.) Ranges per XCD: 4000 x 5003 packed in
+// 12.4 us against 14.9, but 8192 x 6144 activated in 67.5 against 63.9, so only rows off the 128 B
+// lines take them.
 struct RowTile {
   static constexpr int kChunks = 2, kPasses = 2;
   static constexpr int kStep = 16 / kChunks;      // rows between passes
@@ -410,7 +411,9 @@ __device__ __forceinline__ uint32_t row16_umax(uint32_t u) {
 // instructions: with c = fl(1/448), q = a c is within an ulp of a/448, its remainder a - 448 q is
 // exact in one fused step, and q + remainder c rounds to the quotient. The other way the reciprocal
 // of a/16 (so that neither it nor its argument leaves the normal range) is first refined by one
-// Newton step. Checked against the division on MI355X for every float in the range.
+// Newton step. Both are the quotients' bits for every float in the range and a hardware reciprocal
+// off by a unit in the last place either way; tests/test_amax_scale.py runs this function over all
+// of them.
 __device__ __forceinline__ void amax_scale(float a, float& s, float& r) {
   constexpr float c = 1.0f / 448.0f;
   const float q = a * c;

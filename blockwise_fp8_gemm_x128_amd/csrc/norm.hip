@@ -13,7 +13,8 @@
 // alpha (sum q A - rr k1 sum q rh)/D, so one reduction of three sums serves both.
 //
 // HBM-bound: every element of every input is read once into registers, where the row stays until
-// its last output is written; a row belongs to one team of lanes (16, 32 or 64 lanes of a wave for
+// its last output is written (but for the backward pass of rows of more than 8192 columns, which
+// reads a gate per element twice); a row belongs to one team of lanes (16, 32 or 64 lanes of a wave for
 // short rows, whole waves or groups of 16 lanes for longer ones), 8 columns per lane and vector.
 // All statistics and sums are fp32; r' is normalised unrounded, so n does not see the residual
 // stream's rounding.
@@ -771,9 +772,11 @@ Split split_rows(int64_t rows, const Shape& s, int waves, int most_blocks) {
 }
 constexpr int kBwdWaves = 16;
 // Forward: as many waves as the registers allow, but 16 (where blocks make 16) for rows of a
-// multiple of 4 KB in bf16, whose blocks seem to meet on the same memory channels: 8192 x 2048 32.2
-// us against 33.5 with 24, in fp32 47.9 against 50.9, 4096 x 4096 31.6 against 33.4; but 1792
-// columns 35.6 against 34.3, and 6144 columns, where it would be 12 waves, 55.8 against 47.6.
+// multiple of 4 KB in bf16. That is a rule by measurement, with both norms; what causes it was not
+// found: 8192 x 2048 32.2 us against 33.5 with 24, in fp32 47.9 against 50.9, 4096 x 4096 31.6
+// against 33.4; but 1792 columns 35.6 against 34.3, and 6144 columns, where it would be 12 waves,
+// 55.8 against 47.6. The norm before a block alone, which has one load per lane in flight where
+// the two norms have two, takes 20.2 us at 8192 x 2048 under it, 3.4 TB/s.
 int fwd_waves(const Shape& s, int64_t cols) {
   if (s.nv == 2 || s.lanes == kGroups) return 16;
   if (cols % 2048 == 0 && 16 % (s.threads / 64) == 0) return 16;
