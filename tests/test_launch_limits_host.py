@@ -16,7 +16,11 @@ def L():
     from blockwise_fp8_gemm_x128_amd.build import LIB_PATH, build
     if not os.path.exists(LIB_PATH):
         build(verbose=False)
-    return _lib.lib()
+    lib = _lib.lib()
+    level = lib.puro_debug_level()   # debug mode would look at the inputs first
+    lib.puro_set_debug(0)
+    yield lib
+    lib.puro_set_debug(level)
 
 
 # 256 threads for 16 rows x 256 columns: 2^20 row tiles x 16 column tiles are 2^24 blocks, 2^32
