@@ -32,6 +32,9 @@ __all__ = [
     "puro_swiglu_fwd",
     "puro_swiglu_bwd",
     "puro_swiglu_bwd_fp8",
+    "puro_newton_schulz",
+    "puro_linear_xent_fwd",
+    "puro_linear_xent_bwd",
 ]
 
 

@@ -49,9 +49,35 @@ class PuroBlockNormGrad(ctypes.Structure):
                     "w_post", "w_pre", "gate", "dr", "dy", "dw_post", "dw_pre", "dgate")])
 
 
+class PuroNsItem(ctypes.Structure):
+    """puro_ns_item: one matrix of a grouped orthogonalisation."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("g", "m", "m_out", "u")]
+
+
+class PuroNewtonSchulzParams(ctypes.Structure):
+    """puro_newton_schulz_params."""
+    _fields_ = [("steps", ctypes.c_int), ("nesterov", ctypes.c_int), ("beta", ctypes.c_float),
+                ("scale", ctypes.c_float), ("coefficients", ctypes.c_float * 3)]
+
+
+class PuroLinearXent(ctypes.Structure):
+    """puro_linear_xent: one forward cross entropy."""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("tokens", "d", "vocab", "ldh", "ldw")]
+                + [(k, ctypes.c_void_p) for k in ("h", "w", "targets", "loss", "lse")])
+
+
+class PuroLinearXentGrad(ctypes.Structure):
+    """puro_linear_xent_grad: one backward cross entropy."""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("tokens", "d", "vocab", "ldh", "ldw")]
+                + [(k, ctypes.c_int) for k in ("dw_type", "accumulate")]
+                + [(k, ctypes.c_void_p) for k in
+                   ("h", "w", "targets", "lse", "dloss", "dlse", "dh", "dw")])
+
+
 TYPE_BF16, TYPE_FP32 = 0, 1                                     # PURO_TYPE_*
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3     # PURO_GATE_*
 NORM_MAX_COLS = 16384                                           # PURO_NORM_MAX_COLS
+NS_GROUP_MAX = 64                                               # PURO_NS_GROUP_MAX
 
 OPT_MAX_BLOCKS = 2048  # PURO_OPT_MAX_BLOCKS
 OPT_WORKSPACE_BYTES = 8 * OPT_MAX_BLOCKS + 256  # PURO_OPT_WORKSPACE_BYTES
@@ -76,6 +102,14 @@ SIGNATURES.update({
     "puro_frobenius_norm": ([_P, _I64, _P, _P, _P], ctypes.c_int),
     "puro_hyperball_step": ([_P, _P, _I64, ctypes.c_float, _P, _P, _P, _P], ctypes.c_int),
     "puro_hyperball_step_noalloc": ([_P, _P, _I64, ctypes.c_float, _P, _P, _P], ctypes.c_int),
+    "puro_hyperball_step_u16": ([_P, _P, _I64, ctypes.c_float, _P, _P, _P, _P], ctypes.c_int),
+    "puro_newton_schulz_workspace": ([_I64, _I64, _I64], _I64),
+    "puro_newton_schulz": ([ctypes.POINTER(PuroNsItem), ctypes.c_int, _I64, _I64,
+                            ctypes.POINTER(PuroNewtonSchulzParams), _P, _P], ctypes.c_int),
+    "puro_linear_xent_fwd_workspace": ([ctypes.POINTER(PuroLinearXent)], _I64),
+    "puro_linear_xent_fwd": ([ctypes.POINTER(PuroLinearXent), _P, _P], ctypes.c_int),
+    "puro_linear_xent_bwd_workspace": ([ctypes.POINTER(PuroLinearXentGrad)], _I64),
+    "puro_linear_xent_bwd": ([ctypes.POINTER(PuroLinearXentGrad), _P, _P], ctypes.c_int),
     "puro_adamw_step": ([_P, _P, _P, _P, _I64, ctypes.POINTER(PuroAdamWParams), _P, _P],
                         ctypes.c_int),
 })

@@ -13,9 +13,10 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from ._lib import (GATE_CHANNEL, GATE_FULL, GATE_NONE, GATE_TOKEN, OPT_WORKSPACE_BYTES, TYPE_BF16,
-                   TYPE_FP32, W_GROUP_MAX, PuroAdamWParams, PuroBlockNorm, PuroBlockNormGrad,
-                   PuroError, PuroWItem, check, lib)
+from ._lib import (GATE_CHANNEL, GATE_FULL, GATE_NONE, GATE_TOKEN, NS_GROUP_MAX,
+                   OPT_WORKSPACE_BYTES, TYPE_BF16, TYPE_FP32, W_GROUP_MAX, PuroAdamWParams,
+                   PuroBlockNorm, PuroBlockNormGrad, PuroError, PuroLinearXent, PuroLinearXentGrad,
+                   PuroNewtonSchulzParams, PuroNsItem, PuroWItem, check, lib)
 
 FP8 = torch.uint8  # E4M3 codes travel as raw bytes
 
@@ -238,6 +239,24 @@ def puro_hyperball_step(w: torch.Tensor, u: torch.Tensor, lr: float, radius: tor
         _need_workspace(workspace, OPT_WORKSPACE_BYTES, dev)
     check(lib().puro_hyperball_step(w.data_ptr(), u.data_ptr(), n, float(lr), radius.data_ptr(),
                                     w_bf16.data_ptr(), workspace.data_ptr(), _stream(dev)))
+    return w_bf16
+
+
+def puro_hyperball_step_u16(w: torch.Tensor, u: torch.Tensor, lr: float, radius: torch.Tensor,
+                            w_bf16=None, workspace=None):
+    """puro_hyperball_step with the direction in bf16, as puro_newton_schulz writes it."""
+    dev = _dev(w)
+    _need(w, "w", torch.float32, tuple(w.shape), dev)
+    _need(u, "u", torch.bfloat16, tuple(w.shape), dev)
+    _need(radius, "radius", torch.float32, (1,), dev)
+    w_bf16 = _out(w_bf16, "w_bf16", torch.bfloat16, tuple(w.shape), dev)
+    if workspace is None:
+        workspace = optim_workspace(dev)
+    else:
+        _need_workspace(workspace, OPT_WORKSPACE_BYTES, dev)
+    check(lib().puro_hyperball_step_u16(w.data_ptr(), u.data_ptr(), w.numel(), float(lr),
+                                        radius.data_ptr(), w_bf16.data_ptr(),
+                                        workspace.data_ptr(), _stream(dev)))
     return w_bf16
 
 
@@ -729,6 +748,131 @@ def puro_swiglu_bwd_fp8(dh, gu, pow2: bool = False, out=None) -> SwiGLUOperands:
     _call("puro_swiglu_bwd_fp8", p[0], p[1], p[2], gus, rows, f, bool(pow2), p[3], dgus, p[4],
           dguts, p[5], hts, _stream(dev))
     return out
+
+
+# ---------------------------------------------------------------- update direction
+NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def ns_workspace(count: int, rows: int, cols: int, dev) -> torch.Tensor:
+    """Device workspace of puro_newton_schulz for `count` matrices [rows, cols]."""
+    return torch.empty(lib().puro_newton_schulz_workspace(count, rows, cols), dtype=torch.uint8,
+                       device=dev)
+
+
+def puro_newton_schulz(gs, ms=None, us=None, ms_out=None, beta: float = 0.95,
+                       nesterov: bool = True, scale: float = 1.0, steps: int = 5,
+                       coefficients=NS_COEFFICIENTS, workspace=None):
+    """Directions u (a list of bf16 [rows, cols]) of the gradients gs, fp32 matrices of one shape (a
+    list, at most 64): their momentum ms (fp32, updated in place, or into ms_out; None: none),
+    orthogonalised by Newton-Schulz products and scaled."""
+    gs = list(gs)
+    if not gs:
+        return []
+    if len(gs) > NS_GROUP_MAX:
+        raise PuroError(f"at most {NS_GROUP_MAX} matrices per grouped call")
+    dev = _dev(gs[0])
+    rows, cols = shape = _matrix(gs[0], "g[0]")
+    if ms is None and ms_out is not None:
+        raise PuroError("ms_out needs ms")
+    ms = None if ms is None else list(ms)
+    ms_out = ms if ms_out is None else list(ms_out)
+    us = ([torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in gs] if us is None
+          else list(us))
+    for name, ts in (("ms", ms), ("ms_out", ms_out), ("us", us)):
+        if ts is not None and len(ts) != len(gs):
+            raise PuroError(f"{name}: {len(ts)} matrices, expected {len(gs)}")
+    items = (PuroNsItem * len(gs))()
+    for i, (item, g, u) in enumerate(zip(items, gs, us)):
+        _need(g, f"g[{i}]", torch.float32, shape, dev)
+        _need(u, f"u[{i}]", torch.bfloat16, shape, dev)
+        item.g, item.u = g.data_ptr(), u.data_ptr()
+        if ms is not None:
+            _need(ms[i], f"m[{i}]", torch.float32, shape, dev)
+            _need(ms_out[i], f"m_out[{i}]", torch.float32, shape, dev)
+            item.m, item.m_out = ms[i].data_ptr(), ms_out[i].data_ptr()
+    hp = PuroNewtonSchulzParams(int(steps), int(bool(nesterov)), float(beta), float(scale),
+                                (ctypes.c_float * 3)(*coefficients))
+    need = lib().puro_newton_schulz_workspace(len(gs), rows, cols)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need_workspace(workspace, need, dev)
+    check(lib().puro_newton_schulz(items, len(gs), rows, cols, ctypes.byref(hp),
+                                   workspace.data_ptr() or None, _stream(dev)))
+    return us
+
+
+# ---------------------------------------------------------------- output head
+def _need_bf16_rows(x, name, dev):
+    """_need_rows for bf16 alone; returns the row stride."""
+    kind, ld = _need_rows(x, name, dev)
+    if kind != TYPE_BF16:
+        raise PuroError(f"{name}: dtype {x.dtype}, expected {torch.bfloat16}")
+    return ld
+
+
+def _head(h, w, targets):
+    """Checks of the head's inputs; returns (device, tokens, d, vocab, ldh, ldw)."""
+    dev = _dev(h)
+    ldh = _need_bf16_rows(h, "h", dev)
+    ldw = _need_bf16_rows(w, "w", dev)
+    (tokens, d), vocab = h.shape, w.shape[0]
+    if w.shape[1] != d:
+        raise PuroError(f"w: shape {tuple(w.shape)}, expected {(vocab, d)}")
+    _need(targets, "targets", torch.int64, (tokens,), dev)
+    return dev, tokens, d, vocab, ldh, ldw
+
+
+def _with_workspace(name, desc, workspace, dev) -> None:
+    """Calls `name` with its structure and workspace, allocated if there is none."""
+    need = getattr(lib(), name + "_workspace")(ctypes.byref(desc))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need_workspace(workspace, need, dev)
+    check(getattr(lib(), name)(ctypes.byref(desc), workspace.data_ptr() or None, _stream(dev)))
+
+
+def puro_linear_xent_fwd(h, w, targets, loss=None, lse=None, workspace=None):
+    """Softmax cross entropy of hidden states h, bf16 [tokens, d], against the output head's weights
+    w, bf16 [vocab, d] (rows of both may be strided), without the matrix of all logits -> (loss, lse),
+    fp32 [tokens]. targets: int64 [tokens]; a target outside [0, vocab) is none (loss and lse 0)."""
+    dev, tokens, d, vocab, ldh, ldw = _head(h, w, targets)
+    loss = _out(loss, "loss", torch.float32, (tokens,), dev)
+    lse = _out(lse, "lse", torch.float32, (tokens,), dev)
+    desc = PuroLinearXent(tokens, d, vocab, ldh, ldw, h.data_ptr(), w.data_ptr(),
+                          targets.data_ptr(), loss.data_ptr(), lse.data_ptr())
+    _with_workspace("puro_linear_xent_fwd", desc, workspace, dev)
+    return loss, lse
+
+
+def puro_linear_xent_bwd(h, w, targets, lse, dloss, dlse=None, dh=None, dw=None,
+                         dw_dtype=torch.bfloat16, accumulate: bool = False, want_dh: bool = True,
+                         want_dw: bool = True, workspace=None):
+    """The gradients (dh bf16 [tokens, d], dw bf16 or fp32 [vocab, d]) from those of loss (dloss) and
+    lse (dlse, or None), fp32 [tokens]. dw has dw_dtype, or the type of the dw given; accumulate
+    adds to an existing fp32 dw. want_dh, want_dw: False leaves that gradient out (None)."""
+    dev, tokens, d, vocab, ldh, ldw = _head(h, w, targets)
+    _need(lse, "lse", torch.float32, (tokens,), dev)
+    _need(dloss, "dloss", torch.float32, (tokens,), dev)
+    if dlse is not None:
+        _need(dlse, "dlse", torch.float32, (tokens,), dev)
+    if accumulate and dw is None:
+        raise PuroError("accumulate=True needs an existing dw")
+    if isinstance(dw, torch.Tensor):
+        dw_dtype = dw.dtype
+    if dw_dtype not in _TYPES:
+        raise PuroError(f"dw: dtype {dw_dtype}, expected bf16 or fp32")
+    dh = _out(dh, "dh", torch.bfloat16, (tokens, d), dev) if want_dh else None
+    dw = _out(dw, "dw", dw_dtype, (vocab, d), dev) if want_dw else None
+    desc = PuroLinearXentGrad(tokens, d, vocab, ldh, ldw, _TYPES[dw_dtype], int(bool(accumulate)),
+                              h.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(),
+                              dloss.data_ptr(), None if dlse is None else dlse.data_ptr(),
+                              None if dh is None else dh.data_ptr(),
+                              None if dw is None else dw.data_ptr())
+    _with_workspace("puro_linear_xent_bwd", desc, workspace, dev)
+    return dh, dw
 
 
 def _pow2_variant(base):

@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libpuro.so")
 SOURCES = ["abi.hip", "quant.hip", "gemm.hip", "optim.hip", "debug.hip", "norm.hip",
-           "swiglu.hip", "ckpt.hip"]
+           "swiglu.hip", "ckpt.hip", "xent.hip", "ortho.hip"]
 # The matrix-core microbenchmark that bench.py --ceiling runs; a library of its own, outside the
 # GEMM path.
 PROBE_PATH = os.path.join(PKG_DIR, "libpuro_probe.so")

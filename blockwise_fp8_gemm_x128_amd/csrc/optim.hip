@@ -30,6 +30,13 @@ __device__ __forceinline__ float4 load_once4f(const float4* p) {
   return make_float4(t[0], t[1], t[2], t[3]);
 }
 
+// The same of four bf16 values, widened.
+__device__ __forceinline__ float4 load_once4f(const uint2* p) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const u32x2 t = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+  return make_float4(bf16_lo(t[0]), bf16_hi(t[0]), bf16_lo(t[1]), bf16_hi(t[1]));
+}
+
 constexpr int kOptThreads = 256;
 constexpr int kOptMaxBlocks = PURO_OPT_MAX_BLOCKS;
 // workspace layout: [kOptMaxBlocks] double partial sums
@@ -55,15 +62,15 @@ __device__ __forceinline__ double block_sum(double x, double* sh) {
 }
 
 // Sum of squares, per block, of src (kUpdate false) or of v = src - lr*u, which is also
-// written to dst (kUpdate true; dst may be src: the update is done in place).
-template <bool kUpdate>
+// written to dst (kUpdate true; dst may be src: the update is done in place). u in fours: float4, or
+// uint2 for bf16.
+template <bool kUpdate, class U4 = float4>
 __global__ __launch_bounds__(kOptThreads) void sumsq_kernel(const float* src,
-                                                            const float* __restrict__ u,
+                                                            const U4* __restrict__ u4,
                                                             float* dst, int64_t n4, float lr,
                                                             double* __restrict__ partials) {
   __shared__ double sh[kOptThreads / 64];
   const float4* s4 = reinterpret_cast<const float4*>(src);
-  const float4* u4 = reinterpret_cast<const float4*>(u);
   float4* d4 = reinterpret_cast<float4*>(dst);
   double acc = 0.0;
   for (int64_t i = int64_t(blockIdx.x) * kOptThreads + threadIdx.x; i < n4;
@@ -207,6 +214,31 @@ puro_status scratch_ptr(void** out) {
   return PURO_OK;
 }
 
+// The projected step with its direction in fours of U4.
+template <class U4>
+puro_status hyperball(float* w, const void* u, int64_t numel, float lr, const float* radius,
+                      void* w_bf16, void* workspace, void* stream) {
+  if (!numel_ok(numel)) return PURO_ERR_SHAPE;
+  if (!isfinite(lr)) return PURO_ERR_ARG;
+  const bool empty = numel == 0;
+  PURO_TRY(check_ptr(w, empty));
+  PURO_TRY(check_ptr(u, empty));
+  PURO_TRY(check_ptr(w_bf16, empty));
+  if (empty) return PURO_OK;
+  if (radius == nullptr || workspace == nullptr) return PURO_ERR_NULL;
+  if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(radius) & 3u)) return PURO_ERR_ALIGN;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t n4 = numel / 4;
+  const int blocks = opt_blocks(n4);
+  double* partials = static_cast<double*>(workspace);
+  hipLaunchKernelGGL((sumsq_kernel<true, U4>), dim3(blocks), dim3(kOptThreads), 0, s, w,
+                     static_cast<const U4*>(u), w, n4, lr, partials);
+  // the same grid as the reduction: each block re-sums the partials, so keep it small
+  hipLaunchKernelGGL(scale_kernel, dim3(blocks), dim3(kOptThreads), 0, s, w, n4, partials, blocks,
+                     radius, static_cast<uint16_t*>(w_bf16));
+  return launch_status();
+}
+
 }  // namespace
 }  // namespace puro
 
@@ -222,8 +254,8 @@ extern "C" puro_status puro_frobenius_norm(const float* w, int64_t numel, float*
   const int64_t n4 = numel / 4;
   const int blocks = opt_blocks(n4);
   double* partials = static_cast<double*>(workspace);
-  hipLaunchKernelGGL(sumsq_kernel<false>, dim3(blocks), dim3(kOptThreads), 0, s, w, nullptr,
-                     nullptr, n4, 0.0f, partials);
+  hipLaunchKernelGGL(sumsq_kernel<false>, dim3(blocks), dim3(kOptThreads), 0, s, w,
+                     static_cast<const float4*>(nullptr), nullptr, n4, 0.0f, partials);
   hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(kOptThreads), 0, s, partials, blocks, norm);
   return launch_status();
 }
@@ -231,25 +263,13 @@ extern "C" puro_status puro_frobenius_norm(const float* w, int64_t numel, float*
 extern "C" puro_status puro_hyperball_step(float* w, const float* u, int64_t numel, float lr,
                                            const float* radius, void* w_bf16, void* workspace,
                                            void* stream) {
-  if (!numel_ok(numel)) return PURO_ERR_SHAPE;
-  if (!isfinite(lr)) return PURO_ERR_ARG;
-  const bool empty = numel == 0;
-  PURO_TRY(check_ptr(w, empty));
-  PURO_TRY(check_ptr(u, empty));
-  PURO_TRY(check_ptr(w_bf16, empty));
-  if (empty) return PURO_OK;
-  if (radius == nullptr || workspace == nullptr) return PURO_ERR_NULL;
-  if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(radius) & 3u)) return PURO_ERR_ALIGN;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  const int64_t n4 = numel / 4;
-  const int blocks = opt_blocks(n4);
-  double* partials = static_cast<double*>(workspace);
-  hipLaunchKernelGGL(sumsq_kernel<true>, dim3(blocks), dim3(kOptThreads), 0, s, w, u, w, n4, lr,
-                     partials);
-  // the same grid as the reduction: each block re-sums the partials, so keep it small
-  hipLaunchKernelGGL(scale_kernel, dim3(blocks), dim3(kOptThreads), 0, s, w, n4, partials, blocks,
-                     radius, static_cast<uint16_t*>(w_bf16));
-  return launch_status();
+  return hyperball<float4>(w, u, numel, lr, radius, w_bf16, workspace, stream);
+}
+
+extern "C" puro_status puro_hyperball_step_u16(float* w, const void* u, int64_t numel, float lr,
+                                               const float* radius, void* w_bf16, void* workspace,
+                                               void* stream) {
+  return hyperball<uint2>(w, u, numel, lr, radius, w_bf16, workspace, stream);
 }
 
 extern "C" puro_status puro_hyperball_step_noalloc(float* w, const float* u, int64_t numel,

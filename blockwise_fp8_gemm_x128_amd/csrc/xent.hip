@@ -1,0 +1,708 @@
+// Softmax cross entropy of hidden states against a large vocabulary, straight from the output
+// head's weights, without a matrix of all logits; and its gradients.
+//
+//   l[t][v] = sum_k h[t][k] w[v][k],  lse[t] = log sum_v exp l[t][v],  loss[t] = lse[t] - l[t][y_t]
+//   P[t][v] = exp(l[t][v] - lse[t]) (dloss[t] + dlse[t]) - [v = y_t] dloss[t]
+//   dh = P w,  dw = P' h
+//
+// Forward: one product whose tiles end in the running maximum and sum of their 256 (128) columns
+// instead of logits, 8 bytes per row and tile, joined by a second kernel. Backward, piece by piece
+// of the vocabulary: the logits are multiplied out again and their tiles end in P, in bf16; the piece of
+// P is then read along its rows (dh) and along its columns (dw). Rows of a piece of dw are complete
+// at once; dh is summed over the pieces in fp32.
+//
+// P is rounded to bf16 (half a step, 2^-9 of each element, like any operand of the head's
+// products): its rounding errors are independent, so the sums over tokens or vocabulary they enter
+// carry a smaller one. Everything else is fp32 until an output is rounded.
+#include <math.h>
+
+#include "mma16.hpp"
+
+namespace puro {
+namespace {
+
+using namespace mma16;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// A token has a target where the target lies in the vocabulary.
+__device__ __forceinline__ bool has_target(int64_t y, int64_t vocab) { return y >= 0 && y < vocab; }
+
+// ------------------------------------------------------------------ forward
+struct Stat {
+  float m, s;  // maximum of the logits times log2 e, and sum of exp2(. - m)
+};
+
+__device__ __forceinline__ Stat join(Stat a, Stat b) {
+  const float m = fmaxf(a.m, b.m);
+  // nothing but -inf on either side: the sum stays empty
+  const float base = m == -INFINITY ? 0.0f : m;
+  return {m, a.s * exp2f(a.m - base) + b.s * exp2f(b.m - base)};
+}
+
+__device__ __forceinline__ float quarters_max(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t m = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+  const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float quarters_sum(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t s = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(s, s, false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// stats [tiles of the vocabulary][tokens]; at [tokens]: the target's logit, where there is one
+template <class C>
+__global__ __launch_bounds__(C::kThreads) void xent_stats_kernel(
+    Operand h, Operand w, const int64_t* __restrict__ targets, int64_t tiles_i, int64_t tiles_j,
+    Stat* __restrict__ stats, float* __restrict__ at) {
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kStageBytes];
+  int64_t ti, tj;
+  tile_at(regroup(blockIdx.x, tiles_i * tiles_j), tiles_i, tiles_j, 4, ti, tj);
+  const int64_t i0 = uniform64(ti * C::BM), j0 = uniform64(tj * C::BN);
+  const int64_t nk = (h.cols + kChunk - 1) / kChunk;
+  v4f acc[C::MI][C::NJ];
+  multiply<C>(h, w, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  const int G = lane >> 4, r = lane & 15;
+  const int64_t col = j0 + wn * C::WN + 4 * G;
+  if (j0 + C::BN > w.rows) {  // columns behind the vocabulary
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < C::NJ; ++nj)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (col + 16 * nj + k >= w.rows) acc[mi][nj][k] = -INFINITY;
+  }
+  __syncthreads();  // the stages are free
+  lds_f32* sh = (lds_f32*)s0;  // [WAVES_N][BM][2]
+#pragma unroll
+  for (int mi = 0; mi < C::MI; ++mi) {
+    const int row = wm * C::WM + 16 * mi + r;
+    float m = acc[mi][0][0];
+#pragma unroll
+    for (int nj = 0; nj < C::NJ; ++nj)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m = fmaxf(m, acc[mi][nj][k]);
+    m = quarters_max(m) * kLog2e;
+    const float base = m == -INFINITY ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll
+    for (int nj = 0; nj < C::NJ; ++nj)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        s += __builtin_amdgcn_exp2f(fmaf(acc[mi][nj][k], kLog2e, -base));
+    s = quarters_sum(s);
+    if (G == 0) {
+      sh[2 * (wn * C::BM + row)] = m;
+      sh[2 * (wn * C::BM + row) + 1] = s;
+    }
+    if (i0 + row < h.rows) {
+      const int64_t y = targets[i0 + row];
+      const int64_t d = y - col;
+      if (has_target(y, w.rows) && d >= 0 && d < C::WN && (d & 15) < 4) {
+        float l = 0.0f;
+#pragma unroll
+        for (int nj = 0; nj < C::NJ; ++nj)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (d == 16 * nj + k) l = acc[mi][nj][k];
+        at[i0 + row] = l;
+      }
+    }
+  }
+  __syncthreads();
+  for (int row = threadIdx.x; row < C::BM; row += C::kThreads) {
+    if (i0 + row >= h.rows) break;
+    Stat a = {sh[2 * row], sh[2 * row + 1]};
+#pragma unroll
+    for (int n = 1; n < C::WAVES_N; ++n)
+      a = join(a, Stat{sh[2 * (n * C::BM + row)], sh[2 * (n * C::BM + row) + 1]});
+    stats[tj * h.rows + i0 + row] = a;
+  }
+}
+
+// The tiles' statistics of `per` tokens a block (a power of two up to 64), 1024 / per threads to a
+// token: consecutive threads read consecutive tokens.
+constexpr int kJoinThreads = 1024;
+__global__ __launch_bounds__(kJoinThreads) void xent_join_kernel(
+    const Stat* __restrict__ stats, const float* __restrict__ at,
+    const int64_t* __restrict__ targets, int64_t tokens, int64_t vocab, int64_t tiles, int per,
+    float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ Stat sh[kJoinThreads];
+  const int parts = kJoinThreads / per;
+  const int tok = threadIdx.x % per, part = threadIdx.x / per;
+  const int64_t t = int64_t(blockIdx.x) * per + tok;
+  Stat a = {-INFINITY, 0.0f};
+  if (t < tokens)
+    for (int64_t n = part; n < tiles; n += parts) a = join(a, stats[n * tokens + t]);
+  sh[threadIdx.x] = a;
+  __syncthreads();
+  for (int p = parts / 2; p >= 1; p /= 2) {
+    if (part < p) sh[threadIdx.x] = join(sh[threadIdx.x], sh[threadIdx.x + p * per]);
+    __syncthreads();
+  }
+  if (part != 0 || t >= tokens) return;
+  const Stat all = sh[threadIdx.x];
+  const bool has = has_target(targets[t], vocab);
+  const float rest = log2f(all.s);
+  lse[t] = has ? (all.m + rest) * kLn2 : 0.0f;
+  // the target's logit goes against the maximum first: where it is the maximum they cancel exactly
+  loss[t] = has ? ((all.m - at[t] * kLog2e) + rest) * kLn2 : 0.0f;
+}
+
+// ------------------------------------------------------------------ operands laid out
+// src [rows][cols] (row stride ld, any alignment) -> dst [rows][ldd], zeros behind the columns; a
+// row whose token has no target becomes zeros (targets NULL: every row is kept), so that nothing it
+// holds, not even a NaN, meets the zero it has in P.
+__global__ __launch_bounds__(256) void xent_rows_kernel(const uint16_t* __restrict__ src,
+                                                        int64_t rows, int64_t cols, int64_t ld,
+                                                        const int64_t* __restrict__ targets,
+                                                        int64_t vocab, uint16_t* __restrict__ dst,
+                                                        int64_t ldd) {
+  const int64_t groups = ldd / 8;
+  const bool whole = ld % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+  for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < rows * groups;
+       n += int64_t(gridDim.x) * 256) {
+    const int64_t row = n / groups, c = (n - row * groups) * 8;
+    v4i v = {0, 0, 0, 0};
+    if (targets == nullptr || has_target(targets[row], vocab)) {
+      const uint16_t* p = src + row * ld + c;
+      if (whole && c + 8 <= cols) {
+        v = *reinterpret_cast<const v4i*>(p);
+      } else {
+        for (int k = 0; k < 8; ++k)
+          if (c + k < cols) v[k / 2] |= static_cast<int>(uint32_t(p[k]) << (16 * (k & 1)));
+      }
+    }
+    *reinterpret_cast<v4i*>(dst + row * ldd + c) = v;
+  }
+}
+
+// ------------------------------------------------------------------ backward
+// A piece of P: vocabulary [v0, v0 + w.rows) (w is the piece's weights), P [tokens][ldp]; columns
+// behind the vocabulary are written as zeros to the end of their tile, or up to ldp.
+template <class C>
+__global__ __launch_bounds__(C::kThreads) void xent_p_kernel(
+    Operand h, Operand w, const int64_t* __restrict__ targets, int64_t v0, int64_t vocab,
+    const float* __restrict__ lse, const float* __restrict__ dloss,
+    const float* __restrict__ dlse, int64_t tiles_i, int64_t tiles_j, uint16_t* __restrict__ P,
+    int64_t ldp) {
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kStageBytes];
+  int64_t ti, tj;
+  tile_at(regroup(blockIdx.x, tiles_i * tiles_j), tiles_i, tiles_j, 4, ti, tj);
+  const int64_t i0 = uniform64(ti * C::BM), j0 = uniform64(tj * C::BN);
+  const int64_t nk = (h.cols + kChunk - 1) / kChunk;
+  v4f acc[C::MI][C::NJ];
+  multiply<C>(h, w, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
+  __syncthreads();
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  const int G = lane >> 4, r = lane & 15;
+  static_assert(Region<C>::kBytes * C::kWaves <= 2 * C::kStageBytes, "regions fit the stages");
+  constexpr int kFirst = C::kStageBytes / Region<C>::kBytes;  // regions of the first stage
+  const Region<C> region(wave < kFirst ? (lds_u8*)s0 : (lds_u8*)s1,
+                         wave < kFirst ? wave : wave - kFirst, lane);
+  const int64_t col = j0 + wn * C::WN + 4 * G;
+  const bool edge = j0 + C::BN > w.rows;
+#pragma unroll
+  for (int mi = 0; mi < C::MI; ++mi) {
+    const int64_t t = i0 + wm * C::WM + 16 * mi + r;
+    float base = 0.0f, every = 0.0f, hot = 0.0f;
+    int64_t d = -1;
+    bool has = false;
+    if (t < h.rows) {
+      const int64_t y = targets[t];
+      has = has_target(y, vocab);
+      if (has) {
+        base = lse[t] * kLog2e;
+        hot = dloss[t];
+        every = dlse == nullptr ? hot : hot + dlse[t];
+        d = y - v0 - col;
+      }
+    }
+    const bool here = d >= 0 && d < C::WN && (d & 15) < 4;
+#pragma unroll
+    for (int nj = 0; nj < C::NJ; ++nj) {
+      v4f p;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        p[k] = every * __builtin_amdgcn_exp2f(fmaf(acc[mi][nj][k], kLog2e, -base));
+        if (!has || (edge && col + 16 * nj + k >= w.rows)) p[k] = 0.0f;
+      }
+      if (here) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (d == 16 * nj + k) p[k] -= hot;
+      }
+      region.put(mi, nj, v2i{static_cast<int>(pack_bf16x2(p[0], p[1])),
+                             static_cast<int>(pack_bf16x2(p[2], p[3]))});
+    }
+  }
+  region.settle();
+  const int64_t q0 = j0 + wn * C::WN;
+  if (q0 >= ldp) return;
+#pragma unroll
+  for (int n = 0; n < C::WM / 8; ++n) {
+    const v4i v = region.row8(n);
+    const int64_t t = i0 + wm * C::WM + 8 * n + (lane >> 3);
+    if (t < h.rows) *reinterpret_cast<v4i*>(P + t * ldp + q0 + 8 * (lane & 7)) = v;
+  }
+}
+
+// Where a product's tiles end. kind: kBf16 rounds to bf16 [rows][ld]; kFp32 stores or adds fp32
+// [rows][ld]; kJoin adds the fp32 sums of the pieces before this one and rounds to bf16.
+enum Out : int { kBf16, kFp32, kJoin };
+struct Dest {
+  int kind;
+  bool add;         // kFp32: add to what is there
+  float* f;         // kFp32, kJoin: [split][rows][ldf]
+  uint16_t* b;      // kBf16, kJoin: [rows][ldb]
+  int64_t rows, cols, ldf, ldb, split_stride;
+};
+
+// C = A B over split s of `splits` of the reduction.
+template <class C>
+__global__ __launch_bounds__(C::kThreads) void xent_product_kernel(Operand A, Operand B,
+                                                                   int64_t tiles_i,
+                                                                   int64_t tiles_j, int splits,
+                                                                   int64_t band, Dest out) {
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kStageBytes];
+  const int64_t tiles = tiles_i * tiles_j;
+  const int64_t b = regroup(blockIdx.x, tiles * splits);
+  const int64_t split = b / tiles;
+  int64_t ti, tj;
+  tile_at(b - split * tiles, tiles_i, tiles_j, band, ti, tj);
+  const int64_t i0 = uniform64(ti * C::BM), j0 = uniform64(tj * C::BN);
+  const int64_t k = C::kTransA ? A.rows : A.cols;
+  const int64_t nk = (k + kChunk - 1) / kChunk;
+  const int64_t c0 = uniform64(nk * split / splits), c1 = uniform64(nk * (split + 1) / splits);
+  v4f acc[C::MI][C::NJ];
+  multiply<C>(A, B, i0, j0, c0, c1, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  const int G = lane >> 4, r = lane & 15;
+  const int64_t r0 = i0 + wm * C::WM, q0 = j0 + wn * C::WN;
+  if (out.kind != kBf16) {
+    float* f = out.f + split * out.split_stride;
+    const bool whole = out.ldf % 4 == 0;
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < C::NJ; ++nj) {
+        const int64_t row = r0 + 16 * mi + r, col = q0 + 16 * nj + 4 * G;
+        if (row >= out.rows || col >= out.cols) continue;
+        float* p = f + row * out.ldf + col;
+        if (whole) {  // the columns behind out.cols lie in the row's padding, or there are none
+          v4f* q = reinterpret_cast<v4f*>(p);
+          if (out.kind == kJoin)
+            acc[mi][nj] += *q;
+          else
+            *q = out.add ? *q + acc[mi][nj] : acc[mi][nj];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + e < out.cols) p[e] = out.add ? p[e] + acc[mi][nj][e] : acc[mi][nj][e];
+        }
+      }
+    if (out.kind == kFp32) return;
+  }
+  __syncthreads();
+  constexpr int kFirst = C::kStageBytes / Region<C>::kBytes;
+  const Region<C> region(wave < kFirst ? (lds_u8*)s0 : (lds_u8*)s1,
+                         wave < kFirst ? wave : wave - kFirst, lane);
+#pragma unroll
+  for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+    for (int nj = 0; nj < C::NJ; ++nj)
+      region.put(mi, nj, v2i{static_cast<int>(pack_bf16x2(acc[mi][nj][0], acc[mi][nj][1])),
+                             static_cast<int>(pack_bf16x2(acc[mi][nj][2], acc[mi][nj][3]))});
+  region.settle();
+  const bool whole = out.ldb % 8 == 0;
+#pragma unroll
+  for (int n = 0; n < C::WM / 8; ++n) {
+    const v4i v = region.row8(n);
+    const int64_t row = r0 + 8 * n + (lane >> 3), col = q0 + 8 * (lane & 7);
+    if (row >= out.rows || col >= out.cols) continue;
+    uint16_t* p = out.b + row * out.ldb + col;
+    if (whole) {
+      *reinterpret_cast<v4i*>(p) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (col + e < out.cols) p[e] = static_cast<uint16_t>(uint32_t(v[e / 2]) >> (16 * (e & 1)));
+    }
+  }
+}
+
+// The sum of `splits` partial products, rounded to bf16: [rows][ldf] fp32 each -> [rows][cols].
+__global__ __launch_bounds__(256) void xent_sum_kernel(const float* __restrict__ f, int splits,
+                                                       int64_t split_stride, int64_t rows,
+                                                       int64_t cols, int64_t ldf,
+                                                       uint16_t* __restrict__ out) {
+  const int64_t groups = ldf / 4;
+  for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < rows * groups;
+       n += int64_t(gridDim.x) * 256) {
+    const int64_t row = n / groups, c = (n - row * groups) * 4;
+    v4f a = *reinterpret_cast<const v4f*>(f + row * ldf + c);
+    for (int s = 1; s < splits; ++s)
+      a += *reinterpret_cast<const v4f*>(f + s * split_stride + row * ldf + c);
+    const uint32_t lo = pack_bf16x2(a[0], a[1]), hi = pack_bf16x2(a[2], a[3]);
+    uint16_t* p = out + row * cols + c;
+    if (cols % 4 == 0) {
+      if (c < cols) *reinterpret_cast<uint2*>(p) = uint2{lo, hi};
+    } else {
+      const uint32_t v[2] = {lo, hi};
+      for (int e = 0; e < 4; ++e)
+        if (c + e < cols) p[e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1)));
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void xent_zero_kernel(uint32_t* __restrict__ p, int64_t n4,
+                                                        uint16_t* __restrict__ tail) {
+  for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < n4; n += int64_t(gridDim.x) * 256)
+    p[n] = 0;
+  if (tail != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *tail = 0;
+}
+
+// ------------------------------------------------------------------ host
+constexpr int64_t kMaxTokens = PURO_XENT_MAX_TOKENS;
+constexpr int64_t kMaxD = PURO_XENT_MAX_D;
+constexpr int64_t kFill = 256;                       // compute units: tiles that fill the chip
+constexpr int64_t kPieceBytes = int64_t(512) << 20;  // of a piece of P
+
+inline int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+inline int64_t tiles_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
+inline unsigned stream_grid(int64_t n) {
+  const int64_t b = tiles_of(n, 256);
+  return static_cast<unsigned>(b < 1 ? 1 : b > 8192 ? 8192 : b);
+}
+
+// What a matrix needs to be an operand as it lies.
+inline bool direct(const void* p, int64_t cols, int64_t ld) {
+  return aligned16(p) && cols % 8 == 0 && ld % 8 == 0 && ld <= kMaxLd;
+}
+
+puro_status check_sizes(int64_t tokens, int64_t d, int64_t vocab, int64_t ldh, int64_t ldw) {
+  if (tokens < 0 || tokens > kMaxTokens || d < 1 || d > kMaxD || vocab < 1 || vocab > kMaxDim)
+    return PURO_ERR_SHAPE;
+  if (ldh < d || ldw < d || ldh > kMaxDim || ldw > kMaxDim) return PURO_ERR_SHAPE;
+  return PURO_OK;
+}
+
+inline puro_status check_elements(const void* p, size_t size) {
+  if (p == nullptr) return PURO_ERR_NULL;
+  return reinterpret_cast<uintptr_t>(p) % size ? PURO_ERR_ALIGN : PURO_OK;
+}
+
+// The workspace's parts, each 256-byte aligned, dealt out in order.
+struct Carver {
+  uint8_t* base;
+  int64_t used = 0;
+  template <class T>
+  T* take(int64_t n) {
+    T* p = reinterpret_cast<T*>(base + used);
+    used += up(n * static_cast<int64_t>(sizeof(T)), 256);
+    return p;
+  }
+};
+
+// Tile shapes: 64x256 for up to 64 rows (one read of the other operand), 256x256 where such tiles
+// fill the chip, 128x128 below.
+enum Shape { kFlat, kBig, kSmall };
+inline Shape pick(int64_t i, int64_t j) {
+  if (i <= 64) return kFlat;
+  return tiles_of(i, 256) * tiles_of(j, 256) >= kFill ? kBig : kSmall;
+}
+inline int64_t bm_of(Shape s) { return s == kFlat ? 64 : s == kBig ? 256 : 128; }
+inline int64_t bn_of(Shape s) { return s == kSmall ? 128 : 256; }
+template <bool kTransA, bool kTransB>
+using FlatTile = Tile<64, 256, 1, 4, kTransA, kTransB, false>;
+template <bool kTransA, bool kTransB>
+using BigTile = Tile<256, 256, 2, 4, kTransA, kTransB, false>;
+template <bool kTransA, bool kTransB>
+using SmallTile = Tile<128, 128, 2, 2, kTransA, kTransB, false>;
+
+struct FwdPlan {
+  bool copy_h, copy_w;
+  int64_t ldp;  // row stride of copies
+  Shape shape;
+  int64_t tiles_i, tiles_j;
+  Stat* stats;
+  float* at;
+  uint16_t *h, *w;
+  int64_t bytes;
+};
+
+FwdPlan plan_fwd(const puro_linear_xent& x, void* ws) {
+  FwdPlan p;
+  p.copy_h = !direct(x.h, x.d, x.ldh);
+  p.copy_w = !direct(x.w, x.d, x.ldw);
+  p.ldp = up(x.d, kChunk);
+  p.shape = pick(x.tokens, x.vocab);
+  p.tiles_i = tiles_of(x.tokens, bm_of(p.shape));
+  p.tiles_j = tiles_of(x.vocab, bn_of(p.shape));
+  Carver c{static_cast<uint8_t*>(ws)};
+  p.stats = c.take<Stat>(p.tiles_j * x.tokens);
+  p.at = c.take<float>(x.tokens);
+  p.h = c.take<uint16_t>(p.copy_h ? x.tokens * p.ldp : 0);
+  p.w = c.take<uint16_t>(p.copy_w ? x.vocab * p.ldp : 0);
+  p.bytes = c.used;
+  return p;
+}
+
+void copy_rows(const void* src, int64_t rows, int64_t cols, int64_t ld, const int64_t* targets,
+               int64_t vocab, uint16_t* dst, int64_t ldd, hipStream_t s) {
+  hipLaunchKernelGGL(xent_rows_kernel, dim3(stream_grid(rows * (ldd / 8))), dim3(256), 0, s,
+                     static_cast<const uint16_t*>(src), rows, cols, ld, targets, vocab, dst, ldd);
+}
+
+inline Operand operand(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  return {static_cast<const uint8_t*>(p), rows, cols, ld};
+}
+
+puro_status check_fwd(const puro_linear_xent* x) {
+  if (x == nullptr) return PURO_ERR_NULL;
+  PURO_TRY(check_sizes(x->tokens, x->d, x->vocab, x->ldh, x->ldw));
+  if (x->tokens == 0) return PURO_OK;
+  PURO_TRY(check_elements(x->h, 2));
+  PURO_TRY(check_elements(x->w, 2));
+  PURO_TRY(check_elements(x->targets, 8));
+  PURO_TRY(check_elements(x->loss, 4));
+  PURO_TRY(check_elements(x->lse, 4));
+  const Shape s = pick(x->tokens, x->vocab);
+  if (!grid_ok(tiles_of(x->tokens, bm_of(s)) * tiles_of(x->vocab, bn_of(s)), 512))
+    return PURO_ERR_SHAPE;
+  return PURO_OK;
+}
+
+template <class C>
+void launch_stats(const FwdPlan& p, const Operand& h, const Operand& w, const int64_t* targets,
+                  hipStream_t s) {
+  hipLaunchKernelGGL(xent_stats_kernel<C>, dim3(static_cast<uint32_t>(p.tiles_i * p.tiles_j)),
+                     dim3(C::kThreads), 0, s, h, w, targets, p.tiles_i, p.tiles_j, p.stats, p.at);
+}
+
+struct BwdPlan {
+  bool copy_w;
+  int64_t ldh, ldw_copy;
+  int64_t piece, pieces;  // columns of a piece of P (its row stride), pieces
+  Shape p_shape, dh_shape, dw_shape;
+  int splits;
+  int64_t ldf;
+  uint16_t *h, *w, *P;
+  float* dh;
+  int64_t bytes;
+};
+
+BwdPlan plan_bwd(const puro_linear_xent_grad& x, void* ws) {
+  BwdPlan p;
+  p.copy_w = !direct(x.w, x.d, x.ldw);
+  p.ldh = up(x.d, kChunk);
+  p.ldw_copy = up(x.d, kChunk);
+  const int64_t most = up(kPieceBytes / (2 * (x.tokens > 0 ? x.tokens : 1)) + 1, 256);
+  p.pieces = tiles_of(x.vocab, most < 4096 ? 4096 : most > (1 << 20) ? 1 << 20 : most);
+  p.piece = up(tiles_of(x.vocab, p.pieces), 256);
+  p.pieces = tiles_of(x.vocab, p.piece);
+  p.p_shape = pick(x.tokens, p.piece);
+  p.dw_shape = tiles_of(p.piece, 256) * tiles_of(x.d, 256) >= kFill ? kBig : kSmall;
+  // dh: a small output with a long reduction, split until its tiles fill the chip
+  p.dh_shape = x.tokens <= 64 ? kFlat : kBig;
+  if (p.dh_shape == kBig && tiles_of(x.tokens, 256) * tiles_of(x.d, 256) * (p.piece / 512) < kFill)
+    p.dh_shape = kSmall;
+  const int64_t tiles =
+      tiles_of(x.tokens, bm_of(p.dh_shape)) * tiles_of(x.d, bn_of(p.dh_shape));
+  int64_t splits = tiles > 0 ? kFill / tiles : 1;
+  const int64_t longest = p.piece / 512;  // eight chunks a split at least
+  if (splits > longest) splits = longest;
+  if (splits < 1) splits = 1;
+  p.splits = static_cast<int>(splits);
+  p.ldf = up(x.d, 4);
+  Carver c{static_cast<uint8_t*>(ws)};
+  p.h = c.take<uint16_t>(x.tokens * p.ldh);
+  p.w = c.take<uint16_t>(p.copy_w ? x.vocab * p.ldw_copy : 0);
+  p.P = c.take<uint16_t>(x.tokens * p.piece);
+  p.dh = c.take<float>(x.dh != nullptr && (p.splits > 1 || p.pieces > 1)
+                           ? p.splits * x.tokens * p.ldf : 0);
+  p.bytes = c.used;
+  return p;
+}
+
+puro_status check_bwd(const puro_linear_xent_grad* x) {
+  if (x == nullptr) return PURO_ERR_NULL;
+  PURO_TRY(check_sizes(x->tokens, x->d, x->vocab, x->ldh, x->ldw));
+  if (x->dw_type != PURO_TYPE_BF16 && x->dw_type != PURO_TYPE_FP32) return PURO_ERR_ARG;
+  if (x->accumulate != 0 && (x->accumulate != 1 || x->dw_type != PURO_TYPE_FP32))
+    return PURO_ERR_ARG;
+  if (x->dw != nullptr) PURO_TRY(check_ptr(x->dw, false));
+  if (x->tokens == 0) return PURO_OK;
+  PURO_TRY(check_elements(x->h, 2));
+  PURO_TRY(check_elements(x->w, 2));
+  PURO_TRY(check_elements(x->targets, 8));
+  PURO_TRY(check_elements(x->lse, 4));
+  PURO_TRY(check_elements(x->dloss, 4));
+  if (x->dlse != nullptr) PURO_TRY(check_elements(x->dlse, 4));
+  if (x->dh != nullptr) PURO_TRY(check_ptr(x->dh, false));
+  const BwdPlan p = plan_bwd(*x, nullptr);
+  if (!grid_ok(tiles_of(x->tokens, 64) * tiles_of(p.piece, 128), 512) ||
+      !grid_ok(tiles_of(p.piece, 128) * tiles_of(x->d, 128), 512) ||
+      !grid_ok(tiles_of(x->tokens, 64) * tiles_of(x->d, 128) * p.splits, 512))
+    return PURO_ERR_SHAPE;
+  return PURO_OK;
+}
+
+template <class C>
+void launch_p(const BwdPlan& p, const puro_linear_xent_grad& x, const Operand& h, const Operand& w,
+              int64_t v0, hipStream_t s) {
+  // tiles that begin inside the vocabulary: they reach the end of its last chunk of 64
+  const int64_t ti = tiles_of(h.rows, C::BM), tj = tiles_of(w.rows, C::BN);
+  hipLaunchKernelGGL(xent_p_kernel<C>, dim3(static_cast<uint32_t>(ti * tj)), dim3(C::kThreads), 0,
+                     s, h, w, x.targets, v0, x.vocab, x.lse, x.dloss, x.dlse, ti, tj, p.P,
+                     p.piece);
+}
+
+template <class C>
+void launch_product(const Operand& A, const Operand& B, int splits, int64_t band, const Dest& out,
+                    hipStream_t s) {
+  const int64_t ti = tiles_of(out.rows, C::BM), tj = tiles_of(out.cols, C::BN);
+  hipLaunchKernelGGL(xent_product_kernel<C>, dim3(static_cast<uint32_t>(ti * tj * splits)),
+                     dim3(C::kThreads), 0, s, A, B, ti, tj, splits, band, out);
+}
+
+}  // namespace
+}  // namespace puro
+
+using namespace puro;
+
+extern "C" int64_t puro_linear_xent_fwd_workspace(const puro_linear_xent* desc) {
+  if (check_fwd(desc) != PURO_OK || desc->tokens == 0) return 0;
+  return plan_fwd(*desc, nullptr).bytes;
+}
+
+extern "C" puro_status puro_linear_xent_fwd(const puro_linear_xent* desc, void* workspace,
+                                            void* stream) {
+  PURO_TRY(check_fwd(desc));
+  const puro_linear_xent& x = *desc;
+  if (x.tokens == 0) return PURO_OK;
+  PURO_TRY(check_ptr(workspace, false));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const FwdPlan p = plan_fwd(x, workspace);
+  Operand h = operand(x.h, x.tokens, x.d, x.ldh), w = operand(x.w, x.vocab, x.d, x.ldw);
+  if (p.copy_h) {
+    copy_rows(x.h, x.tokens, x.d, x.ldh, nullptr, 0, p.h, p.ldp, s);
+    h = operand(p.h, x.tokens, p.ldp, p.ldp);
+  }
+  if (p.copy_w) {
+    copy_rows(x.w, x.vocab, x.d, x.ldw, nullptr, 0, p.w, p.ldp, s);
+    w = operand(p.w, x.vocab, p.ldp, p.ldp);
+  }
+  if (p.shape == kFlat)
+    launch_stats<FlatTile<false, false>>(p, h, w, x.targets, s);
+  else if (p.shape == kBig)
+    launch_stats<BigTile<false, false>>(p, h, w, x.targets, s);
+  else
+    launch_stats<SmallTile<false, false>>(p, h, w, x.targets, s);
+  int per = 64;
+  while (per > 1 && per / 2 >= x.tokens) per /= 2;
+  hipLaunchKernelGGL(xent_join_kernel, dim3(static_cast<uint32_t>(tiles_of(x.tokens, per))),
+                     dim3(kJoinThreads), 0, s, p.stats, p.at, x.targets, x.tokens, x.vocab,
+                     p.tiles_j, per, x.loss, x.lse);
+  return launch_status();
+}
+
+extern "C" int64_t puro_linear_xent_bwd_workspace(const puro_linear_xent_grad* desc) {
+  if (check_bwd(desc) != PURO_OK || desc->tokens == 0) return 0;
+  return plan_bwd(*desc, nullptr).bytes;
+}
+
+extern "C" puro_status puro_linear_xent_bwd(const puro_linear_xent_grad* desc, void* workspace,
+                                            void* stream) {
+  PURO_TRY(check_bwd(desc));
+  const puro_linear_xent_grad& x = *desc;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (x.dh == nullptr && x.dw == nullptr) return PURO_OK;
+  if (x.tokens == 0) {
+    if (x.dw == nullptr || x.accumulate) return PURO_OK;
+    const int64_t bytes = x.vocab * x.d * (x.dw_type == PURO_TYPE_FP32 ? 4 : 2);
+    uint8_t* p = static_cast<uint8_t*>(x.dw);
+    hipLaunchKernelGGL(xent_zero_kernel, dim3(stream_grid(bytes / 4)), dim3(256), 0, s,
+                       reinterpret_cast<uint32_t*>(p), bytes / 4,
+                       bytes % 4 ? reinterpret_cast<uint16_t*>(p + bytes - 2) : nullptr);
+    return launch_status();
+  }
+  PURO_TRY(check_ptr(workspace, false));
+  const BwdPlan p = plan_bwd(x, workspace);
+  copy_rows(x.h, x.tokens, x.d, x.ldh, x.targets, x.vocab, p.h, p.ldh, s);
+  const Operand h = operand(p.h, x.tokens, p.ldh, p.ldh);
+  Operand w = operand(x.w, x.vocab, x.d, x.ldw);
+  if (p.copy_w) {
+    copy_rows(x.w, x.vocab, x.d, x.ldw, nullptr, 0, p.w, p.ldw_copy, s);
+    w = operand(p.w, x.vocab, p.ldw_copy, p.ldw_copy);
+  }
+  const bool f32 = x.dw_type == PURO_TYPE_FP32;
+  for (int64_t n = 0; n < p.pieces; ++n) {
+    const int64_t v0 = n * p.piece;
+    const int64_t vn = x.vocab - v0 < p.piece ? x.vocab - v0 : p.piece;
+    const Operand wp = operand(w.p + 2 * v0 * w.ld, vn, w.cols, w.ld);
+    if (p.p_shape == kFlat)
+      launch_p<FlatTile<false, false>>(p, x, h, wp, v0, s);
+    else if (p.p_shape == kBig)
+      launch_p<BigTile<false, false>>(p, x, h, wp, v0, s);
+    else
+      launch_p<SmallTile<false, false>>(p, x, h, wp, v0, s);
+    if (x.dw != nullptr) {
+      const Operand a = operand(p.P, x.tokens, p.piece, p.piece);
+      Dest out = {};
+      out.kind = f32 ? kFp32 : kBf16;
+      out.add = x.accumulate != 0;
+      out.f = f32 ? static_cast<float*>(x.dw) + v0 * x.d : nullptr;
+      out.b = f32 ? nullptr : static_cast<uint16_t*>(x.dw) + v0 * x.d;
+      out.rows = vn;
+      out.cols = out.ldf = out.ldb = x.d;
+      if (p.dw_shape == kBig)
+        launch_product<BigTile<true, true>>(a, h, 1, 4, out, s);
+      else
+        launch_product<SmallTile<true, true>>(a, h, 1, 8, out, s);
+    }
+    if (x.dh != nullptr) {
+      // the piece's reduction: its columns of P (zeros behind the vocabulary) and rows of w
+      const Operand a = operand(p.P, x.tokens, up(vn, kChunk), p.piece);
+      const bool once = p.splits == 1;
+      Dest out = {};
+      out.kind = !once || n + 1 < p.pieces ? kFp32 : p.pieces == 1 ? kBf16 : kJoin;
+      out.add = n > 0;
+      out.f = p.dh;
+      out.b = static_cast<uint16_t*>(x.dh);
+      out.rows = x.tokens;
+      out.cols = x.d;
+      out.ldf = p.ldf;
+      out.ldb = x.d;
+      out.split_stride = x.tokens * p.ldf;
+      if (p.dh_shape == kFlat)
+        launch_product<FlatTile<false, true>>(a, wp, p.splits, 4, out, s);
+      else if (p.dh_shape == kBig)
+        launch_product<BigTile<false, true>>(a, wp, p.splits, 4, out, s);
+      else
+        launch_product<SmallTile<false, true>>(a, wp, p.splits, 8, out, s);
+    }
+  }
+  if (x.dh != nullptr && p.splits > 1)
+    hipLaunchKernelGGL(xent_sum_kernel, dim3(stream_grid(x.tokens * (p.ldf / 4))), dim3(256), 0, s,
+                       p.dh, p.splits, x.tokens * p.ldf, x.tokens, x.d, p.ldf,
+                       static_cast<uint16_t*>(x.dh));
+  return launch_status();
+}

@@ -198,6 +198,12 @@ puro_status puro_hyperball_step(float* w, const float* u, int64_t numel, float l
 puro_status puro_hyperball_step_noalloc(float* w, const float* u, int64_t numel, float lr,
                                         const float* radius, void* w_bf16, void* stream);
 
+/* puro_hyperball_step with the update direction in bf16, as puro_newton_schulz writes it: each
+ * element widened exactly, the same kernels and results otherwise. */
+puro_status puro_hyperball_step_u16(float* w, const void* u, int64_t numel, float lr,
+                                    const float* radius, void* w_bf16, void* workspace,
+                                    void* stream);
+
 /* AdamW with decoupled weight decay (Loshchilov and Hutter), in place on fp32 state:
  *   m = b1*m + (1-b1)*g;  v = b2*v + (1-b2)*g^2
  *   p = p*(1 - lr*wd) - lr * (m/(1-b1^t)) / (sqrt(v/(1-b2^t)) + eps)
@@ -394,6 +400,101 @@ puro_status puro_swiglu_bwd(const void* dh, const void* gu, const void* guq, con
 puro_status puro_swiglu_bwd_fp8(const void* dh, const void* gu, const void* guq, const float* gus,
                                 int64_t rows, int64_t f, int pow2, void* dguq, float* dgus,
                                 void* dgutq, float* dguts, void* htq, float* hts, void* stream);
+
+/* ---------------------------------------------------------------- update direction
+ * The direction of the projected step (puro_hyperball_step_u16), for `count` matrices of one shape
+ * in the same launches: momentum of the gradient, orthogonalised by Newton-Schulz products.
+ *   m_out = beta m + (1 - beta) g                      (fp32; may be m itself)
+ *   v     = beta m_out + (1 - beta) g (nesterov = 1), or m_out (0), or g (m and m_out NULL)
+ *   X     = v / |v|_F                                  (a zero v stays zero: u = 0)
+ *   steps times: X = c[0] X + c[1] (XX')X + c[2] (XX')^2 X
+ *   u     = scale X                                    (bf16)
+ * The singular values of v come out near 1 (0.7 to 1.2 with the usual five steps of 3.4445, -4.7750,
+ * 2.0315) and its singular vectors stay. Products run on fp16 operands with fixed scales and fp32
+ * sums; after those five steps u is within about 1.5e-3 (2-norm, before its rounding to bf16) of the
+ * same steps in exact arithmetic. More steps of coefficients that do not converge amplify that by
+ * their slope. Coefficients that could leave the scales' range are refused (PURO_ERR_ARG): over
+ * singular values in [0, 1] X has to stay within 1.75 until the last step and 12 after it, and
+ * |c[0]| + |c[1]| x^2 + |c[2]| x^4 within 28 for the largest such x. An infinite or NaN element makes
+ * its matrix's u NaN.
+ * Matrices are dense row-major fp32 [rows][cols], aligned to 4 bytes (16 is faster), u to 2; the
+ * shorter side at most PURO_NS_MAX_SIDE, the longer at most PURO_NS_MAX_LONG, both of any size from 0
+ * (nothing is written then). Either all matrices of a call have a momentum or none. No output may
+ * overlap another matrix's data.
+ * `workspace`: puro_newton_schulz_workspace bytes (0 for sizes that are refused or empty). */
+#define PURO_NS_GROUP_MAX 64
+#define PURO_NS_MAX_STEPS 16
+#define PURO_NS_MAX_SIDE 16384
+#define PURO_NS_MAX_LONG (1 << 20)
+typedef struct {
+  const float* g;  /* gradient */
+  const float* m;  /* momentum, or NULL */
+  float* m_out;    /* new momentum, NULL with m */
+  void* u;         /* bf16 direction (output) */
+} puro_ns_item;
+typedef struct {
+  int steps;       /* 1 to PURO_NS_MAX_STEPS */
+  int nesterov;    /* 0 or 1 */
+  float beta;      /* 0 <= beta < 1 */
+  float scale;
+  float coefficients[3];
+} puro_newton_schulz_params;
+int64_t puro_newton_schulz_workspace(int64_t count, int64_t rows, int64_t cols);
+/* items: host array of `count` entries (0 <= count <= PURO_NS_GROUP_MAX, else PURO_ERR_ARG). */
+puro_status puro_newton_schulz(const puro_ns_item* items, int count, int64_t rows, int64_t cols,
+                               const puro_newton_schulz_params* hp, void* workspace, void* stream);
+
+/* ---------------------------------------------------------------- output head
+ * Softmax cross entropy of hidden states h [tokens][d] against a vocabulary, from the output head's
+ * weights w [vocab][d] (both bf16), in pieces of the vocabulary: the matrix of all logits
+ * l = h w' is never formed.
+ *   lse[t]  = log sum_v exp l[t][v]
+ *   loss[t] = lse[t] - l[t][targets[t]]
+ * A token whose target lies outside [0, vocab) has none (padding, a prompt): its loss and lse are 0,
+ * it contributes to no gradient, and its row of h may hold anything.
+ * Logits, sums and outputs are fp32; infinite and NaN logits give what the formulas give.
+ * h and w may have row strides (ldh, ldw >= d, in elements); they are read as they lie where their
+ * address is 16-byte aligned and d and the stride are multiples of 8, else from a copy that the call
+ * makes in its workspace. targets are 8-byte, fp32 vectors 4-byte aligned.
+ * tokens from 0 to PURO_XENT_MAX_TOKENS, d from 1 to PURO_XENT_MAX_D, vocab from 1 to 2^24.
+ * Sums run in an order fixed by the sizes and alignment alone, so results repeat exactly.
+ * `workspace`: 16-byte aligned device memory of the bytes that the call's _workspace function
+ * returns for the same structure (0 for one that is refused). */
+#define PURO_XENT_MAX_TOKENS (1 << 20)
+#define PURO_XENT_MAX_D 65536
+typedef struct {
+  int64_t tokens, d, vocab, ldh, ldw;
+  const void* h;
+  const void* w;
+  const int64_t* targets;  /* [tokens] */
+  float* loss;             /* [tokens] (output) */
+  float* lse;              /* [tokens] (output) */
+} puro_linear_xent;
+int64_t puro_linear_xent_fwd_workspace(const puro_linear_xent* desc);
+puro_status puro_linear_xent_fwd(const puro_linear_xent* desc, void* workspace, void* stream);
+
+/* Its backward pass, from the gradients of loss and (optional) lse:
+ *   P[t][v] = exp(l[t][v] - lse[t]) (dloss[t] + dlse[t]) - [v = targets[t]] dloss[t]
+ *   dh = P w (bf16 [tokens][d]),  dw = P' h (bf16 or fp32 [vocab][d]; with accumulate = 1, fp32
+ *   only, added to dw)
+ * The logits are multiplied out again; P is rounded to bf16 (its products sum in fp32). dh or dw may
+ * be NULL to leave that gradient out; both are dense and 16-byte aligned. Without tokens dw is
+ * written as zeros (or left, when accumulating). */
+typedef struct {
+  int64_t tokens, d, vocab, ldh, ldw;
+  int dw_type;             /* PURO_TYPE_* of dw */
+  int accumulate;
+  const void* h;
+  const void* w;
+  const int64_t* targets;
+  const float* lse;        /* the forward pass's */
+  const float* dloss;      /* [tokens] */
+  const float* dlse;       /* [tokens], or NULL for zeros */
+  void* dh;
+  void* dw;
+} puro_linear_xent_grad;
+int64_t puro_linear_xent_bwd_workspace(const puro_linear_xent_grad* desc);
+puro_status puro_linear_xent_bwd(const puro_linear_xent_grad* desc, void* workspace, void* stream);
 
 /* Debug mode: input checks on the device before every quantiser and GEMM.
  * At level 0 (the default) nothing is checked. At level 1 or more each quantiser and GEMM

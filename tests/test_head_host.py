@@ -1,0 +1,227 @@
+"""Refusals and host logic of the output head's cross entropy and of the orthogonalised direction, and
+their 64-bit forms against differences and closed forms (no GPU)."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+import head_ref
+
+FAKE = 0x10000
+NULL, SHAPE, ALIGN, ARG = 1, 2, 3, 5
+
+
+@pytest.fixture(scope="module")
+def L():
+    from blockwise_fp8_gemm_x128_amd import _lib
+    from blockwise_fp8_gemm_x128_amd.build import LIB_PATH, build
+    if not os.path.exists(LIB_PATH):
+        build(verbose=False)
+    return _lib.lib()
+
+
+def _fwd(L, ws=FAKE, **kw):
+    from blockwise_fp8_gemm_x128_amd._lib import PuroLinearXent
+    d = dict(tokens=4, d=64, vocab=100, ldh=64, ldw=64, h=FAKE, w=FAKE, targets=FAKE, loss=FAKE,
+             lse=FAKE)
+    d.update(kw)
+    return L.puro_linear_xent_fwd(ctypes.byref(PuroLinearXent(**d)), ws, None)
+
+
+def _bwd(L, ws=FAKE, **kw):
+    from blockwise_fp8_gemm_x128_amd._lib import PuroLinearXentGrad
+    d = dict(tokens=4, d=64, vocab=100, ldh=64, ldw=64, dw_type=0, accumulate=0, h=FAKE, w=FAKE,
+             targets=FAKE, lse=FAKE, dloss=FAKE, dlse=None, dh=FAKE, dw=FAKE)
+    d.update(kw)
+    return L.puro_linear_xent_bwd(ctypes.byref(PuroLinearXentGrad(**d)), ws, None)
+
+
+SIZES = [dict(tokens=-1), dict(tokens=(1 << 20) + 1), dict(d=0), dict(d=65537, ldh=65537, ldw=65537),
+         dict(vocab=0), dict(vocab=(1 << 24) + 1), dict(ldh=63), dict(ldw=63), dict(ldw=1 << 25)]
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd])
+@pytest.mark.parametrize("kw", SIZES)
+def test_xent_sizes(L, call, kw):
+    assert call(L, **kw) == SHAPE
+
+
+@pytest.mark.parametrize("call,names", [(_fwd, ("h", "w", "targets", "loss", "lse")),
+                                        (_bwd, ("h", "w", "targets", "lse", "dloss"))])
+def test_xent_pointers(L, call, names):
+    for n in names:
+        assert call(L, **{n: None}) == NULL, n
+        assert call(L, **{n: FAKE + 1}) == ALIGN, n
+    assert call(L, ws=None) == NULL
+    assert call(L, ws=FAKE + 8) == ALIGN
+
+
+def test_xent_bwd_arguments(L):
+    assert _bwd(L, dw_type=2) == ARG
+    assert _bwd(L, accumulate=2, dw_type=1) == ARG
+    assert _bwd(L, accumulate=1, dw_type=0) == ARG
+    assert _bwd(L, dh=FAKE + 8) == ALIGN
+    assert _bwd(L, dw=FAKE + 8) == ALIGN
+    assert _bwd(L, dlse=FAKE + 2) == ALIGN
+    # nothing asked for: nothing to do, whatever the workspace
+    assert _bwd(L, dh=None, dw=None, ws=None) == 0
+    # no tokens: only dw is written, and not when accumulating
+    assert _bwd(L, tokens=0, dw=None) == 0
+    assert _bwd(L, tokens=0, accumulate=1, dw_type=1) == 0
+    assert L.puro_linear_xent_fwd(None, FAKE, None) == NULL
+    assert L.puro_linear_xent_bwd(None, FAKE, None) == NULL
+
+
+def test_xent_without_tokens(L):
+    assert _fwd(L, tokens=0, h=None, targets=None, loss=None, lse=None, ws=None) == 0
+
+
+def test_xent_workspace(L):
+    from blockwise_fp8_gemm_x128_amd._lib import PuroLinearXent, PuroLinearXentGrad
+
+    def fwd(**kw):
+        d = dict(tokens=100, d=64, vocab=1000, ldh=64, ldw=64, h=FAKE, w=FAKE, targets=FAKE,
+                 loss=FAKE, lse=FAKE)
+        d.update(kw)
+        return L.puro_linear_xent_fwd_workspace(ctypes.byref(PuroLinearXent(**d)))
+
+    def bwd(**kw):
+        d = dict(tokens=100, d=64, vocab=1000, ldh=64, ldw=64, dw_type=0, accumulate=0, h=FAKE,
+                 w=FAKE, targets=FAKE, lse=FAKE, dloss=FAKE, dlse=None, dh=FAKE, dw=FAKE)
+        d.update(kw)
+        return L.puro_linear_xent_bwd_workspace(ctypes.byref(PuroLinearXentGrad(**d)))
+
+    assert fwd() > 0 and bwd() > 0
+    assert fwd(tokens=0) == 0 and fwd(d=0) == 0 and bwd(dw_type=7) == 0
+    # a copy of w where it cannot be read as it lies: an address, a stride or a width of its own
+    for kw in (dict(w=FAKE + 2), dict(ldw=65), dict(d=60, ldh=64, ldw=64)):
+        assert fwd(**kw) >= fwd() + 2 * 1000 * 60
+        assert bwd(**kw) >= bwd() + 2 * 1000 * 60
+    # the matrix of all logits is never there
+    assert fwd(tokens=8192, vocab=131072) < 8192 * 131072 // 16
+    assert bwd(tokens=8192, vocab=1 << 20) < 8192 * (1 << 20) // 8
+
+
+def _ns(L, count=1, rows=8, cols=8, ws=FAKE, items=None, **kw):
+    from blockwise_fp8_gemm_x128_amd._lib import PuroNewtonSchulzParams, PuroNsItem
+    d = dict(steps=5, nesterov=1, beta=0.95, scale=1.0,
+             coefficients=(ctypes.c_float * 3)(*head_ref.COEFFICIENTS))
+    d.update(kw)
+    if items is None:
+        items = [(FAKE, FAKE, FAKE, FAKE)] * max(count, 0)
+    arr = (PuroNsItem * max(len(items), 1))(*(PuroNsItem(*i) for i in items))
+    return L.puro_newton_schulz(arr, count, rows, cols, ctypes.byref(PuroNewtonSchulzParams(**d)),
+                                ws, None)
+
+
+def test_ns_refusals(L):
+    inf = float("inf")
+    assert _ns(L, rows=-1) == SHAPE and _ns(L, cols=-1) == SHAPE
+    assert _ns(L, rows=16385, cols=16385) == SHAPE
+    assert _ns(L, rows=4, cols=(1 << 20) + 1) == SHAPE
+    assert _ns(L, count=65) == ARG and _ns(L, count=-1) == SHAPE
+    for kw in (dict(steps=0), dict(steps=17), dict(nesterov=2), dict(beta=1.0), dict(beta=-0.1),
+               dict(beta=float("nan")), dict(scale=inf), dict(scale=float("nan"))):
+        assert _ns(L, **kw) == ARG, kw
+    for k in ((inf, 0, 0), (1.0, float("nan"), 0), (3.0, 0, 0), (30.0, 0.0, 0.0), (2.0, 2.0, 2.0)):
+        assert _ns(L, coefficients=(ctypes.c_float * 3)(*k)) == ARG, k
+    assert _ns(L, items=[(None, FAKE, FAKE, FAKE)]) == NULL
+    assert _ns(L, items=[(FAKE, FAKE, FAKE, None)]) == NULL
+    assert _ns(L, items=[(FAKE, FAKE, None, FAKE)]) == NULL
+    assert _ns(L, items=[(FAKE, None, FAKE, FAKE)]) == NULL
+    assert _ns(L, count=2, items=[(FAKE, FAKE, FAKE, FAKE), (FAKE, None, None, FAKE)]) == ARG
+    assert _ns(L, items=[(FAKE + 2, FAKE, FAKE, FAKE)]) == ALIGN
+    assert _ns(L, items=[(FAKE, FAKE, FAKE, FAKE + 1)]) == ALIGN
+    assert _ns(L, ws=None) == NULL and _ns(L, ws=FAKE + 8) == ALIGN
+    assert L.puro_newton_schulz(None, 1, 8, 8, None, FAKE, None) == NULL
+
+
+def test_ns_empty(L):
+    assert _ns(L, count=0, ws=None) == 0
+    assert _ns(L, rows=0, ws=None) == 0 and _ns(L, cols=0, ws=None) == 0
+    assert L.puro_newton_schulz_workspace(0, 8, 8) == 0
+    assert L.puro_newton_schulz_workspace(1, 0, 8) == 0
+    assert L.puro_newton_schulz_workspace(65, 8, 8) == 0
+    assert L.puro_newton_schulz_workspace(1, 8, 8) > 0
+
+
+def test_hyperball_u16_refusals(L):
+    f = L.puro_hyperball_step_u16
+    assert f(FAKE, FAKE, 6, 0.1, FAKE, FAKE, FAKE, None) == SHAPE
+    assert f(FAKE, FAKE, 8, float("nan"), FAKE, FAKE, FAKE, None) == ARG
+    assert f(FAKE, None, 8, 0.1, FAKE, FAKE, FAKE, None) == NULL
+    assert f(FAKE, FAKE + 8, 8, 0.1, FAKE, FAKE, FAKE, None) == ALIGN
+    assert f(FAKE, FAKE, 8, 0.1, FAKE, FAKE, None, None) == NULL
+    assert f(FAKE, FAKE, 0, 0.1, FAKE, FAKE, FAKE, None) == 0
+
+
+def test_binding_refuses_host_tensors():
+    from blockwise_fp8_gemm_x128_amd import PuroError, binding
+    h = torch.zeros((4, 8), dtype=torch.bfloat16)
+    y = torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(PuroError):
+        binding.puro_linear_xent_fwd(h, h, y)
+    with pytest.raises(PuroError):
+        binding.puro_linear_xent_bwd(h, h, y, torch.zeros(4), torch.zeros(4))
+    with pytest.raises(PuroError):
+        binding.puro_newton_schulz([torch.zeros((4, 8))])
+    assert binding.puro_newton_schulz([]) == []
+
+
+# ------------------------------------------------------------------ the 64-bit forms themselves
+def test_xent_gradients_against_differences():
+    gen = torch.Generator().manual_seed(3)
+    t, d, v = 5, 6, 9
+    h = torch.randn((t, d), generator=gen, dtype=torch.float64)
+    w = torch.randn((v, d), generator=gen, dtype=torch.float64)
+    y = torch.tensor([0, 8, -100, 3, 9])
+    dloss = torch.randn(t, generator=gen, dtype=torch.float64)
+    dlse = torch.randn(t, generator=gen, dtype=torch.float64)
+
+    def total(h, w):
+        loss, lse, _, _ = head_ref.xent_fwd(h, w, y)
+        return float((loss * dloss + lse * dlse).sum())
+
+    lse = head_ref.xent_fwd(h, w, y)[1]
+    dh, dw, _, _ = head_ref.xent_bwd(h, w, y, lse, dloss, dlse)
+    step = 1e-5
+    for x, g in ((h, dh), (w, dw)):
+        for i in range(x.numel()):
+            keep = float(x.view(-1)[i])
+            x.view(-1)[i] = keep + step
+            up = total(h, w)
+            x.view(-1)[i] = keep - step
+            down = total(h, w)
+            x.view(-1)[i] = keep
+            assert abs((up - down) / (2 * step) - float(g.reshape(-1)[i])) < 1e-8
+
+
+def test_xent_against_torch():
+    gen = torch.Generator().manual_seed(4)
+    h, w = (torch.randn((n, 16), generator=gen, dtype=torch.float64) for n in (7, 33))
+    y = torch.randint(0, 33, (7,), generator=gen)
+    loss, lse, _, _ = head_ref.xent_fwd(h, w, y)
+    want = torch.nn.functional.cross_entropy(h @ w.t(), y, reduction="none")
+    assert torch.allclose(loss, want, atol=1e-12, rtol=0)
+
+
+@pytest.mark.parametrize("shape", [(8, 8), (5, 17), (17, 5), (1, 9)])
+def test_ortho_is_its_polynomial_of_the_singular_values(shape):
+    gen = torch.Generator().manual_seed(5)
+    v = torch.randn(shape, generator=gen, dtype=torch.float64)
+    u, s, vt = torch.linalg.svd(v, full_matrices=False)
+    s = s / torch.linalg.vector_norm(s)
+    a, b, c = (float(torch.tensor(k, dtype=torch.float32)) for k in head_ref.COEFFICIENTS)
+    for _ in range(5):
+        s = a * s + b * s ** 3 + c * s ** 5
+    assert torch.allclose(head_ref.ortho(v), (u * s) @ vt, atol=1e-11, rtol=0)
+
+
+def test_ortho_default_coefficients_stay_in_range():
+    """What the fixed scales of the fp16 operands rest on: no step takes a value in [0, 1] above 1.21."""
+    x = torch.linspace(0, 1, 100001, dtype=torch.float64)
+    a, b, c = head_ref.COEFFICIENTS
+    for _ in range(16):
+        x = a * x + b * x ** 3 + c * x ** 5
+        assert float(x.abs().max()) < 1.21
