@@ -223,8 +223,9 @@ __device__ __forceinline__ void chunk_step(const lds_u8* stage, Fragments<C>& f,
 
 // The products of one tile over chunks [c0, c1) of the reduction, which has `nk` chunks in all.
 // Each instruction takes the B fragment as its row operand, so lane (G, r) receives row r, columns
-// 4 G .. 4 G + 3 of every 16x16 tile. On return other waves may still read the stages.
-template <class C>
+// 4 G .. 4 G + 3 of every 16x16 tile. On return other waves may still read the stages. kMore adds to
+// what acc holds instead of starting from zero.
+template <class C, bool kMore = false>
 __device__ __forceinline__ void multiply(const Operand& A, const Operand& B, int64_t i0,
                                          int64_t j0, int64_t c0, int64_t c1, int64_t nk,
                                          lds_u8* s0, lds_u8* s1, v4f (&acc)[C::MI][C::NJ]) {
@@ -243,10 +244,12 @@ __device__ __forceinline__ void multiply(const Operand& A, const Operand& B, int
   Fragments<C> f;
   f.fa.init(0, wm * C::WM, lane);
   f.fb.init(C::kBOff, wn * C::WN, lane);
+  if constexpr (!kMore) {
 #pragma unroll
-  for (int mi = 0; mi < C::MI; ++mi)
+    for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
-    for (int nj = 0; nj < C::NJ; ++nj) acc[mi][nj] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int nj = 0; nj < C::NJ; ++nj) acc[mi][nj] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
 
   auto issue_a = [&](lds_u8* st, int64_t c) {
     if (!kPingPong || wave / kIssuers == static_cast<int>(c & 1)) sa.issue(st, c, c == nk - 1);

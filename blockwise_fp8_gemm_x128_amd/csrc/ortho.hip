@@ -8,16 +8,28 @@
 // polynomial), so that A has the shorter side's size. A and its polynomial are symmetric: only
 // tiles on and below the diagonal are multiplied, and each is stored twice.
 //
+// Three ways through the steps, by the sides s <= l of the matrix:
+//
+// - s up to 128: all steps on A alone, in one block per matrix (ns_core_kernel), then one product with X.
+// - l of 1.5 s and more: three steps' polynomials are multiplied into one s x s matrix before it meets X,
+//   then two steps' (A <- P A P and Q <- P Q with P = a I + b A + c A A). 6 s^2 l + 14 s^3 operations
+//   for five steps against 15 s^2 l + 5 s^3, and X is read and written twice instead of five times.
+// - else step by step.
+//
 // Precision. The products run on fp16 operands with fp32 sums. fp16 instead of bf16 (the same
 // rate): every entry is at most a small constant, so no exponent range is needed, and fixed powers
-// of two (kX, kA, kB) keep entries far below the largest in fp16's normal range. What a rounding
-// of X adds in a direction of small singular values is amplified by a = 3.4 a step, as that
-// direction itself is, so the early steps' roundings count most: all but the last two steps keep X
-// as two halves, X = hi + lo, and form a X from both in fp32, while the product with X reads hi alone.
-// It may: the polynomial is large only where X's large directions are, so hi's rounding comes out of
-// it along those. Relative errors of u (2-norm, four spectra of 512 x 512 and 512 x 1536, all operands
-// rounded as here): 0.7 to 1.2e-3, against 1.2 to 12e-3 with X in one half throughout, 10 to
-// 57e-3 in bf16, and 1.7e-3 for the rounding of u itself to bf16.
+// of two (kX, kA, ..) keep entries far below the largest in fp16's normal range. What a rounding
+// adds in a direction of small singular values is amplified by a = 3.4 a step, as that direction
+// itself is, so the early steps' roundings count most. There X is kept as two halves, X = hi + lo,
+// and the multiple of X itself (a X, or a^3 X for three steps) is formed from both in fp32, while the
+// product with the rest of the polynomial reads hi alone. It may: that rest is large only where X's
+// large directions are, so hi's rounding comes out of it along those. In the last two steps, where
+// the multiple of X and the rest nearly cancel, the polynomial is rounded with its diagonal
+// instead. Relative errors of u in the 2-norm, over five spectra of 512 x 512 and 512 x 1536 with
+// all operands rounded as here: 0.7 to 1.5e-3 step by step, 1.3 to 2.4e-3 by three and two
+// (3 to 15e-3 by two and three, up to 0.3 by all five at once), against 1.2 to 12e-3 with X in one
+// half, 10 to 57e-3 in bf16, and 1.7e-3 for the rounding of u itself to bf16. All five at once, as
+// short sides take them, need two halves of every operand.
 #include <math.h>
 
 #include "mma16.hpp"
@@ -112,8 +124,7 @@ __global__ __launch_bounds__(kThreads) void ns_convert_kernel(Items it, int64_t 
                                                               int count_parts,
                                                               _Float16* __restrict__ hi,
                                                               _Float16* __restrict__ lo,
-                                                              int64_t hi_stride,
-                                                              int64_t lo_stride) {
+                                                              int64_t stride) {
   __shared__ double sh[kThreads / 64];
   const int n = blockIdx.y;
   double acc = 0.0;
@@ -123,8 +134,8 @@ __global__ __launch_bounds__(kThreads) void ns_convert_kernel(Items it, int64_t 
   const double f = ss == 0.0 ? 0.0 : double(kX) / sqrt(ss);
   const float* g = it.g[n];
   const float* m = it.mo[n];
-  hi += n * hi_stride;
-  lo += n * lo_stride;
+  hi += n * stride;
+  lo += n * stride;
   const int64_t groups = ldx / 4;
   for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < rows * groups;
        i += int64_t(gridDim.x) * kThreads) {
@@ -175,25 +186,35 @@ __device__ __forceinline__ void triangle_at(int t, int& i, int& j) {
   j = t - i * (i + 1) / 2;
 }
 
-// A symmetric product: A = X X' (kPoly false; kTrans: X' X), or the polynomial's matrix
-// b A + c A A, with a on the diagonal where `diagonal` says so (kPoly, X = A).
-template <class C, bool kPoly>
-__global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Batch x, _Float16* out,
-                                                                   int64_t out_stride, int64_t n,
-                                                                   int64_t ld, int tiles,
-                                                                   float a, float b, float c,
-                                                                   bool diagonal) {
+typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+
+// A symmetric matrix [n][ld] per item: out = f L R' + f1 M1 + f2 M2 + diag I, L R' symmetric (X X', or
+// L and R commuting symmetric matrices). Factors include the operands' and the result's scales.
+struct Symmetric {
+  Batch l, r;
+  _Float16* out;
+  const _Float16 *m1, *m2;  // or NULL
+  int64_t stride, n, ld;    // of out, m1 and m2
+  float f, f1, f2, diag;
+};
+
+// Lower-triangle tiles of one or two (blockIdx.y) symmetric products of every item, each tile stored
+// as it is and mirrored.
+template <class C>
+__global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Symmetric a, Symmetric b,
+                                                                   int tiles) {
   __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kStageBytes];
+  const Symmetric& p = blockIdx.y == 0 ? a : b;
   const int64_t id = regroup(blockIdx.x, gridDim.x);
-  const int64_t item = id / tiles;
+  const int64_t item = uniform64(id / tiles);
   int ti, tj;
   triangle_at(static_cast<int>(id - item * tiles), ti, tj);
   const int64_t i0 = uniform64(int64_t(ti) * C::BM), j0 = uniform64(int64_t(tj) * C::BN);
-  const Operand X = x.at(uniform64(item));
-  const int64_t nk = ((C::kTransA ? X.rows : X.cols) + kChunk - 1) / kChunk;
+  const Operand L = p.l.at(item), R = p.r.at(item);
+  const int64_t nk = ((C::kTransA ? L.rows : L.cols) + kChunk - 1) / kChunk;
   v4f acc[C::MI][C::NJ];
-  multiply<C>(X, X, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
+  multiply<C>(L, R, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
   __syncthreads();
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -203,35 +224,37 @@ __global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Batch x, _Flo
   const Region<C> region(wave < kFirst ? (lds_u8*)s0 : (lds_u8*)s1,
                          wave < kFirst ? wave : wave - kFirst, lane);
   const int64_t r0 = i0 + wm * C::WM, q0 = j0 + wn * C::WN;
-  const _Float16* src = reinterpret_cast<const _Float16*>(X.p);
-  out += item * out_stride;
+  const int64_t at = item * p.stride;
+  const bool one = p.m1 != nullptr, two = p.m2 != nullptr;
 #pragma unroll
   for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
     for (int nj = 0; nj < C::NJ; ++nj) {
-      v4f v = acc[mi][nj];
-      if constexpr (kPoly) {
-        const int64_t row = r0 + 16 * mi + r, col = q0 + 16 * nj + 4 * G;
-        typedef _Float16 v4h __attribute__((ext_vector_type(4)));
-        v4h old = {0, 0, 0, 0};
-        if (row < n && col < ld) old = *reinterpret_cast<const v4h*>(src + row * ld + col);
+      v4f v = acc[mi][nj] * p.f;
+      const int64_t row = r0 + 16 * mi + r, col = q0 + 16 * nj + 4 * G;
+      if (one && row < p.n && col < p.ld) {
+        const v4h m = *reinterpret_cast<const v4h*>(p.m1 + at + row * p.ld + col);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = fmaf(c * (kB / kA / kA), v[e], b * (kB / kA) * float(old[e]));
-          if (diagonal && row == col + e && row < n) v[e] = fmaf(a, kB, v[e]);
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(p.f1, float(m[e]), v[e]);
+        if (two) {
+          const v4h k = *reinterpret_cast<const v4h*>(p.m2 + at + row * p.ld + col);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = fmaf(p.f2, float(k[e]), v[e]);
         }
-      } else {
-        v *= kA / kX / kX;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (row == col + e) v[e] += p.diag;
       }
       region.put(mi, nj, v2i{static_cast<int>(pack_half2(v[0], v[1])),
                              static_cast<int>(pack_half2(v[2], v[3]))});
     }
   region.settle();
+  _Float16* out = p.out + at;
 #pragma unroll
   for (int k = 0; k < C::WM / 8; ++k) {
     const v4i v = region.row8(k);
     const int64_t row = r0 + 8 * k + (lane >> 3), col = q0 + 8 * (lane & 7);
-    if (row < n && col < ld) *reinterpret_cast<v4i*>(out + row * ld + col) = v;
+    if (row < p.n && col < p.ld) *reinterpret_cast<v4i*>(out + row * p.ld + col) = v;
   }
   if (ti == tj) return;
 #pragma unroll
@@ -240,24 +263,301 @@ __global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Batch x, _Flo
     for (int q = 0; q < 4; ++q) {
       const v4i v = region.col8(k, q);
       const int64_t row = q0 + 16 * q + r, col = r0 + 32 * k + 8 * G;
-      if (row < n && col < ld) *reinterpret_cast<v4i*>(out + row * ld + col) = v;
+      if (row < p.n && col < p.ld) *reinterpret_cast<v4i*>(out + row * p.ld + col) = v;
     }
 }
 
-// X <- P X (or X P, P symmetric), plus a X from its two halves where `lo` is given (lo is replaced
-// by the new X's where keep_lo says so). Written as hi [rows][ld], or (u) as bf16 [rows][cols].
+// ------------------------------------------------------------------ long reductions of few tiles
+// Split s of `splits` of A = X X' (kTransA: X' X): fp32 tiles [item][split][tile][BM][BN] of kX^2 A.
+// kBoth: from both halves of X (three products).
+template <class C, bool kBoth>
+__global__ __launch_bounds__(C::kThreads) void ns_gram_part_kernel(Batch hi, Batch lo, int tiles,
+                                                                   int splits,
+                                                                   float* __restrict__ parts) {
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kStageBytes];
+  const int64_t item = blockIdx.x / (tiles * splits);
+  const int rest = static_cast<int>(blockIdx.x - item * tiles * splits);
+  const int split = rest / tiles;
+  int ti, tj;
+  triangle_at(rest - split * tiles, ti, tj);
+  const int64_t i0 = int64_t(ti) * C::BM, j0 = int64_t(tj) * C::BN;
+  const Operand X = hi.at(item);
+  const int64_t nk = ((C::kTransA ? X.rows : X.cols) + kChunk - 1) / kChunk;
+  const int64_t c0 = nk * split / splits, c1 = nk * (split + 1) / splits;
+  v4f acc[C::MI][C::NJ];
+  if constexpr (kBoth) {
+    const Operand Y = lo.at(item);
+    multiply<C>(X, Y, i0, j0, c0, c1, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
+    __syncthreads();
+    multiply<C, true>(Y, X, i0, j0, c0, c1, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < C::NJ; ++nj) acc[mi][nj] *= 1.0f / kLo;
+    __syncthreads();
+    multiply<C, true>(X, X, i0, j0, c0, c1, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
+  } else {
+    multiply<C>(X, X, i0, j0, c0, c1, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  const int G = lane >> 4, r = lane & 15;
+  float* out = parts + int64_t(blockIdx.x) * C::BM * C::BN;
+#pragma unroll
+  for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+    for (int nj = 0; nj < C::NJ; ++nj)
+      *reinterpret_cast<v4f*>(out + (wm * C::WM + 16 * mi + r) * C::BN + wn * C::WN + 16 * nj +
+                              4 * G) = acc[mi][nj];
+}
+
+// The sum of the splits, as the fp16 matrix: one block per 32 x 32 patch of a 128 x 128 tile.
+__global__ __launch_bounds__(kThreads) void ns_gram_sum_kernel(const float* __restrict__ parts,
+                                                               int tiles, int splits, _Float16* out,
+                                                               int64_t stride, int64_t n,
+                                                               int64_t ld) {
+  __shared__ float sh[32][33];
+  const int patch = blockIdx.x & 15;
+  const int64_t tile = blockIdx.x >> 4;
+  const int64_t item = tile / tiles;
+  int ti, tj;
+  triangle_at(static_cast<int>(tile - item * tiles), ti, tj);
+  const int i = 32 * (patch >> 2), j = 32 * (patch & 3);
+  const int row = threadIdx.x >> 3, col = 4 * (threadIdx.x & 7);
+  const float* p = parts + (item * splits * tiles + (tile - item * tiles)) * (128 * 128) +
+                   (i + row) * 128 + j + col;
+  v4f v = *reinterpret_cast<const v4f*>(p);
+  for (int s = 1; s < splits; ++s)
+    v += *reinterpret_cast<const v4f*>(p + int64_t(s) * tiles * (128 * 128));
+  v *= kA / kX / kX;
+  out += item * stride;
+  const v4h h = {static_cast<_Float16>(v[0]), static_cast<_Float16>(v[1]),
+                 static_cast<_Float16>(v[2]), static_cast<_Float16>(v[3])};
+  const int64_t r = int64_t(ti) * 128 + i, c = int64_t(tj) * 128 + j;
+  if (r + row < n && c + col < ld) *reinterpret_cast<v4h*>(out + (r + row) * ld + c + col) = h;
+  if (ti == tj) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sh[row][col + e] = v[e];
+  __syncthreads();
+  const v4h t = {static_cast<_Float16>(sh[col][row]), static_cast<_Float16>(sh[col + 1][row]),
+                 static_cast<_Float16>(sh[col + 2][row]), static_cast<_Float16>(sh[col + 3][row])};
+  if (c + row < n && r + col < ld) *reinterpret_cast<v4h*>(out + (c + row) * ld + r + col) = t;
+}
+
+// ------------------------------------------------------------------ short sides: all steps at once
+// For a shorter side of at most 16 kTiles all steps run on the small matrix alone, one block per
+// matrix: A follows from A (A <- P A P with P = a I + B, B = b A + c A A), Q = the product of all P
+// is kept, and the caller multiplies X by it once. That amplifies an error of the first A by a^2 a
+// step, so here every operand is in two fp16 halves (three products each, 22 bits).
+//
+// Wave w owns rows 16 w .. + 15 of A, T and Q in the layout that the matrix core leaves results in:
+// lane (G, r) holds row r, columns 16 j + 4 G .. + 3. Two neighbouring tiles of columns are a left
+// operand of the next product as they lie, if the right one's k are taken in the same order; the
+// right one (symmetric, so its rows serve as its columns) lies in LDS with its columns permuted so that
+// a lane's eight are adjacent. Rounding makes A <- P A P a little asymmetric, and taking rows for
+// columns turns that part's sign round: it grew nine times a step (1e-3 of u after five steps, 1e-2
+// after six). So each A meets its transpose before it is used; left after five steps: 3e-5.
+template <int kTiles>
+struct Rows {
+  v4f v[kTiles];
+};
+template <int kTiles>
+struct Halves {
+  v4i hi[kTiles / 2], lo[kTiles / 2];
+};
+
+__device__ __forceinline__ void split_half2(float x, float y, float scale, uint32_t& hi,
+                                            uint32_t& lo) {
+  x *= scale;
+  y *= scale;
+  const _Float16 a = static_cast<_Float16>(x), b = static_cast<_Float16>(y);
+  hi = __builtin_bit_cast(uint32_t, half2_t{a, b});
+  lo = pack_half2(x - float(a), y - float(b));
+}
+
+template <int kTiles>
+__device__ __forceinline__ Halves<kTiles> halves(const Rows<kTiles>& x, float scale) {
+  Halves<kTiles> h;
+#pragma unroll
+  for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t hi, lo;
+      split_half2(x.v[j][2 * e], x.v[j][2 * e + 1], scale, hi, lo);
+      h.hi[j / 2][2 * (j & 1) + e] = static_cast<int>(hi);
+      h.lo[j / 2][2 * (j & 1) + e] = static_cast<int>(lo);
+    }
+  return h;
+}
+
+template <int kTiles>
+struct Core {
+  static constexpr int kSide = 16 * kTiles;
+  static constexpr int kThreads = 64 * kTiles;
+  static constexpr int kPitch = 2 * kSide + 16;  // bytes of an LDS row: 16 rows start on 16 banks
+  static constexpr int kBytes = kSide * kPitch;
+
+  lds_u8 *hi, *lo;
+  int wave, G, r;
+
+  // this wave's rows of the right operand
+  __device__ __forceinline__ void put(const Halves<kTiles>& h) const {
+#pragma unroll
+    for (int kk = 0; kk < kTiles / 2; ++kk) {
+      const int at = (16 * wave + r) * kPitch + 64 * kk + 16 * G;
+      *reinterpret_cast<lds_v4i*>(hi + at) = h.hi[kk];
+      *reinterpret_cast<lds_v4i*>(lo + at) = h.lo[kk];
+    }
+  }
+  // x <- (x + y') / 2, y the matrix times `scale` that lies in LDS: what a transposing read of 4 rows
+  // by 16 columns gives lane (G, r) is the column that is this lane's row.
+  __device__ __forceinline__ void symmetrise(Rows<kTiles>& x, float scale) const {
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+      const int at = (16 * j + 4 * G + (r >> 2)) * kPitch + 64 * (wave >> 1) + 16 * (r & 3) +
+                     8 * (wave & 1);
+      const v4h h = __builtin_bit_cast(
+          v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(hi + at)));
+      const v4h l = __builtin_bit_cast(
+          v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lo + at)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x.v[j][e] = 0.5f * fmaf(float(h[e]) + float(l[e]), 1.0f / scale, x.v[j][e]);
+    }
+  }
+  // x += f left right, for one or two left operands
+  template <bool kTwo>
+  __device__ __forceinline__ void multiply(const Halves<kTiles>& l, Rows<kTiles>& x, float f,
+                                           const Halves<kTiles>& l2, Rows<kTiles>& x2,
+                                           float f2) const {
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+      v4f acc = {0.0f, 0.0f, 0.0f, 0.0f}, acc2 = acc;
+#pragma unroll
+      for (int kk = 0; kk < kTiles / 2; ++kk) {
+        const int at = (16 * j + r) * kPitch + 64 * kk + 16 * G;
+        const v4i rh = *reinterpret_cast<const lds_v4i*>(hi + at);
+        const v4i rl = *reinterpret_cast<const lds_v4i*>(lo + at);
+        acc = mfma<true>(rl, l.hi[kk], acc);
+        acc = mfma<true>(rh, l.lo[kk], acc);
+        acc = mfma<true>(rh, l.hi[kk], acc);
+        if constexpr (kTwo) {
+          acc2 = mfma<true>(rl, l2.hi[kk], acc2);
+          acc2 = mfma<true>(rh, l2.lo[kk], acc2);
+          acc2 = mfma<true>(rh, l2.hi[kk], acc2);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x.v[j][e] = fmaf(f, acc[e], x.v[j][e]);
+      if constexpr (kTwo) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x2.v[j][e] = fmaf(f2, acc2[e], x2.v[j][e]);
+      }
+    }
+  }
+};
+
+// parts: the splits of kX^2 A ([item][split][128][128] fp32); q_hi, q_lo: kq Q in halves [n][ld],
+// zeros behind column n.
+template <int kTiles>
+__global__ __launch_bounds__(64 * kTiles) void ns_core_kernel(const float* __restrict__ parts,
+                                                              int splits, int n, int ld, int steps,
+                                                              float a, float b, float c, float kq,
+                                                              _Float16* q_hi, _Float16* q_lo,
+                                                              int64_t stride) {
+  using K = Core<kTiles>;
+  __shared__ __attribute__((aligned(1024))) uint8_t sh[2 * K::kBytes];
+  K core;
+  core.hi = (lds_u8*)sh;
+  core.lo = core.hi + K::kBytes;
+  const int lane = threadIdx.x & 63;
+  core.wave = threadIdx.x >> 6;
+  core.G = lane >> 4;
+  core.r = lane & 15;
+  const int row = 16 * core.wave + core.r;
+  Rows<kTiles> A, T, Q;
+  const float* p = parts + int64_t(blockIdx.x) * splits * (128 * 128) + row * 128 + 4 * core.G;
+#pragma unroll
+  for (int j = 0; j < kTiles; ++j) {
+    A.v[j] = *reinterpret_cast<const v4f*>(p + 16 * j);
+    for (int s = 1; s < splits; ++s)
+      A.v[j] += *reinterpret_cast<const v4f*>(p + int64_t(s) * (128 * 128) + 16 * j);
+    A.v[j] *= 1.0f / kX / kX;
+  }
+  Halves<kTiles> none;
+  for (int k = 0; k < steps; ++k) {
+    core.put(halves(A, kA));
+    __syncthreads();
+    core.symmetrise(A, kA);
+    const Halves<kTiles> ha = halves(A, kA);
+    Rows<kTiles> B;
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) B.v[j] = b * A.v[j];
+    core.template multiply<false>(ha, B, c / kA / kA, none, B, 0.0f);
+    __syncthreads();  // every wave has read A
+    core.put(halves(B, kB));
+    __syncthreads();
+    const bool last = k + 1 == steps;
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) T.v[j] = a * A.v[j];
+    if (k == 0) {
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) {
+        Q.v[j] = B.v[j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (row == 16 * j + 4 * core.G + e && row < n) Q.v[j][e] += a;
+      }
+      if (!last) core.template multiply<false>(ha, T, 1.0f / kA / kB, none, T, 0.0f);
+    } else {
+      const Halves<kTiles> hq = halves(Q, kq);
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) Q.v[j] *= a;
+      if (last)
+        core.template multiply<false>(hq, Q, 1.0f / kq / kB, none, Q, 0.0f);
+      else
+        core.template multiply<true>(hq, Q, 1.0f / kq / kB, ha, T, 1.0f / kA / kB);
+    }
+    if (last) break;
+    const Halves<kTiles> ht = halves(T, kA);
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) A.v[j] = a * T.v[j];
+    core.template multiply<false>(ht, A, 1.0f / kA / kB, none, A, 0.0f);
+    __syncthreads();  // every wave has read B
+  }
+  if (row >= n) return;
+  const int64_t at = int64_t(blockIdx.x) * stride + int64_t(row) * ld;
+  for (int j = 0; 16 * j < ld; ++j) {  // 16 kTiles columns and the zeros behind them, up to ld
+    const int col = 16 * j + 4 * core.G;
+    uint32_t h0 = 0, h1 = 0, l0 = 0, l1 = 0;
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k)
+      if (k == j) {
+        split_half2(Q.v[k][0], Q.v[k][1], kq, h0, l0);
+        split_half2(Q.v[k][2], Q.v[k][3], kq, h1, l1);
+      }
+    *reinterpret_cast<v2i*>(q_hi + at + col) = v2i{static_cast<int>(h0), static_cast<int>(h1)};
+    *reinterpret_cast<v2i*>(q_lo + at + col) = v2i{static_cast<int>(l0), static_cast<int>(l1)};
+  }
+}
+
+// X <- f A B + add X: A B is the polynomial's matrix times X (X times it where X is tall), X's two
+// halves are added where `add` is not zero, and lo is replaced by the new X's where keep_lo says so.
+// Written as hi [rows][ld], or (last) as bf16 [rows][cols]. kBoth: both matrices are in two halves;
+// then x_lo is the product with X's lo and p_lo the one with the polynomial's.
 struct Apply {
   int64_t rows, cols, ld;
   const _Float16* hi;
   _Float16* lo;
   _Float16* out;
-  int64_t hi_stride, lo_stride;
-  float a;
-  bool add, keep_lo, last;
-  float scale;
+  int64_t stride;
+  float f, add;
+  bool keep_lo, last;
+  Batch x_lo[2], p_lo[2];
 };
 
-template <class C>
+template <class C, bool kBoth>
 __global__ __launch_bounds__(C::kThreads) void ns_apply_kernel(Batch A, Batch B, Items it, Apply p,
                                                                int64_t tiles_i, int64_t tiles_j) {
   __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
@@ -270,7 +570,19 @@ __global__ __launch_bounds__(C::kThreads) void ns_apply_kernel(Batch A, Batch B,
   const Operand a = A.at(item), b = B.at(item);
   const int64_t nk = (a.cols + kChunk - 1) / kChunk;
   v4f acc[C::MI][C::NJ];
-  multiply<C>(a, b, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
+  if constexpr (kBoth) {
+    multiply<C>(p.x_lo[0].at(item), p.x_lo[1].at(item), i0, j0, 0, nk, nk, (lds_u8*)s0,
+                (lds_u8*)s1, acc);
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < C::NJ; ++nj) acc[mi][nj] *= 1.0f / kLo;
+    __syncthreads();
+    multiply<C, true>(p.p_lo[0].at(item), p.p_lo[1].at(item), i0, j0, 0, nk, nk, (lds_u8*)s0,
+                      (lds_u8*)s1, acc);
+    __syncthreads();
+  }
+  multiply<C, kBoth>(a, b, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
   __syncthreads();
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -280,25 +592,25 @@ __global__ __launch_bounds__(C::kThreads) void ns_apply_kernel(Batch A, Batch B,
   const Region<C> region(wave < kFirst ? (lds_u8*)s0 : (lds_u8*)s1,
                          wave < kFirst ? wave : wave - kFirst, lane);
   const int64_t r0 = i0 + wm * C::WM, q0 = j0 + wn * C::WN;
-  typedef _Float16 v4h __attribute__((ext_vector_type(4)));
-  const _Float16* hi = p.hi + item * p.hi_stride;
-  _Float16* lo = p.lo + item * p.lo_stride;
+  const _Float16* hi = p.hi + item * p.stride;
+  _Float16* lo = p.lo + item * p.stride;
+  const bool add = p.add != 0.0f;
 #pragma unroll
   for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
     for (int nj = 0; nj < C::NJ; ++nj) {
       const int64_t row = r0 + 16 * mi + r, col = q0 + 16 * nj + 4 * G;
       const bool in = row < p.rows && col < p.ld;
-      v4f v = acc[mi][nj] * (1.0f / kB);
-      if (p.add && in) {
+      v4f v = acc[mi][nj] * p.f;
+      if (add && in) {
         const v4h h = *reinterpret_cast<const v4h*>(hi + row * p.ld + col);
         const v4h l = *reinterpret_cast<const v4h*>(lo + row * p.ld + col);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = fmaf(p.a, fmaf(float(l[e]), 1.0f / kLo, float(h[e])), v[e]);
+        for (int e = 0; e < 4; ++e)
+          v[e] = fmaf(p.add, fmaf(float(l[e]), 1.0f / kLo, float(h[e])), v[e]);
       }
       v2i w;
       if (p.last) {
-        v *= p.scale;
         w = {static_cast<int>(pack_bf16x2(v[0], v[1])), static_cast<int>(pack_bf16x2(v[2], v[3]))};
       } else {
         w = {static_cast<int>(pack_half2(v[0], v[1])), static_cast<int>(pack_half2(v[2], v[3]))};
@@ -316,7 +628,7 @@ __global__ __launch_bounds__(C::kThreads) void ns_apply_kernel(Batch A, Batch B,
   uint16_t* u = it.u[item];
   const bool whole = !p.last || (p.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(u) & 15u) == 0);
   const int64_t ld = p.last ? p.cols : p.ld;
-  uint16_t* dst = p.last ? u : reinterpret_cast<uint16_t*>(p.out + item * p.hi_stride);
+  uint16_t* dst = p.last ? u : reinterpret_cast<uint16_t*>(p.out + item * p.stride);
 #pragma unroll
   for (int k = 0; k < C::WM / 8; ++k) {
     const v4i v = region.row8(k);
@@ -335,16 +647,20 @@ __global__ __launch_bounds__(C::kThreads) void ns_apply_kernel(Batch A, Batch B,
 
 // ------------------------------------------------------------------ host
 constexpr int64_t kFill = 256;  // compute units: tiles that fill the chip
+constexpr int64_t kShortSide = 128;
+constexpr float kQ = 512.0f, kWhole = 1024.0f;  // scales of a product of polynomials without, with a^n I
 
 inline int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 inline int64_t tiles_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
 
 struct Plan {
-  int64_t ldx, side, lds;  // row stride of X; the shorter side and its stride
-  bool tall;
-  int parts;
+  int64_t ldx, side, other, lds;  // row stride of X; the shorter and longer side, the shorter's stride
+  bool tall, short_side;
+  int parts;                     // blocks of the sum of squares
+  int64_t tiles, splits;         // of A by 128x128 tiles: lower triangle, splits of the reduction (1: none)
   double* sums;
-  _Float16 *hi[2], *lo, *A, *P;
+  float* gram;
+  _Float16 *hi[2], *lo, *s[6];
   int64_t x_stride, s_stride, bytes;
 };
 
@@ -352,12 +668,27 @@ Plan plan(int64_t count, int64_t rows, int64_t cols, void* ws) {
   Plan p;
   p.tall = rows > cols;
   p.side = p.tall ? cols : rows;
+  p.other = p.tall ? rows : cols;
+  p.short_side = p.side <= kShortSide;
   p.ldx = up(cols, kChunk);
   p.lds = up(p.side, kChunk);
   const int64_t parts = tiles_of(rows * cols, kThreads * 16);
   p.parts = static_cast<int>(parts > kMaxParts ? kMaxParts : parts);
   p.x_stride = up(rows * p.ldx, 128);
   p.s_stride = up(p.side * p.lds, 128);
+  const int64_t t = tiles_of(p.side, 128), nk = tiles_of(p.other, kChunk);
+  p.tiles = t * (t + 1) / 2;
+  p.splits = 1;
+  if (p.short_side) {
+    // each split's tile is read again by the one block that sums them: few splits, of two chunks at
+    // least, and no more than fill the chip
+    p.splits = nk / 2 < 16 ? nk / 2 : 16;
+    if (p.splits * count > kFill) p.splits = kFill / count;
+  } else if (count * p.tiles <= kFill / 2) {
+    p.splits = kFill / (count * p.tiles);
+    if (p.splits > nk / 8) p.splits = nk / 8;
+  }
+  if (p.splits < 1) p.splits = 1;
   uint8_t* at = static_cast<uint8_t*>(ws);
   auto take = [&](int64_t bytes) {
     uint8_t* q = at + p.bytes;
@@ -369,8 +700,9 @@ Plan plan(int64_t count, int64_t rows, int64_t cols, void* ws) {
   p.hi[0] = reinterpret_cast<_Float16*>(take(2 * count * p.x_stride));
   p.hi[1] = reinterpret_cast<_Float16*>(take(2 * count * p.x_stride));
   p.lo = reinterpret_cast<_Float16*>(take(2 * count * p.x_stride));
-  p.A = reinterpret_cast<_Float16*>(take(2 * count * p.s_stride));
-  p.P = reinterpret_cast<_Float16*>(take(2 * count * p.s_stride));
+  for (_Float16*& m : p.s) m = reinterpret_cast<_Float16*>(take(2 * count * p.s_stride));
+  p.gram = reinterpret_cast<float*>(
+      take(p.short_side || p.splits > 1 ? 4 * count * p.splits * p.tiles * 128 * 128 : 0));
   return p;
 }
 
@@ -379,39 +711,49 @@ using BigTile = Tile<256, 256, 2, 4, kTransA, kTransB, true>;
 template <bool kTransA, bool kTransB>
 using SmallTile = Tile<128, 128, 2, 2, kTransA, kTransB, true>;
 
-// Whether 256x256 tiles of `tiles` per matrix fill the chip.
+// Whether 256x256 tiles of `tiles` per matrix fill half of the chip.
 inline bool use_big(int64_t count, int64_t tiles) { return count * tiles >= kFill / 2; }
 
-template <class C, bool kPoly>
-void launch_symmetric(const Batch& x, _Float16* out, const Plan& p, int64_t count, float a,
-                      float b, float c, bool diagonal, hipStream_t s) {
-  const int64_t t = tiles_of(p.side, C::BM);
+template <class C>
+void launch_symmetric(const Symmetric& a, const Symmetric* b, int64_t count, hipStream_t s) {
+  const int64_t t = tiles_of(a.n, C::BM);
   const int tiles = static_cast<int>(t * (t + 1) / 2);
-  hipLaunchKernelGGL((ns_symmetric_kernel<C, kPoly>), dim3(static_cast<uint32_t>(count * tiles)),
-                     dim3(C::kThreads), 0, s, x, out, p.s_stride, p.side, p.lds, tiles, a, b, c,
-                     diagonal);
+  hipLaunchKernelGGL(ns_symmetric_kernel<C>, dim3(static_cast<uint32_t>(count * tiles), b ? 2 : 1),
+                     dim3(C::kThreads), 0, s, a, b ? *b : a, tiles);
 }
 
-template <class C>
+template <class C, bool kBoth>
 void launch_apply(const Batch& A, const Batch& B, const Items& it, const Apply& ap, int64_t count,
                   hipStream_t s) {
   const int64_t ti = tiles_of(ap.rows, C::BM), tj = tiles_of(ap.cols, C::BN);
-  hipLaunchKernelGGL(ns_apply_kernel<C>, dim3(static_cast<uint32_t>(count * ti * tj)),
+  hipLaunchKernelGGL((ns_apply_kernel<C, kBoth>), dim3(static_cast<uint32_t>(count * ti * tj)),
                      dim3(C::kThreads), 0, s, A, B, it, ap, ti, tj);
 }
 
-// Whether the steps keep every singular value and matrix inside what the fixed scales hold: the
-// default coefficients do (values stay below 1.21); others are followed over a grid of [0, 1].
-bool coefficients_ok(const puro_newton_schulz_params& h) {
+template <int kTiles>
+void launch_core(const Plan& p, int64_t count, const puro_newton_schulz_params& h, float kq,
+                 hipStream_t s) {
+  hipLaunchKernelGGL(ns_core_kernel<kTiles>, dim3(static_cast<uint32_t>(count)), dim3(64 * kTiles),
+                     0, s, p.gram, static_cast<int>(p.splits), static_cast<int>(p.side),
+                     static_cast<int>(p.lds), h.steps, h.coefficients[0], h.coefficients[1],
+                     h.coefficients[2], kq, p.s[0], p.s[1], p.s_stride);
+}
+
+// Whether the steps keep every singular value and matrix inside what the fixed scales hold, followed
+// over a grid of [0, 1], and the largest factor |a + b x^2 + c x^4| of a step there. The default
+// coefficients do (values stay below 1.21, factors below a).
+bool coefficients_ok(const puro_newton_schulz_params& h, double& factor) {
   const float *k = h.coefficients;
   if (!isfinite(k[0]) || !isfinite(k[1]) || !isfinite(k[2])) return false;
+  factor = fabs(k[0]);
   if (k[0] == 3.4445f && k[1] == -4.7750f && k[2] == 2.0315f) return true;
   double top = 1.0, last = 0.0;
   for (int i = 0; i <= 512; ++i) {
     double x = i / 512.0;
     for (int n = 0; n < h.steps; ++n) {
-      const double q = x * x;
-      x = x * (k[0] + q * (k[1] + q * k[2]));
+      const double q = x * x, f = k[0] + q * (k[1] + q * k[2]);
+      if (fabs(f) > factor) factor = fabs(f);
+      x *= f;
       if (!(fabs(x) < 1e4)) return false;
       if (n + 1 < h.steps && fabs(x) > top) top = fabs(x);
       if (fabs(x) > last) last = fabs(x);
@@ -426,10 +768,160 @@ puro_status check_sizes(int64_t count, int64_t rows, int64_t cols) {
   if (count > kMax) return PURO_ERR_ARG;
   const int64_t side = rows < cols ? rows : cols, other = rows < cols ? cols : rows;
   if (side > PURO_NS_MAX_SIDE || other > PURO_NS_MAX_LONG) return PURO_ERR_SHAPE;
-  // launches: 128x128 tiles of every matrix, by 256 threads
+  // launches: 128x128 tiles of every matrix, by 512 threads at most
   if (!grid_ok(count * tiles_of(rows, 128) * tiles_of(cols, 128), 512)) return PURO_ERR_SHAPE;
   return PURO_OK;
 }
+
+// One call's launches.
+struct Run {
+  const Plan& p;
+  const Items& it;
+  const puro_newton_schulz_params& h;
+  int64_t count, rows, cols;
+  hipStream_t s;
+  bool big_s, big_x;
+
+  Batch square(const _Float16* m) const { return {m, p.s_stride, p.side, p.lds, p.lds}; }
+  Batch whole(const _Float16* x) const { return {x, p.x_stride, rows, p.ldx, p.ldx}; }
+
+  Symmetric product(const _Float16* l, const _Float16* r, _Float16* out, float f,
+                    const _Float16* m1 = nullptr, float f1 = 0.0f, const _Float16* m2 = nullptr,
+                    float f2 = 0.0f, float diag = 0.0f) const {
+    return {square(l), square(r), out, m1, m2, p.s_stride, p.side, p.lds, f, f1, f2, diag};
+  }
+  void symmetric(const Symmetric& a, const Symmetric* b = nullptr) const {
+    if (big_s)
+      launch_symmetric<BigTile<false, false>>(a, b, count, s);
+    else
+      launch_symmetric<SmallTile<false, false>>(a, b, count, s);
+  }
+
+  template <bool kTrans>
+  void gram(const _Float16* x, _Float16* out) const {
+    const Batch X = whole(x);
+    if (p.short_side || p.splits > 1) {
+      const dim3 grid(static_cast<uint32_t>(count * p.splits * p.tiles));
+      const int tiles = static_cast<int>(p.tiles), splits = static_cast<int>(p.splits);
+      using C = SmallTile<kTrans, kTrans>;
+      if (out == nullptr) {
+        hipLaunchKernelGGL((ns_gram_part_kernel<C, true>), grid, dim3(C::kThreads), 0, s, X,
+                           whole(p.lo), tiles, splits, p.gram);
+        return;
+      }
+      hipLaunchKernelGGL((ns_gram_part_kernel<C, false>), grid, dim3(C::kThreads), 0, s, X, X,
+                         tiles, splits, p.gram);
+      hipLaunchKernelGGL(ns_gram_sum_kernel, dim3(static_cast<uint32_t>(count * p.tiles * 16)),
+                         dim3(kThreads), 0, s, p.gram, tiles, splits, out, p.s_stride, p.side,
+                         p.lds);
+      return;
+    }
+    const Symmetric a = {X, X, out, nullptr, nullptr, p.s_stride, p.side, p.lds, kA / kX / kX,
+                         0.0f, 0.0f, 0.0f};
+    if (big_s)
+      launch_symmetric<BigTile<kTrans, kTrans>>(a, nullptr, count, s);
+    else
+      launch_symmetric<SmallTile<kTrans, kTrans>>(a, nullptr, count, s);
+  }
+
+  // X (half n) becomes f P X + add X
+  template <bool kBoth>
+  void apply(const _Float16* P, int n, float f, float add, bool keep_lo, bool last) const {
+    Apply ap = {};
+    ap.rows = rows;
+    ap.cols = cols;
+    ap.ld = p.ldx;
+    ap.hi = p.hi[n];
+    ap.lo = p.lo;
+    ap.out = p.hi[1 - n];
+    ap.stride = p.x_stride;
+    const float scale = last ? h.scale / kX : 1.0f;
+    ap.f = f * scale;
+    ap.add = add * scale;
+    ap.keep_lo = keep_lo;
+    ap.last = last;
+    const Batch X = whole(p.hi[n]), M = square(P);
+    if constexpr (kBoth) {
+      ap.x_lo[p.tall ? 0 : 1] = whole(p.lo);
+      ap.x_lo[p.tall ? 1 : 0] = M;
+      ap.p_lo[p.tall ? 0 : 1] = X;
+      ap.p_lo[p.tall ? 1 : 0] = square(p.s[1]);
+      if (p.tall)
+        launch_apply<SmallTile<false, false>, true>(X, M, it, ap, count, s);
+      else
+        launch_apply<SmallTile<false, true>, true>(M, X, it, ap, count, s);
+    } else if (p.tall) {
+      if (big_x)
+        launch_apply<BigTile<false, false>, false>(X, M, it, ap, count, s);
+      else
+        launch_apply<SmallTile<false, false>, false>(X, M, it, ap, count, s);
+    } else {
+      if (big_x)
+        launch_apply<BigTile<false, true>, false>(M, X, it, ap, count, s);
+      else
+        launch_apply<SmallTile<false, true>, false>(M, X, it, ap, count, s);
+    }
+  }
+
+  // All steps on A alone.
+  void at_once(float kq) const {
+    if (p.tall)
+      gram<true>(p.hi[0], nullptr);
+    else
+      gram<false>(p.hi[0], nullptr);
+    if (p.side <= 32)
+      launch_core<2>(p, count, h, kq, s);
+    else if (p.side <= 64)
+      launch_core<4>(p, count, h, kq, s);
+    else
+      launch_core<8>(p, count, h, kq, s);
+    apply<true>(p.s[0], 0, 1.0f / kq, 0.0f, false, true);
+  }
+
+  // `g` steps, up to three, on hi[n] through their small matrices. both: X is in two halves, and a^g X
+  // is added from both; else a^g I is part of the matrix.
+  void steps(int g, int n, bool both, bool keep_lo, bool last) const {
+    const float a = h.coefficients[0], b = h.coefficients[1], c = h.coefficients[2];
+    _Float16 *A = p.s[0], *T = p.s[1], *B = p.s[2], *B2 = p.s[3], *Q = p.s[4], *Q2 = p.s[5];
+    if (p.tall)
+      gram<true>(p.hi[n], A);
+    else
+      gram<false>(p.hi[n], A);
+    const float cc = c * (kB / kA / kA), bb = b * (kB / kA);
+    symmetric(product(A, A, B, cc, A, bb, nullptr, 0.0f, g == 1 && !both ? a * kB : 0.0f));
+    if (g == 1) {
+      apply<false>(B, n, 1.0f / kB, both ? a : 0.0f, keep_lo, last);
+      return;
+    }
+    // Q: the product of the polynomials up to here less `rest` I, times qs
+    const _Float16* q = B;
+    float qs = kB, rest = a;
+    auto times = [&](_Float16* out, float scale, float diag) {  // by a I + B
+      return product(B, q, out, scale / kB / qs, q, a * scale / qs, B, rest * scale / kB, diag);
+    };
+    for (int k = 1; k < g; ++k) {
+      const Symmetric t = product(B, A, T, 1.0f / kB, A, a);
+      if (k > 1) {
+        const Symmetric next = times(Q, kQ, 0.0f);
+        symmetric(t, &next);
+        q = Q;
+        qs = kQ;
+        rest *= a;
+      } else {
+        symmetric(t);
+      }
+      symmetric(product(T, B, A, 1.0f / kB, T, a));
+      _Float16* to = k == 1 ? B2 : p.s[2];  // the first B is read as Q until the third
+      symmetric(product(A, A, to, cc, A, bb));
+      B = to;
+    }
+    _Float16* P = q == Q ? Q2 : Q;
+    const float scale = both ? kQ : kWhole;
+    symmetric(times(P, scale, both ? 0.0f : a * rest * scale));
+    rest *= a;
+    apply<false>(P, n, 1.0f / scale, both ? rest : 0.0f, keep_lo, last);
+  }
+};
 
 }  // namespace
 }  // namespace puro
@@ -446,8 +938,10 @@ extern "C" puro_status puro_newton_schulz(const puro_ns_item* items, int count, 
                                           void* workspace, void* stream) {
   PURO_TRY(check_sizes(count, rows, cols));
   if (hp == nullptr) return PURO_ERR_NULL;
+  double factor = 0.0;
   if (hp->steps < 1 || hp->steps > PURO_NS_MAX_STEPS || (hp->nesterov != 0 && hp->nesterov != 1) ||
-      !(hp->beta >= 0.0f && hp->beta < 1.0f) || !isfinite(hp->scale) || !coefficients_ok(*hp))
+      !(hp->beta >= 0.0f && hp->beta < 1.0f) || !isfinite(hp->scale) ||
+      !coefficients_ok(*hp, factor))
     return PURO_ERR_ARG;
   if (count == 0 || rows == 0 || cols == 0) return PURO_OK;
   if (items == nullptr) return PURO_ERR_NULL;
@@ -480,61 +974,38 @@ extern "C" puro_status puro_newton_schulz(const puro_ns_item* items, int count, 
     hipLaunchKernelGGL(ns_momentum_kernel<true>, sums, dim3(kThreads), 0, s, it, rows * cols, k,
                        p.sums);
     hipLaunchKernelGGL(ns_convert_kernel<true>, conv, dim3(kThreads), 0, s, it, rows, cols, p.ldx,
-                       k, p.sums, p.parts, p.hi[0], p.lo, p.x_stride, p.x_stride);
+                       k, p.sums, p.parts, p.hi[0], p.lo, p.x_stride);
   } else {
     hipLaunchKernelGGL(ns_momentum_kernel<false>, sums, dim3(kThreads), 0, s, it, rows * cols, k,
                        p.sums);
     hipLaunchKernelGGL(ns_convert_kernel<false>, conv, dim3(kThreads), 0, s, it, rows, cols, p.ldx,
-                       k, p.sums, p.parts, p.hi[0], p.lo, p.x_stride, p.x_stride);
+                       k, p.sums, p.parts, p.hi[0], p.lo, p.x_stride);
   }
-  const float a = hp->coefficients[0], b = hp->coefficients[1], c = hp->coefficients[2];
   const int64_t side_tiles = tiles_of(p.side, 256);
-  const bool big_s = use_big(count, side_tiles * (side_tiles + 1) / 2);
-  const bool big_x = use_big(count, tiles_of(rows, 256) * tiles_of(cols, 256));
-  const Batch A = {p.A, p.s_stride, p.side, p.lds, p.lds};
-  const Batch P = {p.P, p.s_stride, p.side, p.lds, p.lds};
-  for (int n = 0; n < hp->steps; ++n) {
-    const Batch X = {p.hi[n & 1], p.x_stride, rows, p.ldx, p.ldx};
-    const bool both = n + 2 < hp->steps;  // this step's X is in two halves
-    if (p.tall) {
-      if (big_s)
-        launch_symmetric<BigTile<true, true>, false>(X, p.A, p, count, 0, 0, 0, false, s);
-      else
-        launch_symmetric<SmallTile<true, true>, false>(X, p.A, p, count, 0, 0, 0, false, s);
-    } else {
-      if (big_s)
-        launch_symmetric<BigTile<false, false>, false>(X, p.A, p, count, 0, 0, 0, false, s);
-      else
-        launch_symmetric<SmallTile<false, false>, false>(X, p.A, p, count, 0, 0, 0, false, s);
+  const Run run = {p, it, *hp, count, rows, cols, s,
+                   use_big(count, side_tiles * (side_tiles + 1) / 2),
+                   use_big(count, tiles_of(rows, 256) * tiles_of(cols, 256))};
+  if (p.short_side) {
+    // The largest power of two (up to 64) with which the product of all polynomials fits fp16. With a
+    // growth above 1e5 (nine steps of the default coefficients) errors of A pass 2e-3 of u: step by step.
+    const double growth = pow(factor, hp->steps);
+    float kq = 64.0f;
+    while (kq * growth > 6e4) kq *= 0.5f;
+    if (kq >= 0.5f) {
+      run.at_once(kq);
+      return launch_status();
     }
-    if (big_s)
-      launch_symmetric<BigTile<false, false>, true>(A, p.P, p, count, a, b, c, !both, s);
-    else
-      launch_symmetric<SmallTile<false, false>, true>(A, p.P, p, count, a, b, c, !both, s);
-    Apply ap = {};
-    ap.rows = rows;
-    ap.cols = cols;
-    ap.ld = p.ldx;
-    ap.hi = p.hi[n & 1];
-    ap.lo = p.lo;
-    ap.out = p.hi[(n + 1) & 1];
-    ap.hi_stride = ap.lo_stride = p.x_stride;
-    ap.a = a;
-    ap.add = both;
-    ap.keep_lo = n + 3 < hp->steps;
-    ap.last = n + 1 == hp->steps;
-    ap.scale = hp->scale / kX;
-    if (p.tall) {
-      if (big_x)
-        launch_apply<BigTile<false, false>>(X, P, it, ap, count, s);
-      else
-        launch_apply<SmallTile<false, false>>(X, P, it, ap, count, s);
-    } else {
-      if (big_x)
-        launch_apply<BigTile<false, true>>(P, X, it, ap, count, s);
-      else
-        launch_apply<SmallTile<false, true>>(P, X, it, ap, count, s);
-    }
+  }
+  // Three steps' matrices, then two's, instead of one's: 3 s^2 l + 9 s^3 and 3 s^2 l + 5 s^3
+  // operations for sides s <= l, against 3 s^2 l + s^3 a step.
+  const bool grouped = !p.short_side && hp->steps >= 3 && factor <= 3.55 && 2 * p.other >= 3 * p.side;
+  int n = 0;
+  for (int done = 0; done < hp->steps; n = 1 - n) {
+    const int left = hp->steps - done;
+    const int g = !grouped ? 1 : done == 0 ? 3 : left < 2 ? left : 2;
+    const bool both = grouped ? done == 0 : left > 2;
+    run.steps(g, n, both, !grouped && left > 3, g == left);
+    done += g;
   }
   return launch_status();
 }

@@ -10,9 +10,11 @@ its exponential (e_l, and roundings of its argument and factors) and half a step
 gradients take those through their sums, add their own summation, and half a step of bf16 if
 rounded.
 
-Orthogonalisation. The bound is not elementary: `ortho` also runs the steps with every operand
+Orthogonalisation. The bound is not elementary: `ortho_rounded` runs the steps with every operand
 rounded to fp16 where the kernels round it (sums exact), and the kernels have to lie within twice that
-run's distance from the exact steps (their sums round too, far below fp16), plus u's rounding."""
+run's distance from the exact steps (their sums round too, far below fp16), plus u's rounding: the
+larger distance of its two orders of the steps. (Short sides are held to the same, though their
+operands are two halves wide.)"""
 import numpy as np
 import torch
 
@@ -77,8 +79,22 @@ def momentum(g, m, beta, nesterov):
     return m, (b * m + rest * g if nesterov else m)
 
 
-def ortho(v, steps=5, coefficients=COEFFICIENTS, rounded=False):
-    """The steps on one float64 matrix; `rounded`: operands in fp16 where the kernels hold them so."""
+def ortho(v, steps=5, coefficients=COEFFICIENTS):
+    """The steps on one float64 matrix."""
+    a, b, c = (float(np.float32(k)) for k in coefficients)
+    tall = v.shape[0] > v.shape[1]
+    x = v.t() if tall else v
+    norm = torch.linalg.matrix_norm(x)
+    x = x / norm if norm > 0 else x
+    for _ in range(steps):
+        gram = x @ x.t()
+        x = a * x + (b * gram + c * (gram @ gram)) @ x
+    return x.t() if tall else x
+
+
+def ortho_rounded(v, steps=5, coefficients=COEFFICIENTS, grouped=False):
+    """The same with every operand in fp16 where the kernels hold it so (sums exact): step by step with
+    X in two halves until the last two steps, or by matrices of three steps (X in two halves), then two."""
     a, b, c = (float(np.float32(k)) for k in coefficients)
     tall = v.shape[0] > v.shape[1]
     x = v.t() if tall else v
@@ -86,19 +102,30 @@ def ortho(v, steps=5, coefficients=COEFFICIENTS, rounded=False):
     x = x / norm if norm > 0 else x
 
     def half(t, scale):
-        return (t * scale).half().double() / scale if rounded else t
+        return (t * scale).half().double() / scale
 
     eye = torch.eye(x.shape[0], dtype=x.dtype, device=x.device)
-    lo = None
-    for n in range(steps):
+    done = 0
+    while done < steps:
+        g = 1 if not grouped else 3 if done == 0 else min(2, steps - done)
+        both = done == 0 if grouped else steps - done > 2
         hi = half(x, 4096.0)
-        lo = half(x - hi, 4096.0 * 2048.0) if n + 2 < steps else None
+        lo = half(x - hi, 4096.0 * 2048.0)
         gram = half(hi @ hi.t(), 16384.0)
         poly = b * gram + c * (gram @ gram)
-        if rounded and lo is None:
-            x = half(a * eye + poly, 2048.0) @ hi
-        elif rounded:
-            x = a * (hi + lo) + half(poly, 2048.0) @ hi
-        else:
-            x = a * x + poly @ x
+        q, rest = poly, a
+        for k in range(1, g):
+            poly = half(poly, 2048.0)
+            if k > 1:
+                q, rest = a * q + rest * poly + poly @ q, rest * a
+            q = half(q, 2048.0 if k == 1 else 512.0)
+            t = half(a * gram + poly @ gram, 16384.0)
+            gram = half(a * t + t @ poly, 16384.0)
+            poly = b * gram + c * (gram @ gram)
+        if g > 1:
+            poly = half(poly, 2048.0)
+            q, rest = a * q + rest * poly + poly @ q, rest * a
+        scale = 2048.0 if g == 1 else 512.0 if both else 1024.0
+        x = rest * (hi + lo) + half(q, scale) @ hi if both else half(rest * eye + q, scale) @ hi
+        done += g
     return x.t() if tall else x
