@@ -37,13 +37,16 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) v4i lds_v4i;
 typedef __attribute__((address_space(3))) v2i lds_v2i;
 typedef __attribute__((address_space(3))) v4s lds_v4s;
+typedef __attribute__((address_space(3))) v4f lds_v4f;
 typedef __attribute__((address_space(3))) float lds_f32;
+typedef __attribute__((address_space(3))) int lds_i32;
 typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kChunk = 64;             // reduction elements of a chunk
 constexpr int kRowBytes = 2 * kChunk;  // bytes of a staged row
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool kTransA_, bool kTransB_, bool kHalf_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool kTransA_, bool kTransB_, bool kHalf_,
+          int kStages_ = 2>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_;
   static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
@@ -55,6 +58,10 @@ struct Tile {
   static constexpr int MI = WM / 16, NJ = WN / 16;
   static constexpr int kBOff = BM * kRowBytes;
   static constexpr int kStageBytes = (BM + BN) * kRowBytes;
+  static constexpr int kStages = kStages_;
+  // the two LDS arrays of a block: a stage each, or the whole ring and nothing
+  static constexpr int kLds0 = kStages == 2 ? kStageBytes : kStages * kStageBytes;
+  static constexpr int kLds1 = kStages == 2 ? kStageBytes : 16;
   static_assert(WN == 64 && WM % 16 == 0 && BM % 64 == 0 && BN % 64 == 0, "tile shape");
 };
 
@@ -143,6 +150,66 @@ struct Stager {
   }
 };
 
+// The ring's loads (multiply, kStages > 2) are inline assembly: the compiler, which does not see that they
+// write LDS, adds no waits of its own before reads of other stages. They have no output registers.
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ v4u rsrc_words(const void* base, int64_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint32_t n = bytes > int64_t(0x7fffffff) ? 0x7fffffffu
+                     : bytes < 0                 ? 0u
+                                                 : static_cast<uint32_t>(bytes);
+  v4u r;
+  r[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b));
+  r[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32) & 0xffffu);
+  r[2] = __builtin_amdgcn_readfirstlane(n);
+  r[3] = 0x00020000u;
+  return r;
+}
+__device__ __forceinline__ void load_lds16(v4u r, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff),
+               "s"(r)
+               : "memory");
+}
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
+}
+
+template <bool kTrans, int BX, int kIssuers>
+struct RingStager : Stager<kTrans, BX, kIssuers> {
+  using Base = Stager<kTrans, BX, kIssuers>;
+  v4u words;
+  __device__ __forceinline__ void init(const Operand& o, int64_t x0, int w_, int lane) {
+    Base::init(o, x0, w_, lane);
+    if constexpr (!kTrans)
+      words = rsrc_words(o.p + x0 * Base::ld2, (o.rows - x0 - 1) * Base::ld2 + 2 * o.cols);
+  }
+  // chunk c of nk; from nk on zeros are written, so that every wave always has the same number of
+  // loads under way
+  __device__ __forceinline__ void send(uint32_t dst, int64_t c, int64_t nk) const {
+    v4u r = words;
+    uint32_t v;
+    if constexpr (kTrans) {
+      r = rsrc_words(Base::p + c * kChunk * Base::ld2,
+                     c < nk ? (Base::rows - c * kChunk - 1) * Base::ld2 + Base::x_bytes : 0);
+      v = Base::voff;
+    } else {
+      v = c < nk ? (c == nk - 1 ? Base::voff_tail : Base::voff) +
+                       static_cast<uint32_t>(c * kRowBytes)
+                 : kOutside;
+      asm volatile("" : "+v"(v));
+    }
+#pragma unroll
+    for (int n = 0; n < Base::kLoads; ++n) {
+      const int q = Base::w + kIssuers * n;
+      const uint32_t off =
+          kTrans ? static_cast<uint32_t>((q & 7) * 8 * Base::ld2) + (q >> 3) * kRowBytes
+                 : static_cast<uint32_t>(8 * q * Base::ld2);
+      load_lds16(r, v + off, dst + 8 * q * kRowBytes);
+    }
+  }
+};
+
 // Lane offsets of a wave's fragment reads of one operand, whose rows (columns) begin at x of the tile.
 template <bool kTrans>
 struct Frag {
@@ -221,6 +288,61 @@ __device__ __forceinline__ void chunk_step(const lds_u8* stage, Fragments<C>& f,
   }
 }
 
+// multiply below with a ring of kStages stages: chunk c lies in stage c % kStages, and chunk
+// c + kStages - 1 is sent while c is multiplied. For tiles too few to share a CU: their loads come
+// from far (another XCD wrote them) and nothing else hides the way.
+template <class C, bool kMore>
+__device__ __forceinline__ void multiply_ring(const Operand& A, const Operand& B, int64_t i0,
+                                              int64_t j0, int64_t c0, int64_t c1, int64_t nk,
+                                              lds_u8* ring, v4f (&acc)[C::MI][C::NJ]) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  RingStager<C::kTransA, C::BM, C::kWaves> sa;
+  RingStager<C::kTransB, C::BN, C::kWaves> sb;
+  sa.init(A, i0, wave, lane);
+  sb.init(B, j0, wave, lane);
+  Fragments<C> f;
+  f.fa.init(0, wm * C::WM, lane);
+  f.fb.init(C::kBOff, wn * C::WN, lane);
+  if constexpr (!kMore) {
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < C::NJ; ++nj) acc[mi][nj] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  constexpr int kLoads = decltype(sa)::kLoads + decltype(sb)::kLoads;
+  const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ring));
+  auto send = [&](int64_t c, int stage) {
+    const int64_t end = c < c1 ? nk : 0;
+    sa.send(base + stage * C::kStageBytes, c, end);
+    sb.send(base + stage * C::kStageBytes + C::kBOff, c, end);
+  };
+#pragma unroll
+  for (int k = 0; k < C::kStages - 1; ++k) send(c0 + k, k);
+  int stage = 0;
+  for (int64_t c = c0; c < c1; ++c) {
+    // chunk c has landed when at most the later chunks' loads are under way, here and, behind the
+    // barrier, in every wave; and every wave has read the stage that is written next
+    wait_loads<(C::kStages - 2) * kLoads>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    send(c + C::kStages - 1, stage == 0 ? C::kStages - 1 : stage - 1);
+    const lds_u8* cur = ring + stage * C::kStageBytes;
+    f.a[0][0] = f.fa.template read<0, 0>(cur);
+    f.a[0][1] = f.fa.template read<0, 1>(cur);
+    __builtin_amdgcn_sched_barrier(0);
+    load_b<C, 0>(cur, f);
+    chunk_step<C, 0>(cur, f, acc, []() {});
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < C::NJ; ++nj) asm volatile("" : "+v"(acc[mi][nj]));
+    stage = stage + 1 == C::kStages ? 0 : stage + 1;
+  }
+  wait_loads<0>();
+}
+
 // The products of one tile over chunks [c0, c1) of the reduction, which has `nk` chunks in all.
 // Each instruction takes the B fragment as its row operand, so lane (G, r) receives row r, columns
 // 4 G .. 4 G + 3 of every 16x16 tile. On return other waves may still read the stages. kMore adds to
@@ -229,6 +351,10 @@ template <class C, bool kMore = false>
 __device__ __forceinline__ void multiply(const Operand& A, const Operand& B, int64_t i0,
                                          int64_t j0, int64_t c0, int64_t c1, int64_t nk,
                                          lds_u8* s0, lds_u8* s1, v4f (&acc)[C::MI][C::NJ]) {
+  if constexpr (C::kStages > 2) {
+    multiply_ring<C, kMore>(A, B, i0, j0, c0, c1, nk, s0, acc);
+    return;
+  }
   // In 8-wave tiles half of the waves load a chunk, the halves alternating: the two waves of a SIMD
   // are in different halves, so one of them keeps the matrix core busy while the other feeds the
   // memory pipeline.
@@ -311,8 +437,12 @@ struct Region {
   static constexpr int kBytes = C::WM * kRowBytes;
   lds_u8* p;
   int lane;
-  __device__ __forceinline__ Region(lds_u8* base, int wave, int lane_)
-      : p(base + wave * kBytes), lane(lane_) {}
+  // from the block's two LDS arrays
+  __device__ __forceinline__ Region(lds_u8* s0, lds_u8* s1, int wave, int lane_) : lane(lane_) {
+    constexpr int kFirst = C::kLds0 / kBytes;  // regions that fit the first
+    static_assert(kFirst >= C::kWaves || kFirst + C::kLds1 / kBytes >= C::kWaves, "regions fit");
+    p = wave < kFirst ? s0 + wave * kBytes : s1 + (wave - kFirst) * kBytes;
+  }
   // Unit swizzle: the writes of 16 rows at one unit meet on no bank as row bits 1-3 enter, the
   // transposing reads (4 rows x 2 blocks of 8 rows at two units) as bits 1 and 3 enter above bit 0.
   static __device__ __forceinline__ int swz(int row) {

@@ -194,7 +194,7 @@ struct Symmetric {
   Batch l, r;
   _Float16* out;
   const _Float16 *m1, *m2;  // or NULL
-  int64_t stride, n, ld;    // of out, m1 and m2
+  int64_t stride, n, ld;    // of out, m1 and m2: n rows, zeros behind column n
   float f, f1, f2, diag;
 };
 
@@ -203,8 +203,8 @@ struct Symmetric {
 template <class C>
 __global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Symmetric a, Symmetric b,
                                                                    int tiles) {
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kLds0];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kLds1];
   const Symmetric& p = blockIdx.y == 0 ? a : b;
   const int64_t id = regroup(blockIdx.x, gridDim.x);
   const int64_t item = uniform64(id / tiles);
@@ -220,9 +220,7 @@ __global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Symmetric a, 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   const int G = lane >> 4, r = lane & 15;
-  constexpr int kFirst = C::kStageBytes / Region<C>::kBytes;
-  const Region<C> region(wave < kFirst ? (lds_u8*)s0 : (lds_u8*)s1,
-                         wave < kFirst ? wave : wave - kFirst, lane);
+  const Region<C> region((lds_u8*)s0, (lds_u8*)s1, wave, lane);
   const int64_t r0 = i0 + wm * C::WM, q0 = j0 + wn * C::WN;
   const int64_t at = item * p.stride;
   const bool one = p.m1 != nullptr, two = p.m2 != nullptr;
@@ -274,8 +272,8 @@ template <class C, bool kBoth>
 __global__ __launch_bounds__(C::kThreads) void ns_gram_part_kernel(Batch hi, Batch lo, int tiles,
                                                                    int splits,
                                                                    float* __restrict__ parts) {
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kLds0];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kLds1];
   const int64_t item = blockIdx.x / (tiles * splits);
   const int rest = static_cast<int>(blockIdx.x - item * tiles * splits);
   const int split = rest / tiles;
@@ -528,7 +526,7 @@ __global__ __launch_bounds__(64 * kTiles) void ns_core_kernel(const float* __res
   }
   if (row >= n) return;
   const int64_t at = int64_t(blockIdx.x) * stride + int64_t(row) * ld;
-  for (int j = 0; 16 * j < ld; ++j) {  // 16 kTiles columns and the zeros behind them, up to ld
+  for (int j = 0; 16 * j < ld; ++j) {  // 16 kTiles columns and the zeros behind them
     const int col = 16 * j + 4 * core.G;
     uint32_t h0 = 0, h1 = 0, l0 = 0, l1 = 0;
 #pragma unroll
@@ -560,8 +558,8 @@ struct Apply {
 template <class C, bool kBoth>
 __global__ __launch_bounds__(C::kThreads) void ns_apply_kernel(Batch A, Batch B, Items it, Apply p,
                                                                int64_t tiles_i, int64_t tiles_j) {
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kLds0];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kLds1];
   const int64_t id = regroup(blockIdx.x, gridDim.x);
   const int64_t item = uniform64(id / (tiles_i * tiles_j));
   int64_t ti, tj;
@@ -588,9 +586,7 @@ __global__ __launch_bounds__(C::kThreads) void ns_apply_kernel(Batch A, Batch B,
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   const int G = lane >> 4, r = lane & 15;
-  constexpr int kFirst = C::kStageBytes / Region<C>::kBytes;
-  const Region<C> region(wave < kFirst ? (lds_u8*)s0 : (lds_u8*)s1,
-                         wave < kFirst ? wave : wave - kFirst, lane);
+  const Region<C> region((lds_u8*)s0, (lds_u8*)s1, wave, lane);
   const int64_t r0 = i0 + wm * C::WM, q0 = j0 + wn * C::WN;
   const _Float16* hi = p.hi + item * p.stride;
   _Float16* lo = p.lo + item * p.stride;
@@ -710,9 +706,15 @@ template <bool kTransA, bool kTransB>
 using BigTile = Tile<256, 256, 2, 4, kTransA, kTransB, true>;
 template <bool kTransA, bool kTransB>
 using SmallTile = Tile<128, 128, 2, 2, kTransA, kTransB, true>;
+template <bool kTransA, bool kTransB>
+using DeepTile = Tile<128, 128, 2, 2, kTransA, kTransB, true, 4>;
 
-// Whether 256x256 tiles of `tiles` per matrix fill half of the chip.
-inline bool use_big(int64_t count, int64_t tiles) { return count * tiles >= kFill / 2; }
+// Tile shape by the tiles of all matrices: 256x256 where they fill half of the chip, else 128x128, with
+// a ring of four stages where no CU gets a second block.
+enum Shape { kBig, kSmall, kDeep };
+inline Shape pick(int64_t tiles256, int64_t tiles128) {
+  return tiles256 >= kFill / 2 ? kBig : tiles128 > kFill ? kSmall : kDeep;
+}
 
 template <class C>
 void launch_symmetric(const Symmetric& a, const Symmetric* b, int64_t count, hipStream_t s) {
@@ -780,7 +782,7 @@ struct Run {
   const puro_newton_schulz_params& h;
   int64_t count, rows, cols;
   hipStream_t s;
-  bool big_s, big_x;
+  Shape shape_s, shape_x;
 
   Batch square(const _Float16* m) const { return {m, p.s_stride, p.side, p.lds, p.lds}; }
   Batch whole(const _Float16* x) const { return {x, p.x_stride, rows, p.ldx, p.ldx}; }
@@ -791,10 +793,16 @@ struct Run {
     return {square(l), square(r), out, m1, m2, p.s_stride, p.side, p.lds, f, f1, f2, diag};
   }
   void symmetric(const Symmetric& a, const Symmetric* b = nullptr) const {
-    if (big_s)
-      launch_symmetric<BigTile<false, false>>(a, b, count, s);
+    launch<false>(a, b);
+  }
+  template <bool kTrans>
+  void launch(const Symmetric& a, const Symmetric* b) const {
+    if (shape_s == kBig)
+      launch_symmetric<BigTile<kTrans, kTrans>>(a, b, count, s);
+    else if (shape_s == kSmall)
+      launch_symmetric<SmallTile<kTrans, kTrans>>(a, b, count, s);
     else
-      launch_symmetric<SmallTile<false, false>>(a, b, count, s);
+      launch_symmetric<DeepTile<kTrans, kTrans>>(a, b, count, s);
   }
 
   template <bool kTrans>
@@ -803,7 +811,7 @@ struct Run {
     if (p.short_side || p.splits > 1) {
       const dim3 grid(static_cast<uint32_t>(count * p.splits * p.tiles));
       const int tiles = static_cast<int>(p.tiles), splits = static_cast<int>(p.splits);
-      using C = SmallTile<kTrans, kTrans>;
+      using C = DeepTile<kTrans, kTrans>;
       if (out == nullptr) {
         hipLaunchKernelGGL((ns_gram_part_kernel<C, true>), grid, dim3(C::kThreads), 0, s, X,
                            whole(p.lo), tiles, splits, p.gram);
@@ -818,10 +826,7 @@ struct Run {
     }
     const Symmetric a = {X, X, out, nullptr, nullptr, p.s_stride, p.side, p.lds, kA / kX / kX,
                          0.0f, 0.0f, 0.0f};
-    if (big_s)
-      launch_symmetric<BigTile<kTrans, kTrans>>(a, nullptr, count, s);
-    else
-      launch_symmetric<SmallTile<kTrans, kTrans>>(a, nullptr, count, s);
+    launch<kTrans>(a, nullptr);
   }
 
   // X (half n) becomes f P X + add X
@@ -846,21 +851,20 @@ struct Run {
       ap.x_lo[p.tall ? 1 : 0] = M;
       ap.p_lo[p.tall ? 0 : 1] = X;
       ap.p_lo[p.tall ? 1 : 0] = square(p.s[1]);
-      if (p.tall)
-        launch_apply<SmallTile<false, false>, true>(X, M, it, ap, count, s);
-      else
-        launch_apply<SmallTile<false, true>, true>(M, X, it, ap, count, s);
-    } else if (p.tall) {
-      if (big_x)
-        launch_apply<BigTile<false, false>, false>(X, M, it, ap, count, s);
-      else
-        launch_apply<SmallTile<false, false>, false>(X, M, it, ap, count, s);
-    } else {
-      if (big_x)
-        launch_apply<BigTile<false, true>, false>(M, X, it, ap, count, s);
-      else
-        launch_apply<SmallTile<false, true>, false>(M, X, it, ap, count, s);
     }
+    if (p.tall)
+      launch_shape<false, kBoth>(X, M, ap);
+    else
+      launch_shape<true, kBoth>(M, X, ap);
+  }
+  template <bool kTransB, bool kBoth>
+  void launch_shape(const Batch& A, const Batch& B, const Apply& ap) const {
+    if (!kBoth && shape_x == kBig)
+      launch_apply<BigTile<false, kTransB>, false>(A, B, it, ap, count, s);
+    else if (shape_x == kDeep)
+      launch_apply<DeepTile<false, kTransB>, kBoth>(A, B, it, ap, count, s);
+    else
+      launch_apply<SmallTile<false, kTransB>, kBoth>(A, B, it, ap, count, s);
   }
 
   // All steps on A alone.
@@ -983,8 +987,9 @@ extern "C" puro_status puro_newton_schulz(const puro_ns_item* items, int count, 
   }
   const int64_t side_tiles = tiles_of(p.side, 256);
   const Run run = {p, it, *hp, count, rows, cols, s,
-                   use_big(count, side_tiles * (side_tiles + 1) / 2),
-                   use_big(count, tiles_of(rows, 256) * tiles_of(cols, 256))};
+                   pick(count * (side_tiles * (side_tiles + 1) / 2), count * p.tiles),
+                   pick(count * tiles_of(rows, 256) * tiles_of(cols, 256),
+                        count * tiles_of(rows, 128) * tiles_of(cols, 128))};
   if (p.short_side) {
     // The largest power of two (up to 64) with which the product of all polynomials fits fp16. With a
     // growth above 1e5 (nine steps of the default coefficients) errors of A pass 2e-3 of u: step by step.

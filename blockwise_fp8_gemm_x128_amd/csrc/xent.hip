@@ -11,7 +11,7 @@
 // P is then read along its rows (dh) and along its columns (dw). Rows of a piece of dw are complete
 // at once; dh is summed over the pieces in fp32.
 //
-// P is rounded to bf16 (half a step, 2^-9 of each element, like any operand of the head's
+// P is rounded to bf16 (at most half a step, 2^-8 of each element, like any operand of the head's
 // products): its rounding errors are independent, so the sums over tokens or vocabulary they enter
 // carry a smaller one. Everything else is fp32 until an output is rounded.
 #include <math.h>
@@ -28,6 +28,11 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 // A token has a target where the target lies in the vocabulary.
 __device__ __forceinline__ bool has_target(int64_t y, int64_t vocab) { return y >= 0 && y < vocab; }
+
+// A token's target as a column of the tile from vocabulary entry `from` on, -1 where it lies outside.
+__device__ __forceinline__ int tile_column(int64_t y, int64_t from, int columns, int64_t vocab) {
+  return has_target(y, vocab) && y >= from && y < from + columns ? static_cast<int>(y - from) : -1;
+}
 
 // ------------------------------------------------------------------ forward
 struct Stat {
@@ -61,12 +66,18 @@ template <class C>
 __global__ __launch_bounds__(C::kThreads) void xent_stats_kernel(
     Operand h, Operand w, const int64_t* __restrict__ targets, int64_t tiles_i, int64_t tiles_j,
     Stat* __restrict__ stats, float* __restrict__ at) {
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kLds0];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kLds1];
   int64_t ti, tj;
   tile_at(regroup(blockIdx.x, tiles_i * tiles_j), tiles_i, tiles_j, 4, ti, tj);
   const int64_t i0 = uniform64(ti * C::BM), j0 = uniform64(tj * C::BN);
   const int64_t nk = (h.cols + kChunk - 1) / kChunk;
+  // Row threadIdx.x's target as a column of the tile, asked for ahead of the products: at their end
+  // it would be a wait of a microsecond for every 16 rows.
+  static_assert(C::kThreads >= C::BM, "a thread per row");
+  int target = -1;
+  if (threadIdx.x < C::BM && i0 + threadIdx.x < h.rows)
+    target = tile_column(targets[i0 + threadIdx.x], j0, C::BN, w.rows);
   v4f acc[C::MI][C::NJ];
   multiply<C>(h, w, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
 
@@ -85,6 +96,9 @@ __global__ __launch_bounds__(C::kThreads) void xent_stats_kernel(
   }
   __syncthreads();  // the stages are free
   lds_f32* sh = (lds_f32*)s0;  // [WAVES_N][BM][2]
+  lds_i32* at_column = (lds_i32*)(sh + 2 * C::WAVES_N * C::BM);  // [BM]
+  if (threadIdx.x < C::BM) at_column[threadIdx.x] = target;
+  __syncthreads();
 #pragma unroll
   for (int mi = 0; mi < C::MI; ++mi) {
     const int row = wm * C::WM + 16 * mi + r;
@@ -106,18 +120,15 @@ __global__ __launch_bounds__(C::kThreads) void xent_stats_kernel(
       sh[2 * (wn * C::BM + row)] = m;
       sh[2 * (wn * C::BM + row) + 1] = s;
     }
-    if (i0 + row < h.rows) {
-      const int64_t y = targets[i0 + row];
-      const int64_t d = y - col;
-      if (has_target(y, w.rows) && d >= 0 && d < C::WN && (d & 15) < 4) {
-        float l = 0.0f;
+    const int d = at_column[row] - (wn * C::WN + 4 * G);
+    if (d >= 0 && d < C::WN && (d & 15) < 4) {
+      float l = 0.0f;
 #pragma unroll
-        for (int nj = 0; nj < C::NJ; ++nj)
+      for (int nj = 0; nj < C::NJ; ++nj)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (d == 16 * nj + k) l = acc[mi][nj][k];
-        at[i0 + row] = l;
-      }
+        for (int k = 0; k < 4; ++k)
+          if (d == 16 * nj + k) l = acc[mi][nj][k];
+      at[i0 + row] = l;
     }
   }
   __syncthreads();
@@ -190,19 +201,31 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const uint16_t* __restri
 
 // ------------------------------------------------------------------ backward
 // A piece of P: vocabulary [v0, v0 + w.rows) (w is the piece's weights), P [tokens][ldp]; columns
-// behind the vocabulary are written as zeros to the end of their tile, or up to ldp.
+// behind the vocabulary are written as zeros to the end of their tile.
 template <class C>
 __global__ __launch_bounds__(C::kThreads) void xent_p_kernel(
     Operand h, Operand w, const int64_t* __restrict__ targets, int64_t v0, int64_t vocab,
     const float* __restrict__ lse, const float* __restrict__ dloss,
     const float* __restrict__ dlse, int64_t tiles_i, int64_t tiles_j, uint16_t* __restrict__ P,
     int64_t ldp) {
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kLds0];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kLds1];
   int64_t ti, tj;
   tile_at(regroup(blockIdx.x, tiles_i * tiles_j), tiles_i, tiles_j, 4, ti, tj);
   const int64_t i0 = uniform64(ti * C::BM), j0 = uniform64(tj * C::BN);
   const int64_t nk = (h.cols + kChunk - 1) / kChunk;
+  // Row threadIdx.x's values, asked for ahead of the products (as in the forward kernel): lse log2 e,
+  // the softmax's factor, the target's, and the target as a column of the tile; -2 without a target.
+  static_assert(C::kThreads >= C::BM, "a thread per row");
+  v4f mine = {0.0f, 0.0f, 0.0f, __int_as_float(-2)};
+  if (threadIdx.x < C::BM && i0 + threadIdx.x < h.rows) {
+    const int64_t t = i0 + threadIdx.x, y = targets[t];
+    if (has_target(y, vocab)) {
+      const float hot = dloss[t];
+      mine = {lse[t] * kLog2e, dlse == nullptr ? hot : hot + dlse[t], hot,
+              __int_as_float(tile_column(y, v0 + j0, C::BN, vocab))};
+    }
+  }
   v4f acc[C::MI][C::NJ];
   multiply<C>(h, w, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
   __syncthreads();
@@ -210,29 +233,23 @@ __global__ __launch_bounds__(C::kThreads) void xent_p_kernel(
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   const int G = lane >> 4, r = lane & 15;
-  static_assert(Region<C>::kBytes * C::kWaves <= 2 * C::kStageBytes, "regions fit the stages");
-  constexpr int kFirst = C::kStageBytes / Region<C>::kBytes;  // regions of the first stage
-  const Region<C> region(wave < kFirst ? (lds_u8*)s0 : (lds_u8*)s1,
-                         wave < kFirst ? wave : wave - kFirst, lane);
+  lds_v4f* rows = (lds_v4f*)s0;  // [BM]
+  if (threadIdx.x < C::BM) rows[threadIdx.x] = mine;
+  __syncthreads();
+  v4f row[C::MI];
+#pragma unroll
+  for (int mi = 0; mi < C::MI; ++mi) row[mi] = rows[wm * C::WM + 16 * mi + r];
+  __syncthreads();  // the regions below lie over them
+  const Region<C> region((lds_u8*)s0, (lds_u8*)s1, wave, lane);
   const int64_t col = j0 + wn * C::WN + 4 * G;
   const bool edge = j0 + C::BN > w.rows;
 #pragma unroll
   for (int mi = 0; mi < C::MI; ++mi) {
-    const int64_t t = i0 + wm * C::WM + 16 * mi + r;
-    float base = 0.0f, every = 0.0f, hot = 0.0f;
-    int64_t d = -1;
-    bool has = false;
-    if (t < h.rows) {
-      const int64_t y = targets[t];
-      has = has_target(y, vocab);
-      if (has) {
-        base = lse[t] * kLog2e;
-        hot = dloss[t];
-        every = dlse == nullptr ? hot : hot + dlse[t];
-        d = y - v0 - col;
-      }
-    }
-    const bool here = d >= 0 && d < C::WN && (d & 15) < 4;
+    const float base = row[mi][0], every = row[mi][1], hot = row[mi][2];
+    const int target = __float_as_int(row[mi][3]);
+    const bool has = target != -2;
+    const int d = target - (wn * C::WN + 4 * G);
+    const bool here = target >= 0 && d >= 0 && d < C::WN && (d & 15) < 4;
 #pragma unroll
     for (int nj = 0; nj < C::NJ; ++nj) {
       v4f p;
@@ -252,7 +269,6 @@ __global__ __launch_bounds__(C::kThreads) void xent_p_kernel(
   }
   region.settle();
   const int64_t q0 = j0 + wn * C::WN;
-  if (q0 >= ldp) return;
 #pragma unroll
   for (int n = 0; n < C::WM / 8; ++n) {
     const v4i v = region.row8(n);
@@ -278,8 +294,8 @@ __global__ __launch_bounds__(C::kThreads) void xent_product_kernel(Operand A, Op
                                                                    int64_t tiles_i,
                                                                    int64_t tiles_j, int splits,
                                                                    int64_t band, Dest out) {
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kStageBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kLds0];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kLds1];
   const int64_t tiles = tiles_i * tiles_j;
   const int64_t b = regroup(blockIdx.x, tiles * splits);
   const int64_t split = b / tiles;
@@ -321,9 +337,7 @@ __global__ __launch_bounds__(C::kThreads) void xent_product_kernel(Operand A, Op
     if (out.kind == kFp32) return;
   }
   __syncthreads();
-  constexpr int kFirst = C::kStageBytes / Region<C>::kBytes;
-  const Region<C> region(wave < kFirst ? (lds_u8*)s0 : (lds_u8*)s1,
-                         wave < kFirst ? wave : wave - kFirst, lane);
+  const Region<C> region((lds_u8*)s0, (lds_u8*)s1, wave, lane);
 #pragma unroll
   for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
@@ -348,11 +362,13 @@ __global__ __launch_bounds__(C::kThreads) void xent_product_kernel(Operand A, Op
   }
 }
 
-// The sum of `splits` partial products, rounded to bf16: [rows][ldf] fp32 each -> [rows][cols].
+// The sum of `splits` partial products, [rows][ldf] fp32 each, as bf16 [rows][cols] (out), or stored in or
+// added to fp32 [rows][cols] (out32).
 __global__ __launch_bounds__(256) void xent_sum_kernel(const float* __restrict__ f, int splits,
                                                        int64_t split_stride, int64_t rows,
                                                        int64_t cols, int64_t ldf,
-                                                       uint16_t* __restrict__ out) {
+                                                       uint16_t* __restrict__ out,
+                                                       float* __restrict__ out32, bool add) {
   const int64_t groups = ldf / 4;
   for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < rows * groups;
        n += int64_t(gridDim.x) * 256) {
@@ -360,6 +376,13 @@ __global__ __launch_bounds__(256) void xent_sum_kernel(const float* __restrict__
     v4f a = *reinterpret_cast<const v4f*>(f + row * ldf + c);
     for (int s = 1; s < splits; ++s)
       a += *reinterpret_cast<const v4f*>(f + s * split_stride + row * ldf + c);
+    if (out32 != nullptr) {
+      float* p = out32 + row * cols + c;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < cols) p[e] = add ? p[e] + a[e] : a[e];
+      continue;
+    }
     const uint32_t lo = pack_bf16x2(a[0], a[1]), hi = pack_bf16x2(a[2], a[3]);
     uint16_t* p = out + row * cols + c;
     if (cols % 4 == 0) {
@@ -383,7 +406,11 @@ __global__ __launch_bounds__(256) void xent_zero_kernel(uint32_t* __restrict__ p
 constexpr int64_t kMaxTokens = PURO_XENT_MAX_TOKENS;
 constexpr int64_t kMaxD = PURO_XENT_MAX_D;
 constexpr int64_t kFill = 256;                       // compute units: tiles that fill the chip
-constexpr int64_t kPieceBytes = int64_t(512) << 20;  // of a piece of P
+// A piece of P: small enough that the memory-side cache (256 MB) holds it with the operands until both
+// gradients have read it (8192 x 2048 x 131072: 10.2 ms, against 10.5 with 256 MB, 10.6 with 512),
+// but as many columns as fill the chip with 256x256 tiles of dw, as long as it stays below the second
+// bound (8192 x 131072 with 64 MB, half of that: 13.8 ms; 8000 x 256 x 20000 in one piece 437 us, in three 531).
+constexpr int64_t kPieceBytes = int64_t(128) << 20, kMostBytes = int64_t(1) << 30;
 
 inline int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 inline int64_t tiles_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
@@ -421,27 +448,38 @@ struct Carver {
   }
 };
 
-// Tile shapes: 64x256 for up to 64 rows (one read of the other operand), 256x256 where such tiles
-// fill the chip, 128x128 below.
+// Tile shapes: 64x128 for up to 64 rows (a ring of three stages, two blocks a CU: one read of the other
+// operand, enough of it under way to keep the memory busy), 256x256, and 128x128 with two blocks a CU.
 enum Shape { kFlat, kBig, kSmall };
-inline Shape pick(int64_t i, int64_t j) {
-  if (i <= 64) return kFlat;
-  return tiles_of(i, 256) * tiles_of(j, 256) >= kFill ? kBig : kSmall;
-}
 inline int64_t bm_of(Shape s) { return s == kFlat ? 64 : s == kBig ? 256 : 128; }
-inline int64_t bn_of(Shape s) { return s == kSmall ? 128 : 256; }
+inline int64_t bn_of(Shape s) { return s == kBig ? 256 : 128; }
 template <bool kTransA, bool kTransB>
-using FlatTile = Tile<64, 256, 1, 4, kTransA, kTransB, false>;
+using FlatTile = Tile<64, 128, 2, 2, kTransA, kTransB, false, 3>;
 template <bool kTransA, bool kTransB>
 using BigTile = Tile<256, 256, 2, 4, kTransA, kTransB, false>;
 template <bool kTransA, bool kTransB>
 using SmallTile = Tile<128, 128, 2, 2, kTransA, kTransB, false>;
 
+// The shape for an i x j product, by rounds of 256x256 tiles over the chip. A last round of few of
+// them costs less than a whole one; a round of 128x128 tiles, two on every CU, costs 0.7, or 0.35 with one
+// (measured on the forward kernel: 777 x 50021 x 1000, 784 big tiles 119 us, 2737 small 140; 8192 x
+// 131072 x 2048 3.6 ms against 4.4).
+inline Shape pick(int64_t i, int64_t j) {
+  if (i <= 64) return kFlat;
+  const int64_t big = tiles_of(i, 256) * tiles_of(j, 256);
+  const int64_t small = tiles_of(i, 128) * tiles_of(j, 128);
+  const int64_t big_rest = big % kFill, small_rest = small % (2 * kFill);
+  const double big_cost = double(big / kFill) + (big_rest ? 0.42 + 0.58 * big_rest / kFill : 0.0);
+  const double small_cost = 0.7 * double(small / (2 * kFill)) +
+                            (small_rest == 0 ? 0.0 : small_rest <= kFill ? 0.35 : 0.7);
+  return small_cost < big_cost ? kSmall : kBig;
+}
+
 struct FwdPlan {
   bool copy_h, copy_w;
   int64_t ldp;  // row stride of copies
   Shape shape;
-  int64_t tiles_i, tiles_j;
+  int64_t tiles;  // of the vocabulary
   Stat* stats;
   float* at;
   uint16_t *h, *w;
@@ -454,10 +492,9 @@ FwdPlan plan_fwd(const puro_linear_xent& x, void* ws) {
   p.copy_w = !direct(x.w, x.d, x.ldw);
   p.ldp = up(x.d, kChunk);
   p.shape = pick(x.tokens, x.vocab);
-  p.tiles_i = tiles_of(x.tokens, bm_of(p.shape));
-  p.tiles_j = tiles_of(x.vocab, bn_of(p.shape));
+  p.tiles = tiles_of(x.vocab, bn_of(p.shape));
   Carver c{static_cast<uint8_t*>(ws)};
-  p.stats = c.take<Stat>(p.tiles_j * x.tokens);
+  p.stats = c.take<Stat>(p.tiles * x.tokens);
   p.at = c.take<float>(x.tokens);
   p.h = c.take<uint16_t>(p.copy_h ? x.tokens * p.ldp : 0);
   p.w = c.take<uint16_t>(p.copy_w ? x.vocab * p.ldp : 0);
@@ -484,8 +521,7 @@ puro_status check_fwd(const puro_linear_xent* x) {
   PURO_TRY(check_elements(x->targets, 8));
   PURO_TRY(check_elements(x->loss, 4));
   PURO_TRY(check_elements(x->lse, 4));
-  const Shape s = pick(x->tokens, x->vocab);
-  if (!grid_ok(tiles_of(x->tokens, bm_of(s)) * tiles_of(x->vocab, bn_of(s)), 512))
+  if (!grid_ok(tiles_of(x->tokens, x->tokens <= 64 ? 64 : 128) * tiles_of(x->vocab, 128), 512))
     return PURO_ERR_SHAPE;
   return PURO_OK;
 }
@@ -493,19 +529,39 @@ puro_status check_fwd(const puro_linear_xent* x) {
 template <class C>
 void launch_stats(const FwdPlan& p, const Operand& h, const Operand& w, const int64_t* targets,
                   hipStream_t s) {
-  hipLaunchKernelGGL(xent_stats_kernel<C>, dim3(static_cast<uint32_t>(p.tiles_i * p.tiles_j)),
-                     dim3(C::kThreads), 0, s, h, w, targets, p.tiles_i, p.tiles_j, p.stats, p.at);
+  const int64_t ti = tiles_of(h.rows, C::BM);
+  hipLaunchKernelGGL(xent_stats_kernel<C>, dim3(static_cast<uint32_t>(ti * p.tiles)),
+                     dim3(C::kThreads), 0, s, h, w, targets, ti, p.tiles, p.stats, p.at);
+}
+
+// A product whose output has few tiles for a reduction of `k`: the reduction is split until the tiles
+// fill the chip, eight chunks a split at least, and the partial sums are added by xent_sum_kernel.
+struct Split {
+  Shape shape;
+  int splits;
+};
+inline Split split(int64_t rows, int64_t cols, int64_t k) {
+  const int64_t longest = k / (8 * kChunk);
+  auto tiles = [&](Shape s) { return tiles_of(rows, bm_of(s)) * tiles_of(cols, bn_of(s)); };
+  Split r = {kFlat, 1};
+  if (rows > 64) r.shape = tiles(kBig) * longest >= kFill ? kBig : kSmall;
+  int64_t n = tiles(r.shape);
+  n = n > 0 ? kFill / n : 1;
+  if (n > longest) n = longest;
+  r.splits = static_cast<int>(n < 1 ? 1 : n);
+  // a short reduction is mostly the tiles' ends: two blocks a CU hide them behind each other
+  if (r.splits == 1 && rows > 64) r.shape = k <= 4 * kChunk ? kSmall : pick(rows, cols);
+  return r;
 }
 
 struct BwdPlan {
   bool copy_w;
-  int64_t ldh, ldw_copy;
+  int64_t ldh;  // row stride of copies
   int64_t piece, pieces;  // columns of a piece of P (its row stride), pieces
-  Shape p_shape, dh_shape, dw_shape;
-  int splits;
-  int64_t ldf;
+  Split dh_split, dw_split;
+  int64_t ldf;            // row stride of partial sums
   uint16_t *h, *w, *P;
-  float* dh;
+  float *dh, *dw;
   int64_t bytes;
 };
 
@@ -513,31 +569,26 @@ BwdPlan plan_bwd(const puro_linear_xent_grad& x, void* ws) {
   BwdPlan p;
   p.copy_w = !direct(x.w, x.d, x.ldw);
   p.ldh = up(x.d, kChunk);
-  p.ldw_copy = up(x.d, kChunk);
-  const int64_t most = up(kPieceBytes / (2 * (x.tokens > 0 ? x.tokens : 1)) + 1, 256);
-  p.pieces = tiles_of(x.vocab, most < 4096 ? 4096 : most > (1 << 20) ? 1 << 20 : most);
+  const int64_t row = 2 * (x.tokens > 0 ? x.tokens : 1);
+  int64_t most = kPieceBytes / row;
+  const int64_t filling = 256 * tiles_of(kFill, tiles_of(x.d, 256));
+  if (most < filling) most = filling * row <= kMostBytes ? filling : kMostBytes / row;
+  if (most < 4096) most = 4096;
+  if (most > 1 << 20) most = 1 << 20;
+  p.pieces = tiles_of(x.vocab, up(most, 256));
   p.piece = up(tiles_of(x.vocab, p.pieces), 256);
   p.pieces = tiles_of(x.vocab, p.piece);
-  p.p_shape = pick(x.tokens, p.piece);
-  p.dw_shape = tiles_of(p.piece, 256) * tiles_of(x.d, 256) >= kFill ? kBig : kSmall;
-  // dh: a small output with a long reduction, split until its tiles fill the chip
-  p.dh_shape = x.tokens <= 64 ? kFlat : kBig;
-  if (p.dh_shape == kBig && tiles_of(x.tokens, 256) * tiles_of(x.d, 256) * (p.piece / 512) < kFill)
-    p.dh_shape = kSmall;
-  const int64_t tiles =
-      tiles_of(x.tokens, bm_of(p.dh_shape)) * tiles_of(x.d, bn_of(p.dh_shape));
-  int64_t splits = tiles > 0 ? kFill / tiles : 1;
-  const int64_t longest = p.piece / 512;  // eight chunks a split at least
-  if (splits > longest) splits = longest;
-  if (splits < 1) splits = 1;
-  p.splits = static_cast<int>(splits);
+  p.dh_split = split(x.tokens, x.d, p.piece);
+  p.dw_split = split(p.piece > 64 ? p.piece : 65, x.d, x.tokens);
   p.ldf = up(x.d, 4);
   Carver c{static_cast<uint8_t*>(ws)};
   p.h = c.take<uint16_t>(x.tokens * p.ldh);
-  p.w = c.take<uint16_t>(p.copy_w ? x.vocab * p.ldw_copy : 0);
+  p.w = c.take<uint16_t>(p.copy_w ? x.vocab * p.ldh : 0);
   p.P = c.take<uint16_t>(x.tokens * p.piece);
-  p.dh = c.take<float>(x.dh != nullptr && (p.splits > 1 || p.pieces > 1)
-                           ? p.splits * x.tokens * p.ldf : 0);
+  p.dh = c.take<float>(x.dh != nullptr && (p.dh_split.splits > 1 || p.pieces > 1)
+                           ? p.dh_split.splits * x.tokens * p.ldf : 0);
+  p.dw = c.take<float>(x.dw != nullptr && p.dw_split.splits > 1
+                           ? p.dw_split.splits * p.piece * p.ldf : 0);
   p.bytes = c.used;
   return p;
 }
@@ -560,7 +611,7 @@ puro_status check_bwd(const puro_linear_xent_grad* x) {
   const BwdPlan p = plan_bwd(*x, nullptr);
   if (!grid_ok(tiles_of(x->tokens, 64) * tiles_of(p.piece, 128), 512) ||
       !grid_ok(tiles_of(p.piece, 128) * tiles_of(x->d, 128), 512) ||
-      !grid_ok(tiles_of(x->tokens, 64) * tiles_of(x->d, 128) * p.splits, 512))
+      !grid_ok(tiles_of(x->tokens, 64) * tiles_of(x->d, 128) * p.dh_split.splits, 512))
     return PURO_ERR_SHAPE;
   return PURO_OK;
 }
@@ -616,11 +667,12 @@ extern "C" puro_status puro_linear_xent_fwd(const puro_linear_xent* desc, void* 
     launch_stats<BigTile<false, false>>(p, h, w, x.targets, s);
   else
     launch_stats<SmallTile<false, false>>(p, h, w, x.targets, s);
+  // as many blocks as fill the chip, but eight tokens (64 bytes of a tile's statistics) each
   int per = 64;
-  while (per > 1 && per / 2 >= x.tokens) per /= 2;
+  while (per > 1 && (per / 2 >= x.tokens || (per > 8 && tiles_of(x.tokens, per) < kFill))) per /= 2;
   hipLaunchKernelGGL(xent_join_kernel, dim3(static_cast<uint32_t>(tiles_of(x.tokens, per))),
                      dim3(kJoinThreads), 0, s, p.stats, p.at, x.targets, x.tokens, x.vocab,
-                     p.tiles_j, per, x.loss, x.lse);
+                     p.tiles, per, x.loss, x.lse);
   return launch_status();
 }
 
@@ -650,40 +702,28 @@ extern "C" puro_status puro_linear_xent_bwd(const puro_linear_xent_grad* desc, v
   const Operand h = operand(p.h, x.tokens, p.ldh, p.ldh);
   Operand w = operand(x.w, x.vocab, x.d, x.ldw);
   if (p.copy_w) {
-    copy_rows(x.w, x.vocab, x.d, x.ldw, nullptr, 0, p.w, p.ldw_copy, s);
-    w = operand(p.w, x.vocab, p.ldw_copy, p.ldw_copy);
+    copy_rows(x.w, x.vocab, x.d, x.ldw, nullptr, 0, p.w, p.ldh, s);
+    w = operand(p.w, x.vocab, p.ldh, p.ldh);
   }
   const bool f32 = x.dw_type == PURO_TYPE_FP32;
   for (int64_t n = 0; n < p.pieces; ++n) {
     const int64_t v0 = n * p.piece;
     const int64_t vn = x.vocab - v0 < p.piece ? x.vocab - v0 : p.piece;
     const Operand wp = operand(w.p + 2 * v0 * w.ld, vn, w.cols, w.ld);
-    if (p.p_shape == kFlat)
+    const Shape shape = pick(x.tokens, vn);
+    if (shape == kFlat)
       launch_p<FlatTile<false, false>>(p, x, h, wp, v0, s);
-    else if (p.p_shape == kBig)
+    else if (shape == kBig)
       launch_p<BigTile<false, false>>(p, x, h, wp, v0, s);
     else
       launch_p<SmallTile<false, false>>(p, x, h, wp, v0, s);
-    if (x.dw != nullptr) {
-      const Operand a = operand(p.P, x.tokens, p.piece, p.piece);
-      Dest out = {};
-      out.kind = f32 ? kFp32 : kBf16;
-      out.add = x.accumulate != 0;
-      out.f = f32 ? static_cast<float*>(x.dw) + v0 * x.d : nullptr;
-      out.b = f32 ? nullptr : static_cast<uint16_t*>(x.dw) + v0 * x.d;
-      out.rows = vn;
-      out.cols = out.ldf = out.ldb = x.d;
-      if (p.dw_shape == kBig)
-        launch_product<BigTile<true, true>>(a, h, 1, 4, out, s);
-      else
-        launch_product<SmallTile<true, true>>(a, h, 1, 8, out, s);
-    }
+    // dh first: the piece of w that P was made from is still in the memory-side cache
     if (x.dh != nullptr) {
       // the piece's reduction: its columns of P (zeros behind the vocabulary) and rows of w
       const Operand a = operand(p.P, x.tokens, up(vn, kChunk), p.piece);
-      const bool once = p.splits == 1;
+      const int splits = p.dh_split.splits;
       Dest out = {};
-      out.kind = !once || n + 1 < p.pieces ? kFp32 : p.pieces == 1 ? kBf16 : kJoin;
+      out.kind = splits > 1 || n + 1 < p.pieces ? kFp32 : p.pieces == 1 ? kBf16 : kJoin;
       out.add = n > 0;
       out.f = p.dh;
       out.b = static_cast<uint16_t*>(x.dh);
@@ -692,17 +732,41 @@ extern "C" puro_status puro_linear_xent_bwd(const puro_linear_xent_grad* desc, v
       out.ldf = p.ldf;
       out.ldb = x.d;
       out.split_stride = x.tokens * p.ldf;
-      if (p.dh_shape == kFlat)
-        launch_product<FlatTile<false, true>>(a, wp, p.splits, 4, out, s);
-      else if (p.dh_shape == kBig)
-        launch_product<BigTile<false, true>>(a, wp, p.splits, 4, out, s);
+      if (p.dh_split.shape == kFlat)
+        launch_product<FlatTile<false, true>>(a, wp, splits, 4, out, s);
+      else if (p.dh_split.shape == kBig)
+        launch_product<BigTile<false, true>>(a, wp, splits, 4, out, s);
       else
-        launch_product<SmallTile<false, true>>(a, wp, p.splits, 8, out, s);
+        launch_product<SmallTile<false, true>>(a, wp, splits, 8, out, s);
+    }
+    if (x.dw != nullptr) {
+      // rows of dw: the piece's columns of P
+      const Operand a = operand(p.P, x.tokens, p.piece, p.piece);
+      const int splits = p.dw_split.splits;
+      float* dw32 = f32 ? static_cast<float*>(x.dw) + v0 * x.d : nullptr;
+      uint16_t* dw16 = f32 ? nullptr : static_cast<uint16_t*>(x.dw) + v0 * x.d;
+      Dest out = {};
+      out.kind = f32 || splits > 1 ? kFp32 : kBf16;
+      out.add = splits == 1 && x.accumulate != 0;
+      out.f = splits > 1 ? p.dw : dw32;
+      out.b = dw16;
+      out.rows = vn;
+      out.cols = out.ldb = x.d;
+      out.ldf = splits > 1 ? p.ldf : x.d;
+      out.split_stride = vn * p.ldf;
+      if (p.dw_split.shape == kBig)
+        launch_product<BigTile<true, true>>(a, h, splits, 4, out, s);
+      else
+        launch_product<SmallTile<true, true>>(a, h, splits, 8, out, s);
+      if (splits > 1)
+        hipLaunchKernelGGL(xent_sum_kernel, dim3(stream_grid(vn * (p.ldf / 4))), dim3(256), 0, s,
+                           p.dw, splits, vn * p.ldf, vn, x.d, p.ldf, dw16, dw32,
+                           x.accumulate != 0);
     }
   }
-  if (x.dh != nullptr && p.splits > 1)
+  if (x.dh != nullptr && p.dh_split.splits > 1)
     hipLaunchKernelGGL(xent_sum_kernel, dim3(stream_grid(x.tokens * (p.ldf / 4))), dim3(256), 0, s,
-                       p.dh, p.splits, x.tokens * p.ldf, x.tokens, x.d, p.ldf,
-                       static_cast<uint16_t*>(x.dh));
+                       p.dh, p.dh_split.splits, x.tokens * p.ldf, x.tokens, x.d, p.ldf,
+                       static_cast<uint16_t*>(x.dh), static_cast<float*>(nullptr), false);
   return launch_status();
 }
