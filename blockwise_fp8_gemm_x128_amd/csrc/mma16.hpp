@@ -429,6 +429,38 @@ __device__ __forceinline__ void tile_at(int64_t b, int64_t ti, int64_t tj, int64
   j = local / rows;
 }
 
+// Reads of another matrix at a wave's results (rows from r0, columns from q0): the four elements that a
+// lane needs beside tile (mi, nj), through a resource, so that a read behind the last row gives zeros
+// and no branch keeps the compiler from sending many at once (with branches, each waited for its own).
+// Columns behind the row's end read the next row: results there are not stored. T: 2 or 4 bytes.
+template <int kBytes>
+struct Beside {
+  rsrc_t r;
+  uint32_t lane_off, ld;
+  // rows x ld elements, at least up to the last row's `cols`
+  __device__ __forceinline__ Beside(const void* p, int64_t rows, int64_t cols, int64_t ld_, int64_t r0,
+                                    int64_t q0, int lane)
+      : ld(static_cast<uint32_t>(ld_) * kBytes) {
+    const int64_t at = uniform64(r0 * ld_ + q0);
+    r = make_rsrc(static_cast<const uint8_t*>(p) + at * kBytes,
+                  (uniform64((rows - 1) * ld_ + cols) - at) * kBytes);
+    lane_off = (lane & 15) * ld + 4 * (lane >> 4) * kBytes;
+  }
+  __device__ __forceinline__ uint32_t off(int mi, int nj) const {
+    return lane_off + 16 * mi * ld + 16 * nj * kBytes;
+  }
+  __device__ __forceinline__ v2i half4(int mi, int nj) const {
+    static_assert(kBytes == 2, "16-bit elements");
+    return __builtin_bit_cast(
+        v2i, __builtin_amdgcn_raw_buffer_load_b64(r, static_cast<int>(off(mi, nj)), 0, 0));
+  }
+  __device__ __forceinline__ v4f float4(int mi, int nj) const {
+    static_assert(kBytes == 4, "32-bit elements");
+    return __builtin_bit_cast(
+        v4f, __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off(mi, nj)), 0, 0));
+  }
+};
+
 // A wave's WM x 64 block as 16-bit values in its own LDS region, rows of 128 bytes with their
 // 16-byte units XOR-permuted: pack(mi, nj, value) gives the two dwords of four adjacent columns. The
 // region is then read by whole rows, or transposed.

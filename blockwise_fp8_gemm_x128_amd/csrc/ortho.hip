@@ -200,7 +200,8 @@ struct Symmetric {
 
 // Lower-triangle tiles of one or two (blockIdx.y) symmetric products of every item, each tile stored
 // as it is and mirrored.
-template <class C>
+// kMore: there is an M1 (and, where not NULL, an M2).
+template <class C, bool kMore>
 __global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Symmetric a, Symmetric b,
                                                                    int tiles) {
   __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kLds0];
@@ -223,25 +224,24 @@ __global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Symmetric a, 
   const Region<C> region((lds_u8*)s0, (lds_u8*)s1, wave, lane);
   const int64_t r0 = i0 + wm * C::WM, q0 = j0 + wn * C::WN;
   const int64_t at = item * p.stride;
-  const bool one = p.m1 != nullptr, two = p.m2 != nullptr;
+  // (without an M2 its reads are behind the last of no rows, and give zeros)
+  const Beside<2> m1(kMore ? p.m1 + at : p.out, kMore ? p.n : 0, p.ld, p.ld, r0, q0, lane);
+  const bool two = kMore && p.m2 != nullptr;
+  const Beside<2> m2(two ? p.m2 + at : p.out, two ? p.n : 0, p.ld, p.ld, r0, q0, lane);
 #pragma unroll
   for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
     for (int nj = 0; nj < C::NJ; ++nj) {
       v4f v = acc[mi][nj] * p.f;
-      const int64_t row = r0 + 16 * mi + r, col = q0 + 16 * nj + 4 * G;
-      if (one && row < p.n && col < p.ld) {
-        const v4h m = *reinterpret_cast<const v4h*>(p.m1 + at + row * p.ld + col);
+      if constexpr (kMore) {
+        const v4h x = __builtin_bit_cast(v4h, m1.half4(mi, nj));
+        const v4h y = __builtin_bit_cast(v4h, m2.half4(mi, nj));
+        const int64_t row = r0 + 16 * mi + r, col = q0 + 16 * nj + 4 * G;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = fmaf(p.f1, float(m[e]), v[e]);
-        if (two) {
-          const v4h k = *reinterpret_cast<const v4h*>(p.m2 + at + row * p.ld + col);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = fmaf(p.f2, float(k[e]), v[e]);
+        for (int e = 0; e < 4; ++e) {
+          v[e] = fmaf(p.f2, float(y[e]), fmaf(p.f1, float(x[e]), v[e]));
+          if (row == col + e && row < p.n) v[e] += p.diag;
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (row == col + e) v[e] += p.diag;
       }
       region.put(mi, nj, v2i{static_cast<int>(pack_half2(v[0], v[1])),
                              static_cast<int>(pack_half2(v[2], v[3]))});
@@ -357,37 +357,30 @@ __global__ __launch_bounds__(kThreads) void ns_gram_sum_kernel(const float* __re
 // columns turns that part's sign round: it grew nine times a step (1e-3 of u after five steps, 1e-2
 // after six). So each A meets its transpose before it is used; left after five steps: 3e-5.
 template <int kTiles>
-struct Rows {
-  v4f v[kTiles];
-};
-template <int kTiles>
 struct Halves {
   v4i hi[kTiles / 2], lo[kTiles / 2];
-};
-
-__device__ __forceinline__ void split_half2(float x, float y, float scale, uint32_t& hi,
-                                            uint32_t& lo) {
-  x *= scale;
-  y *= scale;
-  const _Float16 a = static_cast<_Float16>(x), b = static_cast<_Float16>(y);
-  hi = __builtin_bit_cast(uint32_t, half2_t{a, b});
-  lo = pack_half2(x - float(a), y - float(b));
-}
-
-template <int kTiles>
-__device__ __forceinline__ Halves<kTiles> halves(const Rows<kTiles>& x, float scale) {
-  Halves<kTiles> h;
-#pragma unroll
-  for (int j = 0; j < kTiles; ++j)
+  // the four values of tile j
+  __device__ __forceinline__ v4f get(int j) const {
+    v4f x;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      uint32_t hi, lo;
-      split_half2(x.v[j][2 * e], x.v[j][2 * e + 1], scale, hi, lo);
-      h.hi[j / 2][2 * (j & 1) + e] = static_cast<int>(hi);
-      h.lo[j / 2][2 * (j & 1) + e] = static_cast<int>(lo);
+      const half2_t h = __builtin_bit_cast(half2_t, static_cast<int>(hi[j / 2][2 * (j & 1) + e]));
+      const half2_t l = __builtin_bit_cast(half2_t, static_cast<int>(lo[j / 2][2 * (j & 1) + e]));
+      x[2 * e] = float(h[0]) + float(l[0]);
+      x[2 * e + 1] = float(h[1]) + float(l[1]);
     }
-  return h;
-}
+    return x;
+  }
+  __device__ __forceinline__ void set(int j, v4f x) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const _Float16 a = static_cast<_Float16>(x[2 * e]), c = static_cast<_Float16>(x[2 * e + 1]);
+      hi[j / 2][2 * (j & 1) + e] = static_cast<int>(__builtin_bit_cast(uint32_t, half2_t{a, c}));
+      lo[j / 2][2 * (j & 1) + e] =
+          static_cast<int>(pack_half2(x[2 * e] - float(a), x[2 * e + 1] - float(c)));
+    }
+  }
+};
 
 template <int kTiles>
 struct Core {
@@ -408,9 +401,9 @@ struct Core {
       *reinterpret_cast<lds_v4i*>(lo + at) = h.lo[kk];
     }
   }
-  // x <- (x + y') / 2, y the matrix times `scale` that lies in LDS: what a transposing read of 4 rows
-  // by 16 columns gives lane (G, r) is the column that is this lane's row.
-  __device__ __forceinline__ void symmetrise(Rows<kTiles>& x, float scale) const {
+  // x <- (x + y') / 2, y the matrix that lies in LDS: what a transposing read of 4 rows by 16 columns
+  // gives lane (G, r) is the column that is this lane's row.
+  __device__ __forceinline__ void symmetrise(Halves<kTiles>& x) const {
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) {
       const int at = (16 * j + 4 * G + (r >> 2)) * kPitch + 64 * (wave >> 1) + 16 * (r & 3) +
@@ -419,45 +412,53 @@ struct Core {
           v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(hi + at)));
       const v4h l = __builtin_bit_cast(
           v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lo + at)));
+      v4f v = x.get(j);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        x.v[j][e] = 0.5f * fmaf(float(h[e]) + float(l[e]), 1.0f / scale, x.v[j][e]);
+      for (int e = 0; e < 4; ++e) v[e] = 0.5f * (v[e] + (float(h[e]) + float(l[e])));
+      x.set(j, v);
     }
   }
-  // x += f left right, for one or two left operands
-  template <bool kTwo>
-  __device__ __forceinline__ void multiply(const Halves<kTiles>& l, Rows<kTiles>& x, float f,
-                                           const Halves<kTiles>& l2, Rows<kTiles>& x2,
-                                           float f2) const {
+  // left right, handed to `done` by tiles of columns
+  template <class Done>
+  __device__ __forceinline__ void multiply(const Halves<kTiles>& l, const Done& done) const {
+    both<false>(l, l, [&](int j, v4f x, v4f) { done(j, x); });
+  }
+  // the same of two left operands (kTwo) at once
+  template <bool kTwo, class Done>
+  __device__ __forceinline__ void both(const Halves<kTiles>& l, const Halves<kTiles>& l2,
+                                       const Done& done) const {
+    // two tiles of columns at a time: a matrix instruction that adds to the previous one's result waits
+    // for it
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) {
-      v4f acc = {0.0f, 0.0f, 0.0f, 0.0f}, acc2 = acc;
+    for (int j = 0; j < kTiles; j += 2) {
+      v4f acc[2] = {}, acc2[2] = {};
 #pragma unroll
       for (int kk = 0; kk < kTiles / 2; ++kk) {
-        const int at = (16 * j + r) * kPitch + 64 * kk + 16 * G;
-        const v4i rh = *reinterpret_cast<const lds_v4i*>(hi + at);
-        const v4i rl = *reinterpret_cast<const lds_v4i*>(lo + at);
-        acc = mfma<true>(rl, l.hi[kk], acc);
-        acc = mfma<true>(rh, l.lo[kk], acc);
-        acc = mfma<true>(rh, l.hi[kk], acc);
-        if constexpr (kTwo) {
-          acc2 = mfma<true>(rl, l2.hi[kk], acc2);
-          acc2 = mfma<true>(rh, l2.lo[kk], acc2);
-          acc2 = mfma<true>(rh, l2.hi[kk], acc2);
+        v4i rh[2], rl[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int at = (16 * (j + q) + r) * kPitch + 64 * kk + 16 * G;
+          rh[q] = *reinterpret_cast<const lds_v4i*>(hi + at);
+          rl[q] = *reinterpret_cast<const lds_v4i*>(lo + at);
         }
+#pragma unroll
+        for (int term = 0; term < 3; ++term)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const v4i right = term == 0 ? rl[q] : rh[q];
+            acc[q] = mfma<true>(right, term == 1 ? l.lo[kk] : l.hi[kk], acc[q]);
+            if constexpr (kTwo)
+              acc2[q] = mfma<true>(right, term == 1 ? l2.lo[kk] : l2.hi[kk], acc2[q]);
+          }
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x.v[j][e] = fmaf(f, acc[e], x.v[j][e]);
-      if constexpr (kTwo) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x2.v[j][e] = fmaf(f2, acc2[e], x2.v[j][e]);
-      }
+      for (int q = 0; q < 2; ++q) done(j + q, acc[q], acc2[q]);
     }
   }
 };
 
 // parts: the splits of kX^2 A ([item][split][128][128] fp32); q_hi, q_lo: kq Q in halves [n][ld],
-// zeros behind column n.
+// zeros behind column n. A and T are held times kA, B times kB, Q times kq.
 template <int kTiles>
 __global__ __launch_bounds__(64 * kTiles) void ns_core_kernel(const float* __restrict__ parts,
                                                               int splits, int n, int ld, int steps,
@@ -474,69 +475,64 @@ __global__ __launch_bounds__(64 * kTiles) void ns_core_kernel(const float* __res
   core.G = lane >> 4;
   core.r = lane & 15;
   const int row = 16 * core.wave + core.r;
-  Rows<kTiles> A, T, Q;
+  Halves<kTiles> A, B, T, Q;
   const float* p = parts + int64_t(blockIdx.x) * splits * (128 * 128) + row * 128 + 4 * core.G;
 #pragma unroll
   for (int j = 0; j < kTiles; ++j) {
-    A.v[j] = *reinterpret_cast<const v4f*>(p + 16 * j);
+    v4f v = *reinterpret_cast<const v4f*>(p + 16 * j);
     for (int s = 1; s < splits; ++s)
-      A.v[j] += *reinterpret_cast<const v4f*>(p + int64_t(s) * (128 * 128) + 16 * j);
-    A.v[j] *= 1.0f / kX / kX;
+      v += *reinterpret_cast<const v4f*>(p + int64_t(s) * (128 * 128) + 16 * j);
+    A.set(j, v * (kA / kX / kX));
   }
-  Halves<kTiles> none;
   for (int k = 0; k < steps; ++k) {
-    core.put(halves(A, kA));
+    core.put(A);
     __syncthreads();
-    core.symmetrise(A, kA);
-    const Halves<kTiles> ha = halves(A, kA);
-    Rows<kTiles> B;
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) B.v[j] = b * A.v[j];
-    core.template multiply<false>(ha, B, c / kA / kA, none, B, 0.0f);
+    core.symmetrise(A);
+    core.multiply(A, [&](int j, v4f x) {
+      B.set(j, x * (c * (kB / kA / kA)) + A.get(j) * (b * (kB / kA)));
+    });
     __syncthreads();  // every wave has read A
-    core.put(halves(B, kB));
+    core.put(B);
     __syncthreads();
     const bool last = k + 1 == steps;
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) T.v[j] = a * A.v[j];
+    Halves<kTiles> next;
     if (k == 0) {
 #pragma unroll
       for (int j = 0; j < kTiles; ++j) {
-        Q.v[j] = B.v[j];
+        v4f v = B.get(j) * (1.0f / kB);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (row == 16 * j + 4 * core.G + e && row < n) Q.v[j][e] += a;
+          if (row == 16 * j + 4 * core.G + e && row < n) v[e] += a;
+        Q.set(j, v * kq);
       }
-      if (!last) core.template multiply<false>(ha, T, 1.0f / kA / kB, none, T, 0.0f);
+      if (last) break;
+      core.multiply(A, [&](int j, v4f x) { T.set(j, x * (1.0f / kB) + A.get(j) * a); });
+    } else if (last) {
+      core.multiply(Q, [&](int j, v4f x) { next.set(j, x * (1.0f / kB) + Q.get(j) * a); });
+      Q = next;
+      break;
     } else {
-      const Halves<kTiles> hq = halves(Q, kq);
-#pragma unroll
-      for (int j = 0; j < kTiles; ++j) Q.v[j] *= a;
-      if (last)
-        core.template multiply<false>(hq, Q, 1.0f / kq / kB, none, Q, 0.0f);
-      else
-        core.template multiply<true>(hq, Q, 1.0f / kq / kB, ha, T, 1.0f / kA / kB);
+      core.template both<true>(Q, A, [&](int j, v4f x, v4f y) {
+        next.set(j, x * (1.0f / kB) + Q.get(j) * a);
+        T.set(j, y * (1.0f / kB) + A.get(j) * a);
+      });
+      Q = next;
     }
-    if (last) break;
-    const Halves<kTiles> ht = halves(T, kA);
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) A.v[j] = a * T.v[j];
-    core.template multiply<false>(ht, A, 1.0f / kA / kB, none, A, 0.0f);
+    core.multiply(T, [&](int j, v4f x) { A.set(j, x * (1.0f / kB) + T.get(j) * a); });
     __syncthreads();  // every wave has read B
   }
   if (row >= n) return;
   const int64_t at = int64_t(blockIdx.x) * stride + int64_t(row) * ld;
-  for (int j = 0; 16 * j < ld; ++j) {  // 16 kTiles columns and the zeros behind them
-    const int col = 16 * j + 4 * core.G;
-    uint32_t h0 = 0, h1 = 0, l0 = 0, l1 = 0;
+  for (int j = 0; 16 * j < ld; ++j) {  // 16 kTiles columns and the zeros behind them, up to ld
+    v2i h = {0, 0}, l = {0, 0};
 #pragma unroll
     for (int k = 0; k < kTiles; ++k)
       if (k == j) {
-        split_half2(Q.v[k][0], Q.v[k][1], kq, h0, l0);
-        split_half2(Q.v[k][2], Q.v[k][3], kq, h1, l1);
+        h = v2i{Q.hi[k / 2][2 * (k & 1)], Q.hi[k / 2][2 * (k & 1) + 1]};
+        l = v2i{Q.lo[k / 2][2 * (k & 1)], Q.lo[k / 2][2 * (k & 1) + 1]};
       }
-    *reinterpret_cast<v2i*>(q_hi + at + col) = v2i{static_cast<int>(h0), static_cast<int>(h1)};
-    *reinterpret_cast<v2i*>(q_lo + at + col) = v2i{static_cast<int>(l0), static_cast<int>(l1)};
+    *reinterpret_cast<v2i*>(q_hi + at + 16 * j + 4 * core.G) = h;
+    *reinterpret_cast<v2i*>(q_lo + at + 16 * j + 4 * core.G) = l;
   }
 }
 
@@ -588,29 +584,39 @@ __global__ __launch_bounds__(C::kThreads) void ns_apply_kernel(Batch A, Batch B,
   const int G = lane >> 4, r = lane & 15;
   const Region<C> region((lds_u8*)s0, (lds_u8*)s1, wave, lane);
   const int64_t r0 = i0 + wm * C::WM, q0 = j0 + wn * C::WN;
-  const _Float16* hi = p.hi + item * p.stride;
   _Float16* lo = p.lo + item * p.stride;
-  const bool add = p.add != 0.0f;
+  if (p.add != 0.0f) {
+    const Beside<2> hs(p.hi + item * p.stride, p.rows, p.ld, p.ld, r0, q0, lane);
+    const Beside<2> ls(lo, p.rows, p.ld, p.ld, r0, q0, lane);
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < C::NJ; ++nj) {
+        const v4h h = __builtin_bit_cast(v4h, hs.half4(mi, nj));
+        const v4h l = __builtin_bit_cast(v4h, ls.half4(mi, nj));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[mi][nj][e] = fmaf(p.add, fmaf(float(l[e]), 1.0f / kLo, float(h[e])),
+                                acc[mi][nj][e] * p.f);
+      }
+  } else {
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < C::NJ; ++nj) acc[mi][nj] *= p.f;
+  }
 #pragma unroll
   for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
     for (int nj = 0; nj < C::NJ; ++nj) {
-      const int64_t row = r0 + 16 * mi + r, col = q0 + 16 * nj + 4 * G;
-      const bool in = row < p.rows && col < p.ld;
-      v4f v = acc[mi][nj] * p.f;
-      if (add && in) {
-        const v4h h = *reinterpret_cast<const v4h*>(hi + row * p.ld + col);
-        const v4h l = *reinterpret_cast<const v4h*>(lo + row * p.ld + col);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[e] = fmaf(p.add, fmaf(float(l[e]), 1.0f / kLo, float(h[e])), v[e]);
-      }
+      const v4f v = acc[mi][nj];
       v2i w;
       if (p.last) {
         w = {static_cast<int>(pack_bf16x2(v[0], v[1])), static_cast<int>(pack_bf16x2(v[2], v[3]))};
       } else {
         w = {static_cast<int>(pack_half2(v[0], v[1])), static_cast<int>(pack_half2(v[2], v[3]))};
-        if (p.keep_lo && in) {
+        const int64_t row = r0 + 16 * mi + r, col = q0 + 16 * nj + 4 * G;
+        if (p.keep_lo && row < p.rows && col < p.ld) {
           const v4h h = __builtin_bit_cast(v4h, w);
           v4h l;
 #pragma unroll
@@ -716,11 +722,11 @@ inline Shape pick(int64_t tiles256, int64_t tiles128) {
   return tiles256 >= kFill / 2 ? kBig : tiles128 > kFill ? kSmall : kDeep;
 }
 
-template <class C>
+template <class C, bool kMore>
 void launch_symmetric(const Symmetric& a, const Symmetric* b, int64_t count, hipStream_t s) {
   const int64_t t = tiles_of(a.n, C::BM);
   const int tiles = static_cast<int>(t * (t + 1) / 2);
-  hipLaunchKernelGGL(ns_symmetric_kernel<C>, dim3(static_cast<uint32_t>(count * tiles), b ? 2 : 1),
+  hipLaunchKernelGGL((ns_symmetric_kernel<C, kMore>), dim3(static_cast<uint32_t>(count * tiles), b ? 2 : 1),
                      dim3(C::kThreads), 0, s, a, b ? *b : a, tiles);
 }
 
@@ -793,16 +799,16 @@ struct Run {
     return {square(l), square(r), out, m1, m2, p.s_stride, p.side, p.lds, f, f1, f2, diag};
   }
   void symmetric(const Symmetric& a, const Symmetric* b = nullptr) const {
-    launch<false>(a, b);
+    launch<false, true>(a, b);
   }
-  template <bool kTrans>
+  template <bool kTrans, bool kMore>
   void launch(const Symmetric& a, const Symmetric* b) const {
     if (shape_s == kBig)
-      launch_symmetric<BigTile<kTrans, kTrans>>(a, b, count, s);
+      launch_symmetric<BigTile<kTrans, kTrans>, kMore>(a, b, count, s);
     else if (shape_s == kSmall)
-      launch_symmetric<SmallTile<kTrans, kTrans>>(a, b, count, s);
+      launch_symmetric<SmallTile<kTrans, kTrans>, kMore>(a, b, count, s);
     else
-      launch_symmetric<DeepTile<kTrans, kTrans>>(a, b, count, s);
+      launch_symmetric<DeepTile<kTrans, kTrans>, kMore>(a, b, count, s);
   }
 
   template <bool kTrans>
@@ -826,7 +832,7 @@ struct Run {
     }
     const Symmetric a = {X, X, out, nullptr, nullptr, p.s_stride, p.side, p.lds, kA / kX / kX,
                          0.0f, 0.0f, 0.0f};
-    launch<kTrans>(a, nullptr);
+    launch<kTrans, false>(a, nullptr);
   }
 
   // X (half n) becomes f P X + add X

@@ -181,15 +181,14 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const uint16_t* __restri
                                                         int64_t vocab, uint16_t* __restrict__ dst,
                                                         int64_t ldd) {
   const int64_t groups = ldd / 8;
-  const bool whole = ld % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
   for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < rows * groups;
        n += int64_t(gridDim.x) * 256) {
     const int64_t row = n / groups, c = (n - row * groups) * 8;
     v4i v = {0, 0, 0, 0};
     if (targets == nullptr || has_target(targets[row], vocab)) {
       const uint16_t* p = src + row * ld + c;
-      if (whole && c + 8 <= cols) {
-        v = *reinterpret_cast<const v4i*>(p);
+      if (c + 8 <= cols) {
+        __builtin_memcpy(&v, p, 16);  // one load at any alignment
       } else {
         for (int k = 0; k < 8; ++k)
           if (c + k < cols) v[k / 2] |= static_cast<int>(uint32_t(p[k]) << (16 * (k & 1)));
@@ -315,26 +314,31 @@ __global__ __launch_bounds__(C::kThreads) void xent_product_kernel(Operand A, Op
   if (out.kind != kBf16) {
     float* f = out.f + split * out.split_stride;
     const bool whole = out.ldf % 4 == 0;
+    if (whole && (out.add || out.kind == kJoin)) {
+      const Beside<4> sum(f, out.rows, out.ldf, out.ldf, r0, q0, lane);
 #pragma unroll
-    for (int mi = 0; mi < C::MI; ++mi)
+      for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
-      for (int nj = 0; nj < C::NJ; ++nj) {
-        const int64_t row = r0 + 16 * mi + r, col = q0 + 16 * nj + 4 * G;
-        if (row >= out.rows || col >= out.cols) continue;
-        float* p = f + row * out.ldf + col;
-        if (whole) {  // the columns behind out.cols lie in the row's padding, or there are none
-          v4f* q = reinterpret_cast<v4f*>(p);
-          if (out.kind == kJoin)
-            acc[mi][nj] += *q;
-          else
-            *q = out.add ? *q + acc[mi][nj] : acc[mi][nj];
-        } else {
+        for (int nj = 0; nj < C::NJ; ++nj) acc[mi][nj] += sum.float4(mi, nj);
+    }
+    if (out.kind == kFp32) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col + e < out.cols) p[e] = out.add ? p[e] + acc[mi][nj][e] : acc[mi][nj][e];
+      for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+        for (int nj = 0; nj < C::NJ; ++nj) {
+          const int64_t row = r0 + 16 * mi + r, col = q0 + 16 * nj + 4 * G;
+          if (row >= out.rows || col >= out.cols) continue;
+          float* p = f + row * out.ldf + col;
+          if (whole) {  // columns behind out.cols lie in the row's padding, or there are none
+            *reinterpret_cast<v4f*>(p) = acc[mi][nj];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (col + e < out.cols) p[e] = out.add ? p[e] + acc[mi][nj][e] : acc[mi][nj][e];
+          }
         }
-      }
-    if (out.kind == kFp32) return;
+      return;
+    }
   }
   __syncthreads();
   const Region<C> region((lds_u8*)s0, (lds_u8*)s1, wave, lane);
