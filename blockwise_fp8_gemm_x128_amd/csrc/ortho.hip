@@ -366,18 +366,22 @@ struct Halves {
     for (int e = 0; e < 2; ++e) {
       const half2_t h = __builtin_bit_cast(half2_t, static_cast<int>(hi[j / 2][2 * (j & 1) + e]));
       const half2_t l = __builtin_bit_cast(half2_t, static_cast<int>(lo[j / 2][2 * (j & 1) + e]));
-      x[2 * e] = float(h[0]) + float(l[0]);
-      x[2 * e + 1] = float(h[1]) + float(l[1]);
+      // (as multiply-adds of 16-bit values: one instruction each)
+      x[2 * e] = fmaf(float(h[0]), 1.0f, float(l[0]));
+      x[2 * e + 1] = fmaf(float(h[1]), 1.0f, float(l[1]));
     }
     return x;
   }
+  // hi is x cut off, not rounded (two values an instruction): lo holds what it leaves
   __device__ __forceinline__ void set(int j, v4f x) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const _Float16 a = static_cast<_Float16>(x[2 * e]), c = static_cast<_Float16>(x[2 * e + 1]);
-      hi[j / 2][2 * (j & 1) + e] = static_cast<int>(__builtin_bit_cast(uint32_t, half2_t{a, c}));
-      lo[j / 2][2 * (j & 1) + e] =
-          static_cast<int>(pack_half2(x[2 * e] - float(a), x[2 * e + 1] - float(c)));
+      const auto h = __builtin_amdgcn_cvt_pkrtz(x[2 * e], x[2 * e + 1]);
+      const half2_t v = __builtin_bit_cast(half2_t, h);
+      const auto l = __builtin_amdgcn_cvt_pkrtz(fmaf(float(v[0]), -1.0f, x[2 * e]),
+                                                fmaf(float(v[1]), -1.0f, x[2 * e + 1]));
+      hi[j / 2][2 * (j & 1) + e] = __builtin_bit_cast(int, h);
+      lo[j / 2][2 * (j & 1) + e] = __builtin_bit_cast(int, l);
     }
   }
 };
@@ -386,8 +390,14 @@ template <int kTiles>
 struct Core {
   static constexpr int kSide = 16 * kTiles;
   static constexpr int kThreads = 64 * kTiles;
-  static constexpr int kPitch = 2 * kSide + 16;  // bytes of an LDS row: 16 rows start on 16 banks
+  static constexpr int kPitch = 2 * kSide;  // bytes of an LDS row, in units of 16
+  static constexpr int kUnits = kPitch / 16;
   static constexpr int kBytes = kSide * kPitch;
+  // A row's units are XOR-permuted by the row so that no 16 lanes of a read meet on a bank: a row covers
+  // kUnits of the 16 unit columns of LDS, so 16 / kUnits rows share a permutation.
+  static __device__ __forceinline__ int at(int row, int unit) {
+    return row * kPitch + 16 * (unit ^ ((row * kUnits / 16) & (kUnits - 1)));
+  }
 
   lds_u8 *hi, *lo;
   int wave, G, r;
@@ -396,9 +406,9 @@ struct Core {
   __device__ __forceinline__ void put(const Halves<kTiles>& h) const {
 #pragma unroll
     for (int kk = 0; kk < kTiles / 2; ++kk) {
-      const int at = (16 * wave + r) * kPitch + 64 * kk + 16 * G;
-      *reinterpret_cast<lds_v4i*>(hi + at) = h.hi[kk];
-      *reinterpret_cast<lds_v4i*>(lo + at) = h.lo[kk];
+      const int to = at(16 * wave + r, 4 * kk + G);
+      *reinterpret_cast<lds_v4i*>(hi + to) = h.hi[kk];
+      *reinterpret_cast<lds_v4i*>(lo + to) = h.lo[kk];
     }
   }
   // x <- (x + y') / 2, y the matrix that lies in LDS: what a transposing read of 4 rows by 16 columns
@@ -406,12 +416,12 @@ struct Core {
   __device__ __forceinline__ void symmetrise(Halves<kTiles>& x) const {
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) {
-      const int at = (16 * j + 4 * G + (r >> 2)) * kPitch + 64 * (wave >> 1) + 16 * (r & 3) +
-                     8 * (wave & 1);
+      const int from =
+          at(16 * j + 4 * G + (r >> 2), 4 * (wave >> 1) + (r & 3)) + 8 * (wave & 1);
       const v4h h = __builtin_bit_cast(
-          v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(hi + at)));
+          v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(hi + from)));
       const v4h l = __builtin_bit_cast(
-          v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lo + at)));
+          v4h, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lo + from)));
       v4f v = x.get(j);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = 0.5f * (v[e] + (float(h[e]) + float(l[e])));
@@ -437,9 +447,9 @@ struct Core {
         v4i rh[2], rl[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int at = (16 * (j + q) + r) * kPitch + 64 * kk + 16 * G;
-          rh[q] = *reinterpret_cast<const lds_v4i*>(hi + at);
-          rl[q] = *reinterpret_cast<const lds_v4i*>(lo + at);
+          const int from = at(16 * (j + q) + r, 4 * kk + G);
+          rh[q] = *reinterpret_cast<const lds_v4i*>(hi + from);
+          rl[q] = *reinterpret_cast<const lds_v4i*>(lo + from);
         }
 #pragma unroll
         for (int term = 0; term < 3; ++term)
