@@ -347,7 +347,9 @@ def _load_native():
                *(ctypes.cast(getattr(lib(), "puro_" + name), ctypes.c_void_p).value
                  for name in ("ckpt_pack", "ckpt_unpack", "ckpt_transpose", "block_norm_fwd",
                               "block_norm_workspace", "block_norm_bwd", "swiglu_fwd", "swiglu_bwd",
-                              "swiglu_bwd_fp8")))
+                              "swiglu_bwd_fp8", "linear_xent_fwd_workspace", "linear_xent_fwd",
+                              "linear_xent_bwd_workspace", "linear_xent_bwd",
+                              "newton_schulz_workspace", "newton_schulz")))
     _native = _args
     return _args
 
@@ -769,16 +771,21 @@ def puro_newton_schulz(gs, ms=None, us=None, ms_out=None, beta: float = 0.95,
     gs = list(gs)
     if not gs:
         return []
-    if len(gs) > NS_GROUP_MAX:
-        raise PuroError(f"at most {NS_GROUP_MAX} matrices per grouped call")
-    dev = _dev(gs[0])
-    rows, cols = shape = _matrix(gs[0], "g[0]")
     if ms is None and ms_out is not None:
         raise PuroError("ms_out needs ms")
     ms = None if ms is None else list(ms)
     ms_out = ms if ms_out is None else list(ms_out)
-    us = ([torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in gs] if us is None
-          else list(us))
+    if us is None:
+        us = [torch.empty(_matrix(g, "g"), dtype=torch.bfloat16, device=_dev(g)) for g in gs]
+    else:
+        us = list(us)
+    if _done((_native or _load_native()).newton_schulz(
+            gs, ms, ms_out, us, beta, nesterov, scale, steps, tuple(coefficients), workspace)):
+        return us
+    if len(gs) > NS_GROUP_MAX:
+        raise PuroError(f"at most {NS_GROUP_MAX} matrices per grouped call")
+    dev = _dev(gs[0])
+    rows, cols = shape = _matrix(gs[0], "g[0]")
     for name, ts in (("ms", ms), ("ms_out", ms_out), ("us", us)):
         if ts is not None and len(ts) != len(gs):
             raise PuroError(f"{name}: {len(ts)} matrices, expected {len(gs)}")
@@ -838,9 +845,15 @@ def puro_linear_xent_fwd(h, w, targets, loss=None, lse=None, workspace=None):
     """Softmax cross entropy of hidden states h, bf16 [tokens, d], against the output head's weights
     w, bf16 [vocab, d] (rows of both may be strided), without the matrix of all logits -> (loss, lse),
     fp32 [tokens]. targets: int64 [tokens]; a target outside [0, vocab) is none (loss and lse 0)."""
+    if loss is None or lse is None:
+        tokens = _matrix(h, "h")[0]
+        new = [torch.empty((tokens,), dtype=torch.float32, device=_dev(h)) for _ in range(2)]
+        loss, lse = new[0] if loss is None else loss, new[1] if lse is None else lse
+    if _done((_native or _load_native()).xent_fwd(h, w, targets, loss, lse, workspace)):
+        return loss, lse
     dev, tokens, d, vocab, ldh, ldw = _head(h, w, targets)
-    loss = _out(loss, "loss", torch.float32, (tokens,), dev)
-    lse = _out(lse, "lse", torch.float32, (tokens,), dev)
+    _need(loss, "loss", torch.float32, (tokens,), dev)
+    _need(lse, "lse", torch.float32, (tokens,), dev)
     desc = PuroLinearXent(tokens, d, vocab, ldh, ldw, h.data_ptr(), w.data_ptr(),
                           targets.data_ptr(), loss.data_ptr(), lse.data_ptr())
     _with_workspace("puro_linear_xent_fwd", desc, workspace, dev)
@@ -853,19 +866,32 @@ def puro_linear_xent_bwd(h, w, targets, lse, dloss, dlse=None, dh=None, dw=None,
     """The gradients (dh bf16 [tokens, d], dw bf16 or fp32 [vocab, d]) from those of loss (dloss) and
     lse (dlse, or None), fp32 [tokens]. dw has dw_dtype, or the type of the dw given; accumulate
     adds to an existing fp32 dw. want_dh, want_dw: False leaves that gradient out (None)."""
-    dev, tokens, d, vocab, ldh, ldw = _head(h, w, targets)
-    _need(lse, "lse", torch.float32, (tokens,), dev)
-    _need(dloss, "dloss", torch.float32, (tokens,), dev)
-    if dlse is not None:
-        _need(dlse, "dlse", torch.float32, (tokens,), dev)
     if accumulate and dw is None:
         raise PuroError("accumulate=True needs an existing dw")
     if isinstance(dw, torch.Tensor):
         dw_dtype = dw.dtype
     if dw_dtype not in _TYPES:
         raise PuroError(f"dw: dtype {dw_dtype}, expected bf16 or fp32")
-    dh = _out(dh, "dh", torch.bfloat16, (tokens, d), dev) if want_dh else None
-    dw = _out(dw, "dw", dw_dtype, (vocab, d), dev) if want_dw else None
+    if not want_dh:
+        dh = None
+    elif dh is None:
+        dh = torch.empty(_matrix(h, "h"), dtype=torch.bfloat16, device=_dev(h))
+    if not want_dw:
+        dw = None
+    elif dw is None:
+        dw = torch.empty(_matrix(w, "w"), dtype=dw_dtype, device=_dev(w))
+    if _done((_native or _load_native()).xent_bwd(h, w, targets, lse, dloss, dlse, dh, dw,
+                                                  accumulate, workspace)):
+        return dh, dw
+    dev, tokens, d, vocab, ldh, ldw = _head(h, w, targets)
+    _need(lse, "lse", torch.float32, (tokens,), dev)
+    _need(dloss, "dloss", torch.float32, (tokens,), dev)
+    if dlse is not None:
+        _need(dlse, "dlse", torch.float32, (tokens,), dev)
+    if dh is not None:
+        _need(dh, "dh", torch.bfloat16, (tokens, d), dev)
+    if dw is not None:
+        _need(dw, "dw", dw_dtype, (vocab, d), dev)
     desc = PuroLinearXentGrad(tokens, d, vocab, ldh, ldw, _TYPES[dw_dtype], int(bool(accumulate)),
                               h.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(),
                               dloss.data_ptr(), None if dlse is None else dlse.data_ptr(),

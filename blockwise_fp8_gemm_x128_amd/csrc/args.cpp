@@ -82,6 +82,12 @@ struct Entries {
   decltype(&puro_swiglu_fwd) swiglu_fwd;
   decltype(&puro_swiglu_bwd) swiglu_bwd;
   decltype(&puro_swiglu_bwd_fp8) swiglu_bwd_fp8;
+  decltype(&puro_linear_xent_fwd_workspace) xent_fwd_workspace;
+  decltype(&puro_linear_xent_fwd) xent_fwd;
+  decltype(&puro_linear_xent_bwd_workspace) xent_bwd_workspace;
+  decltype(&puro_linear_xent_bwd) xent_bwd;
+  decltype(&puro_newton_schulz_workspace) ns_workspace;
+  decltype(&puro_newton_schulz) ns;
 } entry = {};
 
 template <typename F>
@@ -93,12 +99,15 @@ bool take_address(PyObject* o, F* f) {
 
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Entries e = {};
-  if (n != 10 || !take_address(a[1], &e.pack) || !take_address(a[2], &e.unpack) ||
+  if (n != 16 || !take_address(a[1], &e.pack) || !take_address(a[2], &e.unpack) ||
       !take_address(a[3], &e.transpose) || !take_address(a[4], &e.norm_fwd) ||
       !take_address(a[5], &e.norm_workspace) || !take_address(a[6], &e.norm_bwd) ||
       !take_address(a[7], &e.swiglu_fwd) || !take_address(a[8], &e.swiglu_bwd) ||
-      !take_address(a[9], &e.swiglu_bwd_fp8)) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "bind(stream, nine addresses)");
+      !take_address(a[9], &e.swiglu_bwd_fp8) || !take_address(a[10], &e.xent_fwd_workspace) ||
+      !take_address(a[11], &e.xent_fwd) || !take_address(a[12], &e.xent_bwd_workspace) ||
+      !take_address(a[13], &e.xent_bwd) || !take_address(a[14], &e.ns_workspace) ||
+      !take_address(a[15], &e.ns)) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "bind(stream, fifteen addresses)");
     return nullptr;
   }
   e.stream = Py_NewRef(a[0]);
@@ -391,6 +400,107 @@ PyObject* swiglu_bwd_fp8(PyObject* const* a) {
   });
 }
 
+// The caller's scratch memory of at least `need` bytes, or (None) some of torch's, in the order of the
+// current stream.
+void* scratch(Call& c, PyObject* o, int64_t need, at::Tensor* own) {
+  if (!c.ok) return nullptr;
+  const at::Tensor* w = as_tensor(o);
+  if (o == Py_None) {
+    *own = at::empty({need}, c.lead->options().dtype(at::kByte));
+    w = own;
+  }
+  c.ok = w != nullptr && w->layout() == at::kStrided && w->is_contiguous() && w->is_cuda() &&
+         w->get_device() == c.device && w->numel() * static_cast<int64_t>(w->element_size()) >= need;
+  return c.ok ? const_cast<void*>(w->const_data_ptr()) : nullptr;
+}
+
+// A bf16 matrix of `cols` adjacent columns and any row stride from cols up.
+const void* bf16_rows(Call& c, const at::Tensor* t, int64_t cols, int64_t* rows, int64_t* ld) {
+  c.ok = c.ok && t != nullptr && t->layout() == at::kStrided && t->dim() == 2 &&
+         t->scalar_type() == at::kBFloat16 && t->size(1) == cols && t->is_cuda() &&
+         t->get_device() == c.device;
+  if (!c.ok) return nullptr;
+  *rows = t->size(0);
+  *ld = *rows <= 1 ? cols : t->stride(0);
+  c.ok = (cols <= 1 || t->stride(1) == 1) && *ld >= cols;
+  return c.ok ? t->const_data_ptr() : nullptr;
+}
+
+PyObject* xent_fwd(PyObject* const* a) {   // h, w, targets, loss, lse, workspace
+  Call c(a[0]);
+  puro_linear_xent d = {};
+  d.d = c.cols;
+  d.h = bf16_rows(c, c.lead, d.d, &d.tokens, &d.ldh);
+  d.w = c.ok ? bf16_rows(c, as_tensor(a[1]), d.d, &d.vocab, &d.ldw) : nullptr;
+  d.targets = c.get<int64_t>(a[2], at::kLong, d.tokens, -1);
+  d.loss = c.get<float>(a[3], at::kFloat, d.tokens, -1);
+  d.lse = c.get<float>(a[4], at::kFloat, d.tokens, -1);
+  at::Tensor own;
+  void* ws = c.ok ? scratch(c, a[5], entry.xent_fwd_workspace(&d), &own) : nullptr;
+  return finish(c, [&](void* st) { return entry.xent_fwd(&d, ws, st); });
+}
+
+PyObject* xent_bwd(PyObject* const* a) {
+  // h, w, targets, lse, dloss, dlse, dh, dw, accumulate, workspace
+  Call c(a[0]);
+  puro_linear_xent_grad d = {};
+  d.d = c.cols;
+  d.h = bf16_rows(c, c.lead, d.d, &d.tokens, &d.ldh);
+  d.w = c.ok ? bf16_rows(c, as_tensor(a[1]), d.d, &d.vocab, &d.ldw) : nullptr;
+  d.targets = c.get<int64_t>(a[2], at::kLong, d.tokens, -1);
+  d.lse = c.get<float>(a[3], at::kFloat, d.tokens, -1);
+  d.dloss = c.get<float>(a[4], at::kFloat, d.tokens, -1);
+  d.dlse = c.may<float>(a[5], at::kFloat, d.tokens, -1);
+  d.dh = c.may(a[6], at::kBFloat16, d.tokens, d.d);
+  const at::Tensor* dw = c.ok && a[7] != Py_None ? as_tensor(a[7]) : nullptr;
+  const bool f32 = dw != nullptr && dw->scalar_type() == at::kFloat;
+  d.dw_type = f32 ? PURO_TYPE_FP32 : PURO_TYPE_BF16;
+  d.dw = c.may(a[7], f32 ? at::kFloat : at::kBFloat16, d.vocab, d.d);
+  d.accumulate = c.flag(a[8]);
+  at::Tensor own;
+  void* ws = c.ok ? scratch(c, a[9], entry.xent_bwd_workspace(&d), &own) : nullptr;
+  return finish(c, [&](void* st) { return entry.xent_bwd(&d, ws, st); });
+}
+
+PyObject* newton_schulz(PyObject* const* a) {
+  // [g], [m] or None, [m_out] (None with m), [u], beta, nesterov, scale, steps, (coefficients),
+  // workspace
+  const bool momentum = a[1] != Py_None;
+  if (!PyList_Check(a[0]) || !PyList_Check(a[3]) || (momentum && !PyList_Check(a[1])) ||
+      (momentum && !PyList_Check(a[2])) || !PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 3 ||
+      !PyLong_Check(a[7]))
+    Py_RETURN_NONE;
+  const Py_ssize_t n = PyList_GET_SIZE(a[0]);
+  if (n < 1 || n > PURO_NS_GROUP_MAX || PyList_GET_SIZE(a[3]) != n ||
+      (momentum && (PyList_GET_SIZE(a[1]) != n || PyList_GET_SIZE(a[2]) != n)))
+    Py_RETURN_NONE;
+  Call c(PyList_GET_ITEM(a[0], 0));
+  puro_ns_item items[PURO_NS_GROUP_MAX] = {};
+  for (Py_ssize_t i = 0; i < n && c.ok; ++i) {
+    items[i].g = c.get<float>(PyList_GET_ITEM(a[0], i), at::kFloat, c.rows, c.cols);
+    if (momentum) {
+      items[i].m = c.get<float>(PyList_GET_ITEM(a[1], i), at::kFloat, c.rows, c.cols);
+      items[i].m_out = c.get<float>(PyList_GET_ITEM(a[2], i), at::kFloat, c.rows, c.cols);
+    }
+    items[i].u = c.get(PyList_GET_ITEM(a[3], i), at::kBFloat16, c.rows, c.cols);
+  }
+  puro_newton_schulz_params h = {};
+  h.beta = static_cast<float>(c.number(a[4]));
+  h.nesterov = c.flag(a[5]);
+  h.scale = static_cast<float>(c.number(a[6]));
+  const long steps = PyLong_AsLong(a[7]);
+  if (PyErr_Occurred()) PyErr_Clear();
+  c.ok = c.ok && steps >= 1 && steps <= PURO_NS_MAX_STEPS;
+  h.steps = static_cast<int>(steps);
+  for (int i = 0; i < 3; ++i)
+    h.coefficients[i] = static_cast<float>(c.number(PyTuple_GET_ITEM(a[8], i)));
+  at::Tensor own;
+  void* ws = c.ok ? scratch(c, a[9], entry.ns_workspace(n, c.rows, c.cols), &own) : nullptr;
+  return finish(c, [&](void* st) {
+    return entry.ns(items, static_cast<int>(n), c.rows, c.cols, &h, ws, st);
+  });
+}
+
 // As a method of kN arguments; torch's exceptions (a layout without strides or storage) and a
 // wrong number of arguments leave the question to the binding.
 template <PyObject* (*kCall)(PyObject* const*), Py_ssize_t kN>
@@ -418,6 +528,9 @@ PyMethodDef kMethods[] = {
     {"swiglu_fwd", as_method(method<swiglu_fwd, 3>), METH_FASTCALL, nullptr},
     {"swiglu_bwd", as_method(method<swiglu_bwd, 3>), METH_FASTCALL, nullptr},
     {"swiglu_bwd_fp8", as_method(method<swiglu_bwd_fp8, 4>), METH_FASTCALL, nullptr},
+    {"xent_fwd", as_method(method<xent_fwd, 6>), METH_FASTCALL, nullptr},
+    {"xent_bwd", as_method(method<xent_bwd, 10>), METH_FASTCALL, nullptr},
+    {"newton_schulz", as_method(method<newton_schulz, 10>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_args", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
