@@ -46,22 +46,24 @@ constexpr int kChunk = 64;             // reduction elements of a chunk
 constexpr int kRowBytes = 2 * kChunk;  // bytes of a staged row
 
 template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool kTransA_, bool kTransB_, bool kHalf_,
-          int kStages_ = 2>
+          int kStages_ = 2, int kGroups_ = 1>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_;
   static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
   static constexpr bool kTransA = kTransA_, kTransB = kTransB_;
   static constexpr bool kHalf = kHalf_;  // fp16 operands, else bf16
   static constexpr int kWaves = WAVES_M * WAVES_N;
-  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int kGroups = kGroups_;  // groups of kWaves waves that share the reduction
+  static constexpr int kThreads = 64 * kWaves * kGroups;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int MI = WM / 16, NJ = WN / 16;
   static constexpr int kBOff = BM * kRowBytes;
   static constexpr int kStageBytes = (BM + BN) * kRowBytes;
   static constexpr int kStages = kStages_;
   // the two LDS arrays of a block: a stage each, or the whole ring and nothing
-  static constexpr int kLds0 = kStages == 2 ? kStageBytes : kStages * kStageBytes;
-  static constexpr int kLds1 = kStages == 2 ? kStageBytes : 16;
+  static constexpr bool kRing = kStages > 2 || kGroups > 1;
+  static constexpr int kLds0 = kRing ? kGroups * kStages * kStageBytes : kStageBytes;
+  static constexpr int kLds1 = kRing ? 16 : kStageBytes;
   static_assert(WN == 64 && WM % 16 == 0 && BM % 64 == 0 && BN % 64 == 0, "tile shape");
 };
 
@@ -290,14 +292,19 @@ __device__ __forceinline__ void chunk_step(const lds_u8* stage, Fragments<C>& f,
 
 // multiply below with a ring of kStages stages: chunk c lies in stage c % kStages, and chunk
 // c + kStages - 1 is sent while c is multiplied. For tiles too few to share a CU: their loads come
-// from far (another XCD wrote them) and nothing else hides the way.
+// from far (another XCD wrote them) and nothing else hides the way. With two groups of waves each
+// has a ring and every second chunk (one block of four waves spends half of a chunk's time sending the
+// next), and the second hands its sums to the first, which alone has the result in acc.
 template <class C, bool kMore>
 __device__ __forceinline__ void multiply_ring(const Operand& A, const Operand& B, int64_t i0,
                                               int64_t j0, int64_t c0, int64_t c1, int64_t nk,
-                                              lds_u8* ring, v4f (&acc)[C::MI][C::NJ]) {
+                                              lds_u8* rings, v4f (&acc)[C::MI][C::NJ]) {
+  static_assert(C::kGroups == 1 || (C::kGroups == 2 && !kMore), "one or two groups");
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = all / C::kWaves, wave = all % C::kWaves;
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  lds_u8* ring = rings + group * C::kStages * C::kStageBytes;
   RingStager<C::kTransA, C::BM, C::kWaves> sa;
   RingStager<C::kTransB, C::BN, C::kWaves> sb;
   sa.init(A, i0, wave, lane);
@@ -313,21 +320,23 @@ __device__ __forceinline__ void multiply_ring(const Operand& A, const Operand& B
   }
   constexpr int kLoads = decltype(sa)::kLoads + decltype(sb)::kLoads;
   const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ring));
-  auto send = [&](int64_t c, int stage) {
+  auto send = [&](int64_t n, int stage) {  // the group's n-th chunk
+    const int64_t c = c0 + group + C::kGroups * n;
     const int64_t end = c < c1 ? nk : 0;
     sa.send(base + stage * C::kStageBytes, c, end);
     sb.send(base + stage * C::kStageBytes + C::kBOff, c, end);
   };
 #pragma unroll
-  for (int k = 0; k < C::kStages - 1; ++k) send(c0 + k, k);
+  for (int k = 0; k < C::kStages - 1; ++k) send(k, k);
   int stage = 0;
-  for (int64_t c = c0; c < c1; ++c) {
-    // chunk c has landed when at most the later chunks' loads are under way, here and, behind the
+  const int64_t count = (c1 - c0 + C::kGroups - 1) / C::kGroups;  // the same for both groups
+  for (int64_t n = 0; n < count; ++n) {
+    // the chunk has landed when at most the later chunks' loads are under way, here and, behind the
     // barrier, in every wave; and every wave has read the stage that is written next
     wait_loads<(C::kStages - 2) * kLoads>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    send(c + C::kStages - 1, stage == 0 ? C::kStages - 1 : stage - 1);
+    send(n + C::kStages - 1, stage == 0 ? C::kStages - 1 : stage - 1);
     const lds_u8* cur = ring + stage * C::kStageBytes;
     f.a[0][0] = f.fa.template read<0, 0>(cur);
     f.a[0][1] = f.fa.template read<0, 1>(cur);
@@ -341,17 +350,36 @@ __device__ __forceinline__ void multiply_ring(const Operand& A, const Operand& B
     stage = stage + 1 == C::kStages ? 0 : stage + 1;
   }
   wait_loads<0>();
+  if constexpr (C::kGroups == 2) {
+    static_assert(C::kWaves * C::MI * C::NJ * 64 * 16 <= C::kLds0, "the sums fit the rings");
+    __syncthreads();
+    // lane's sums 16 bytes at a time, neighbouring lanes adjacent
+    lds_v4f* sums = (lds_v4f*)rings + wave * C::MI * C::NJ * 64 + lane;
+    if (group == 1) {
+#pragma unroll
+      for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+        for (int nj = 0; nj < C::NJ; ++nj) sums[(mi * C::NJ + nj) * 64] = acc[mi][nj];
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+        for (int nj = 0; nj < C::NJ; ++nj) acc[mi][nj] += sums[(mi * C::NJ + nj) * 64];
+    }
+  }
 }
 
 // The products of one tile over chunks [c0, c1) of the reduction, which has `nk` chunks in all.
 // Each instruction takes the B fragment as its row operand, so lane (G, r) receives row r, columns
 // 4 G .. 4 G + 3 of every 16x16 tile. On return other waves may still read the stages. kMore adds to
-// what acc holds instead of starting from zero.
+// what acc holds instead of starting from zero. With kGroups = 2 the first group's waves have the result.
 template <class C, bool kMore = false>
 __device__ __forceinline__ void multiply(const Operand& A, const Operand& B, int64_t i0,
                                          int64_t j0, int64_t c0, int64_t c1, int64_t nk,
                                          lds_u8* s0, lds_u8* s1, v4f (&acc)[C::MI][C::NJ]) {
-  if constexpr (C::kStages > 2) {
+  if constexpr (C::kRing) {
     multiply_ring<C, kMore>(A, B, i0, j0, c0, c1, nk, s0, acc);
     return;
   }

@@ -217,6 +217,7 @@ __global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Symmetric a, 
   v4f acc[C::MI][C::NJ];
   multiply<C>(L, R, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
   __syncthreads();
+  if (C::kGroups > 1 && threadIdx.x >= 64 * C::kWaves) return;  // no barrier follows
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
@@ -588,6 +589,7 @@ __global__ __launch_bounds__(C::kThreads) void ns_apply_kernel(Batch A, Batch B,
   }
   multiply<C, kBoth>(a, b, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
   __syncthreads();
+  if (C::kGroups > 1 && threadIdx.x >= 64 * C::kWaves) return;  // no barrier follows
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
@@ -724,12 +726,17 @@ template <bool kTransA, bool kTransB>
 using SmallTile = Tile<128, 128, 2, 2, kTransA, kTransB, true>;
 template <bool kTransA, bool kTransB>
 using DeepTile = Tile<128, 128, 2, 2, kTransA, kTransB, true, 4>;
+template <bool kTransA, bool kTransB>
+using SplitTile = Tile<128, 128, 2, 2, kTransA, kTransB, true, 2, 2>;
 
-// Tile shape by the tiles of all matrices: 256x256 where they fill half of the chip, else 128x128, with
-// a ring of four stages where no CU gets a second block.
-enum Shape { kBig, kSmall, kDeep };
-inline Shape pick(int64_t tiles256, int64_t tiles128) {
-  return tiles256 >= kFill / 2 ? kBig : tiles128 > kFill ? kSmall : kDeep;
+// Tile shape by the tiles of all matrices: 256x256 where they fill half of the chip, else 128x128, where
+// no CU gets a second block with a ring of four stages, or two groups of waves from eight chunks on.
+enum Shape { kBig, kSmall, kDeep, kSplit };
+inline Shape pick(int64_t tiles256, int64_t tiles128, int64_t k) {
+  return tiles256 >= kFill / 2 ? kBig
+         : tiles128 > kFill    ? kSmall
+         : k < 8 * kChunk      ? kDeep
+                               : kSplit;
 }
 
 template <class C, bool kMore>
@@ -817,8 +824,10 @@ struct Run {
       launch_symmetric<BigTile<kTrans, kTrans>, kMore>(a, b, count, s);
     else if (shape_s == kSmall)
       launch_symmetric<SmallTile<kTrans, kTrans>, kMore>(a, b, count, s);
-    else
+    else if (shape_s == kDeep)
       launch_symmetric<DeepTile<kTrans, kTrans>, kMore>(a, b, count, s);
+    else
+      launch_symmetric<SplitTile<kTrans, kTrans>, kMore>(a, b, count, s);
   }
 
   template <bool kTrans>
@@ -877,10 +886,12 @@ struct Run {
   void launch_shape(const Batch& A, const Batch& B, const Apply& ap) const {
     if (!kBoth && shape_x == kBig)
       launch_apply<BigTile<false, kTransB>, false>(A, B, it, ap, count, s);
-    else if (shape_x == kDeep)
-      launch_apply<DeepTile<false, kTransB>, kBoth>(A, B, it, ap, count, s);
-    else
+    else if (!kBoth && shape_x == kSplit)
+      launch_apply<SplitTile<false, kTransB>, false>(A, B, it, ap, count, s);
+    else if (shape_x == kSmall)
       launch_apply<SmallTile<false, kTransB>, kBoth>(A, B, it, ap, count, s);
+    else
+      launch_apply<DeepTile<false, kTransB>, kBoth>(A, B, it, ap, count, s);
   }
 
   // All steps on A alone.
@@ -1003,9 +1014,9 @@ extern "C" puro_status puro_newton_schulz(const puro_ns_item* items, int count, 
   }
   const int64_t side_tiles = tiles_of(p.side, 256);
   const Run run = {p, it, *hp, count, rows, cols, s,
-                   pick(count * (side_tiles * (side_tiles + 1) / 2), count * p.tiles),
+                   pick(count * (side_tiles * (side_tiles + 1) / 2), count * p.tiles, p.side),
                    pick(count * tiles_of(rows, 256) * tiles_of(cols, 256),
-                        count * tiles_of(rows, 128) * tiles_of(cols, 128))};
+                        count * tiles_of(rows, 128) * tiles_of(cols, 128), p.side)};
   if (p.short_side) {
     // The largest power of two (up to 64) with which the product of all polynomials fits fp16. With a
     // growth above 1e5 (nine steps of the default coefficients) errors of A pass 2e-3 of u: step by step.
