@@ -13,12 +13,18 @@ checkpoints, the activation's gradient goes straight to the operands of the two 
 the weight gradients' transposed operands are made from the kept ones (n: puro_ckpt_transpose; h:
 from the checkpoint of gu).
 
+TokenModel puts a stack between an embedding and an output head of its own and trains on token targets:
+the loss comes from the head's weights directly (puro_linear_xent_fwd and _bwd), so the logits of the
+whole vocabulary are never there. With a momentum, Trainer steps along its orthogonalised direction
+(puro_newton_schulz, all matrices of a shape in one call).
+
 ``python -m blockwise_fp8_gemm_x128_amd.mlp_stack`` trains a small stack to imitate another one:
-matrices by the projected step, vectors by AdamW.
+matrices by the projected step, vectors by AdamW. With ``--vocab`` it trains a small token model on
+a fixed rule of which token follows which, matrices along their orthogonalised momentum.
 """
 from __future__ import annotations
 
-from typing import List, NamedTuple
+from typing import List, NamedTuple, Optional
 
 import torch
 
@@ -109,25 +115,93 @@ class MlpStack:
 
 
 class Trainer:
-    """Projected steps of the matrices along their gradients, scaled to the matrix's radius; AdamW
-    for the vectors."""
+    """Projected steps of the matrices along their gradients, scaled to the matrix's radius, or, with
+    a momentum (beta), along their orthogonalised momentum; AdamW for the vectors."""
 
-    def __init__(self, stack: MlpStack, lr: float):
-        self.stack, self.lr, self.step = stack, lr, 0
+    def __init__(self, stack: MlpStack, lr: float, beta: Optional[float] = None):
+        self.stack, self.lr, self.step, self.beta = stack, lr, 0, beta
         self.radii = [(puro.puro_frobenius_norm(p.wgu), puro.puro_frobenius_norm(p.wd))
                       for p in stack.layers]
         vectors = [stack.w_first, *(v for p in stack.layers for v in (p.w_post, p.gate, p.w_pre))]
         self.state = [(v, torch.zeros_like(v), torch.zeros_like(v)) for v in vectors]
+        if beta is not None:
+            self.momenta = [[torch.zeros_like(w) for w in ws] for ws in self._matrices()]
+
+    def _matrices(self):
+        """Masters by shape: every block's wgu, every block's wd."""
+        return [[p.wgu for p in self.stack.layers], [p.wd for p in self.stack.layers]]
 
     def update(self, dw_first, grads):
         self.step += 1
-        for p, radii, (dwgu, dwd, *_) in zip(self.stack.layers, self.radii, grads):
-            for w, w16, g, r in ((p.wgu, p.wgu16, dwgu, radii[0]), (p.wd, p.wd16, dwd, radii[1])):
-                g.mul_(r / puro.puro_frobenius_norm(g).clamp_min(1e-30))
-                puro.puro_hyperball_step(w, g, self.lr, r, w_bf16=w16)
+        if self.beta is not None:
+            self._orthogonal_steps(grads)
+        else:
+            for p, radii, (dwgu, dwd, *_) in zip(self.stack.layers, self.radii, grads):
+                for w, w16, g, r in ((p.wgu, p.wgu16, dwgu, radii[0]),
+                                     (p.wd, p.wd16, dwd, radii[1])):
+                    g.mul_(r / puro.puro_frobenius_norm(g).clamp_min(1e-30))
+                    puro.puro_hyperball_step(w, g, self.lr, r, w_bf16=w16)
         flat = [dw_first, *(v for g in grads for v in g[2:])]
         for (v, m, s), g in zip(self.state, flat):
             puro.puro_adamw_step(v, g, m, s, 0.1 * self.lr, 0.9, 0.95, 1e-8, 0.0, self.step)
+
+    def _orthogonal_steps(self, grads):
+        copies = [[p.wgu16 for p in self.stack.layers], [p.wd16 for p in self.stack.layers]]
+        for i, (ws, w16s, ms) in enumerate(zip(self._matrices(), copies, self.momenta)):
+            rows, cols = ws[0].shape
+            # a direction of about the radius of a matrix drawn with variance 1 / cols
+            scale = (rows / min(rows, cols)) ** 0.5
+            for at in range(0, len(ws), puro.NS_GROUP_MAX):
+                part = slice(at, at + puro.NS_GROUP_MAX)
+                us = puro.puro_newton_schulz([g[i] for g in grads[part]], ms[part], beta=self.beta,
+                                             scale=scale)
+                for w, w16, u, radii in zip(ws[part], w16s[part], us, self.radii[part]):
+                    puro.puro_hyperball_step_u16(w, u, self.lr, radii[i], w_bf16=w16)
+
+
+class TokenModel:
+    """An embedding, a stack of blocks and an output head of its own: `vocab` tokens (a multiple of 4),
+    masters in fp32 with bf16 copies."""
+
+    def __init__(self, vocab: int, layers: int, d: int, f: int, seed: int = 0, device="cuda:0"):
+        gen = torch.Generator(device=device)
+        gen.manual_seed(seed + 1000)
+        self.stack = MlpStack(layers, d, f, seed, device=device)
+        self.embedding = torch.randn((vocab, d), generator=gen, device=device)
+        self.head = torch.randn((vocab, d), generator=gen, device=device) * d ** -0.5
+        self.embedding16, self.head16 = self.embedding.bfloat16(), self.head.bfloat16()
+
+    def forward(self, tokens, targets):
+        """tokens, targets: int64 [tokens] (a target outside the vocabulary: none) -> (loss fp32
+        [tokens], kept)."""
+        n, kept = self.stack.forward(self.embedding16[tokens])
+        loss, lse = puro.puro_linear_xent_fwd(n, self.head16, targets)
+        return loss, (tokens, targets, n, lse, kept)
+
+    def backward(self, dloss, kept):
+        """dloss: the gradient of forward's loss, fp32 [tokens] -> (gradients of the embedding and the
+        head, fp32, and of the stack as MlpStack.backward gives them)."""
+        tokens, targets, n, lse, kept = kept
+        dn, dhead = puro.puro_linear_xent_bwd(n, self.head16, targets, lse, dloss,
+                                              dw_dtype=torch.float32)
+        dr, dw_first, grads = self.stack.backward(dn, kept)
+        dembedding = torch.zeros_like(self.embedding).index_add_(0, tokens, dr.float())
+        return dembedding, dhead, dw_first, grads
+
+
+class TokenTrainer(Trainer):
+    """Trainer for a token model: AdamW for its embedding and head."""
+
+    def __init__(self, model: TokenModel, lr: float, beta: Optional[float] = 0.95):
+        super().__init__(model.stack, lr, beta)
+        self.tables = [(w, w16, torch.zeros_like(w), torch.zeros_like(w)) for w, w16 in
+                       ((model.embedding, model.embedding16), (model.head, model.head16))]
+
+    def update_all(self, dembedding, dhead, dw_first, grads):
+        self.update(dw_first, grads)
+        for (w, w16, m, s), g in zip(self.tables, (dembedding, dhead)):
+            puro.puro_adamw_step(w, g, m, s, 0.1 * self.lr, 0.9, 0.95, 1e-8, 0.0, self.step,
+                                 p_bf16=w16)
 
 
 def train(layers=2, d=256, f=512, tokens=1024, steps=30, lr=0.05, seed=0, say=print):
@@ -150,6 +224,27 @@ def train(layers=2, d=256, f=512, tokens=1024, steps=30, lr=0.05, seed=0, say=pr
     return losses
 
 
+def train_tokens(vocab=4096, layers=2, d=256, f=512, tokens=1024, steps=30, lr=0.05, seed=0,
+                 say=print):
+    """Trains a token model to name the token that a fixed permutation puts after each; returns the
+    mean loss of every step."""
+    model = TokenModel(vocab, layers, d, f, seed)
+    trainer = TokenTrainer(model, lr)
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(seed)
+    follows = torch.randperm(vocab, generator=gen, device="cuda:0")
+    dloss = torch.full((tokens,), 1.0 / tokens, device="cuda:0")
+    losses = []
+    for step in range(steps):
+        x = torch.randint(0, vocab, (tokens,), generator=gen, device="cuda:0")
+        loss, kept = model.forward(x, follows[x])
+        losses.append(float(loss.mean()))
+        trainer.update_all(*model.backward(dloss, kept))
+        if say and (step % 5 == 0 or step == steps - 1):
+            say("step %3d  loss %.4f" % (step, losses[-1]))
+    return losses
+
+
 def main(argv=None):
     import argparse
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
@@ -159,7 +254,11 @@ def main(argv=None):
     ap.add_argument("--tokens", type=int, default=1024)
     ap.add_argument("--steps", type=int, default=30)
     ap.add_argument("--lr", type=float, default=0.05)
+    ap.add_argument("--vocab", type=int, default=0, help="train a token model over that many tokens")
     a = ap.parse_args(argv)
+    if a.vocab:
+        train_tokens(a.vocab, a.layers, a.d, a.f, a.tokens, a.steps, a.lr)
+        return
     train(a.layers, a.d, a.f, a.tokens, a.steps, a.lr)
 
 
