@@ -167,9 +167,9 @@ __device__ __forceinline__ v4u rsrc_words(const void* base, int64_t bytes) {
   r[3] = 0x00020000u;
   return r;
 }
+// (m0, the LDS address, may be read one wait state after it is written at the earliest)
 __device__ __forceinline__ void load_lds16(v4u r, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff),
-               "s"(r)
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(lds), "v"(voff), "s"(r)
                : "memory");
 }
 template <int n>
