@@ -178,12 +178,26 @@ struct Batch {
   }
 };
 
-// Row and column of tile t of the lower triangle (t = row (row + 1) / 2 + column).
-__device__ __forceinline__ void triangle_at(int t, int& i, int& j) {
-  i = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
-  while (i * (i + 1) / 2 > t) --i;
-  while ((i + 1) * (i + 2) / 2 <= t) ++i;
-  j = t - i * (i + 1) / 2;
+// Row and column of tile t of the lower triangle of `rows` rows of tiles, in bands of four rows, column by
+// column: tiles that run together share rows and columns of the operands.
+constexpr int kBand = 4;
+__device__ __forceinline__ void triangle_at(int t, int rows, int& i, int& j) {
+  int top = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);  // the row in row order
+  while (top * (top + 1) / 2 > t) --top;
+  while ((top + 1) * (top + 2) / 2 <= t) ++top;
+  const int first = top / kBand * kBand;  // whole rows come before this band either way
+  const int height = rows - first < kBand ? rows - first : kBand;
+  int u = t - first * (first + 1) / 2;
+  if (u < height * first) {  // columns left of the band's corner
+    j = u / height;
+    i = first + u - j * height;
+    return;
+  }
+  u -= height * first;
+  int d = 0;  // the corner's columns, each a tile shorter
+  while (u >= height - d) u -= height - d++;
+  j = first + d;
+  i = first + d + u;
 }
 
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
@@ -203,14 +217,14 @@ struct Symmetric {
 // kMore: there is an M1 (and, where not NULL, an M2).
 template <class C, bool kMore>
 __global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Symmetric a, Symmetric b,
-                                                                   int tiles) {
+                                                                   int tiles, int rows) {
   __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kLds0];
   __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kLds1];
   const Symmetric& p = blockIdx.y == 0 ? a : b;
   const int64_t id = regroup(blockIdx.x, gridDim.x);
   const int64_t item = uniform64(id / tiles);
   int ti, tj;
-  triangle_at(static_cast<int>(id - item * tiles), ti, tj);
+  triangle_at(static_cast<int>(id - item * tiles), rows, ti, tj);
   const int64_t i0 = uniform64(int64_t(ti) * C::BM), j0 = uniform64(int64_t(tj) * C::BN);
   const Operand L = p.l.at(item), R = p.r.at(item);
   const int64_t nk = ((C::kTransA ? L.rows : L.cols) + kChunk - 1) / kChunk;
@@ -271,7 +285,7 @@ __global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Symmetric a, 
 // kBoth: from both halves of X (three products).
 template <class C, bool kBoth>
 __global__ __launch_bounds__(C::kThreads) void ns_gram_part_kernel(Batch hi, Batch lo, int tiles,
-                                                                   int splits,
+                                                                   int rows, int splits,
                                                                    float* __restrict__ parts) {
   __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kLds0];
   __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kLds1];
@@ -279,7 +293,7 @@ __global__ __launch_bounds__(C::kThreads) void ns_gram_part_kernel(Batch hi, Bat
   const int rest = static_cast<int>(blockIdx.x - item * tiles * splits);
   const int split = rest / tiles;
   int ti, tj;
-  triangle_at(rest - split * tiles, ti, tj);
+  triangle_at(rest - split * tiles, rows, ti, tj);
   const int64_t i0 = int64_t(ti) * C::BM, j0 = int64_t(tj) * C::BN;
   const Operand X = hi.at(item);
   const int64_t nk = ((C::kTransA ? X.rows : X.cols) + kChunk - 1) / kChunk;
@@ -313,7 +327,8 @@ __global__ __launch_bounds__(C::kThreads) void ns_gram_part_kernel(Batch hi, Bat
 
 // The sum of the splits, as the fp16 matrix: one block per 32 x 32 patch of a 128 x 128 tile.
 __global__ __launch_bounds__(kThreads) void ns_gram_sum_kernel(const float* __restrict__ parts,
-                                                               int tiles, int splits, _Float16* out,
+                                                               int tiles, int rows, int splits,
+                                                               _Float16* out,
                                                                int64_t stride, int64_t n,
                                                                int64_t ld) {
   __shared__ float sh[32][33];
@@ -321,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void ns_gram_sum_kernel(const float* __re
   const int64_t tile = blockIdx.x >> 4;
   const int64_t item = tile / tiles;
   int ti, tj;
-  triangle_at(static_cast<int>(tile - item * tiles), ti, tj);
+  triangle_at(static_cast<int>(tile - item * tiles), rows, ti, tj);
   const int i = 32 * (patch >> 2), j = 32 * (patch & 3);
   const int row = threadIdx.x >> 3, col = 4 * (threadIdx.x & 7);
   const float* p = parts + (item * splits * tiles + (tile - item * tiles)) * (128 * 128) +
@@ -743,8 +758,9 @@ template <class C, bool kMore>
 void launch_symmetric(const Symmetric& a, const Symmetric* b, int64_t count, hipStream_t s) {
   const int64_t t = tiles_of(a.n, C::BM);
   const int tiles = static_cast<int>(t * (t + 1) / 2);
-  hipLaunchKernelGGL((ns_symmetric_kernel<C, kMore>), dim3(static_cast<uint32_t>(count * tiles), b ? 2 : 1),
-                     dim3(C::kThreads), 0, s, a, b ? *b : a, tiles);
+  hipLaunchKernelGGL((ns_symmetric_kernel<C, kMore>),
+                     dim3(static_cast<uint32_t>(count * tiles), b ? 2 : 1), dim3(C::kThreads), 0, s,
+                     a, b ? *b : a, tiles, static_cast<int>(t));
 }
 
 template <class C, bool kBoth>
@@ -837,16 +853,17 @@ struct Run {
       const dim3 grid(static_cast<uint32_t>(count * p.splits * p.tiles));
       const int tiles = static_cast<int>(p.tiles), splits = static_cast<int>(p.splits);
       using C = DeepTile<kTrans, kTrans>;
+      const int tile_rows = static_cast<int>((p.side + C::BM - 1) / C::BM);
       if (out == nullptr) {
         hipLaunchKernelGGL((ns_gram_part_kernel<C, true>), grid, dim3(C::kThreads), 0, s, X,
-                           whole(p.lo), tiles, splits, p.gram);
+                           whole(p.lo), tiles, tile_rows, splits, p.gram);
         return;
       }
       hipLaunchKernelGGL((ns_gram_part_kernel<C, false>), grid, dim3(C::kThreads), 0, s, X, X,
-                         tiles, splits, p.gram);
+                         tiles, tile_rows, splits, p.gram);
       hipLaunchKernelGGL(ns_gram_sum_kernel, dim3(static_cast<uint32_t>(count * p.tiles * 16)),
-                         dim3(kThreads), 0, s, p.gram, tiles, splits, out, p.s_stride, p.side,
-                         p.lds);
+                         dim3(kThreads), 0, s, p.gram, tiles, tile_rows, splits, out, p.s_stride,
+                         p.side, p.lds);
       return;
     }
     const Symmetric a = {X, X, out, nullptr, nullptr, p.s_stride, p.side, p.lds, kA / kX / kX,
