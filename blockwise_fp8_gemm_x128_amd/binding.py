@@ -254,9 +254,10 @@ def puro_hyperball_step_u16(w: torch.Tensor, u: torch.Tensor, lr: float, radius:
         workspace = optim_workspace(dev)
     else:
         _need_workspace(workspace, OPT_WORKSPACE_BYTES, dev)
-    check(lib().puro_hyperball_step_u16(w.data_ptr(), u.data_ptr(), w.numel(), float(lr),
-                                        radius.data_ptr(), w_bf16.data_ptr(),
-                                        workspace.data_ptr(), _stream(dev)))
+    with torch.cuda.device(dev):
+        check(lib().puro_hyperball_step_u16(w.data_ptr(), u.data_ptr(), w.numel(), float(lr),
+                                            radius.data_ptr(), w_bf16.data_ptr(),
+                                            workspace.data_ptr(), _stream(dev)))
     return w_bf16
 
 
@@ -805,8 +806,9 @@ def puro_newton_schulz(gs, ms=None, us=None, ms_out=None, beta: float = 0.95,
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _need_workspace(workspace, need, dev)
-    check(lib().puro_newton_schulz(items, len(gs), rows, cols, ctypes.byref(hp),
-                                   workspace.data_ptr() or None, _stream(dev)))
+    with torch.cuda.device(dev):
+        check(lib().puro_newton_schulz(items, len(gs), rows, cols, ctypes.byref(hp),
+                                       workspace.data_ptr() or None, _stream(dev)))
     return us
 
 
@@ -838,7 +840,8 @@ def _with_workspace(name, desc, workspace, dev) -> None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _need_workspace(workspace, need, dev)
-    check(getattr(lib(), name)(ctypes.byref(desc), workspace.data_ptr() or None, _stream(dev)))
+    with torch.cuda.device(dev):
+        check(getattr(lib(), name)(ctypes.byref(desc), workspace.data_ptr() or None, _stream(dev)))
 
 
 def puro_linear_xent_fwd(h, w, targets, loss=None, lse=None, workspace=None):

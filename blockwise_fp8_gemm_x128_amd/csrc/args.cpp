@@ -15,6 +15,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -195,6 +196,8 @@ struct Call {
 template <typename F>
 PyObject* finish(Call& c, F&& f) {
   if (!c.ok) Py_RETURN_NONE;
+  // the tensors' device may not be the current one, which launches (and the default stream) go by
+  const c10::DeviceGuard guard(c.lead->device());
   void* stream = c.stream();
   if (!c.ok) Py_RETURN_NONE;
   puro_status st;
