@@ -332,3 +332,14 @@ def test_refusals_of_the_binding(puro):
     for call in bad:
         with pytest.raises(puro.PuroError):
             call()
+
+
+# weights past 2^32 bytes, and a piece of P past them
+@pytest.mark.parametrize("size", [(3, 2048, 1100003), (540001, 64, 4100)], ids=str)
+def test_offsets_past_32_bits(puro, size):
+    h, w, y, dloss, dlse = draw(*size)
+    y[-1] = size[2] - 1
+    loss, lse = puro.puro_linear_xent_fwd(h, w, y)
+    check_fwd((loss, lse), h, w, y)
+    out = puro.puro_linear_xent_bwd(h, w, y, lse, dloss, dlse)
+    check_bwd(out, h, w, y, lse, dloss, dlse)
