@@ -32,6 +32,8 @@
 // short sides take them, need two halves of every operand.
 #include <math.h>
 
+#include <algorithm>
+
 #include "mma16.hpp"
 
 namespace puro {
@@ -814,6 +816,32 @@ puro_status check_sizes(int64_t count, int64_t rows, int64_t cols) {
   return PURO_OK;
 }
 
+// Whether an output lies over another matrix's data (the same momentum given twice, say): blocks would
+// write it while others read it.
+bool outputs_overlap(const puro_ns_item* items, int count, int64_t numel) {
+  struct Range {
+    uintptr_t begin, end;
+    int item;
+    bool written;
+  } r[4 * kMax];
+  int n = 0;
+  auto add = [&](const void* p, int64_t bytes, int item, bool written) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (p != nullptr) r[n++] = {at, at + static_cast<uintptr_t>(bytes), item, written};
+  };
+  for (int i = 0; i < count; ++i) {
+    add(items[i].g, 4 * numel, i, false);
+    add(items[i].m_out, 4 * numel, i, true);
+    if (items[i].m != items[i].m_out) add(items[i].m, 4 * numel, i, false);
+    add(items[i].u, 2 * numel, i, true);
+  }
+  std::sort(r, r + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  for (int i = 0; i < n; ++i)
+    for (int k = i + 1; k < n && r[k].begin < r[i].end; ++k)
+      if (r[i].item != r[k].item && (r[i].written || r[k].written)) return true;
+  return false;
+}
+
 // One call's launches.
 struct Run {
   const Plan& p;
@@ -1010,6 +1038,7 @@ extern "C" puro_status puro_newton_schulz(const puro_ns_item* items, int count, 
     it.mo[n] = i.m_out;
     it.u[n] = static_cast<uint16_t*>(i.u);
   }
+  if (outputs_overlap(items, count, rows * cols)) return PURO_ERR_ARG;
   PURO_TRY(check_ptr(workspace, false));
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const Plan p = plan(count, rows, cols, workspace);

@@ -419,8 +419,8 @@ puro_status puro_swiglu_bwd_fp8(const void* dh, const void* gu, const void* guq,
  * its matrix's u NaN.
  * Matrices are dense row-major fp32 [rows][cols], aligned to 4 bytes (16 is faster), u to 2; the
  * shorter side at most PURO_NS_MAX_SIDE, the longer at most PURO_NS_MAX_LONG, both of any size from 0
- * (nothing is written then). Either all matrices of a call have a momentum or none. No output may
- * overlap another matrix's data.
+ * (nothing is written then). Either all matrices of a call have a momentum or none. Gradients
+ * may be shared; an output that overlaps another matrix's data is refused (PURO_ERR_ARG).
  * `workspace`: puro_newton_schulz_workspace bytes (0 for sizes that are refused or empty). */
 #define PURO_NS_GROUP_MAX 64
 #define PURO_NS_MAX_STEPS 16

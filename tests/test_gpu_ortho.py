@@ -251,3 +251,18 @@ def test_refusals_of_the_binding(puro):
     w = torch.zeros((8, 8), device=DEV)
     with pytest.raises(puro.PuroError):
         puro.puro_hyperball_step_u16(w, w, 0.1, torch.ones(1, device=DEV))
+
+
+@pytest.mark.parametrize("size", [(1, 2 ** 20, 90), (1, 160, 2 ** 20)], ids=str)
+def test_longest_sides(puro, size):
+    g = draw(*size)[0]
+    check(puro.puro_newton_schulz([g[0]])[0], g[0])
+
+
+def test_offsets_past_32_bits(puro):
+    """A group of 2^31 elements and more, its last matrix another one than the rest."""
+    g = [draw(1, 2050, 16400, seed=k)[0][0] for k in range(2)]
+    us = puro.puro_newton_schulz([g[0]] * 63 + [g[1]])
+    check(us[0], g[0])
+    check(us[63], g[1])
+    assert all(torch.equal(u, us[0]) for u in us[1:63])

@@ -139,6 +139,22 @@ def test_ns_refusals(L):
     assert L.puro_newton_schulz(None, 1, 8, 8, None, FAKE, None) == NULL
 
 
+def test_ns_outputs_over_another_matrix(L):
+    """64 fp32 elements from each address; sharing is refused before the workspace is looked at."""
+    def at(*items):
+        return _ns(L, count=len(items), items=list(items), ws=None)
+    f4, f2 = 256, 128  # bytes of a matrix of 8 x 8
+    g, m, u = FAKE, FAKE + 4096, FAKE + 8192
+    assert at((g, m, m, u), (g, m + f4, m + f4, u + f2)) == NULL  # a shared gradient
+    assert at((g, m, m, u), (g, m, m, u + f2)) == ARG              # a momentum twice
+    assert at((g, m, m, u), (g, m, m + f4, u + f2)) == ARG         # read by one, written by the other
+    assert at((g, m, m, u), (g + f4, m + f4, m + f4, u)) == ARG    # a direction twice
+    assert at((g, m, m, u), (g, m + f4, m + f4, u + f2 - 2)) == ARG
+    assert at((g, m, m, u), (m, m + f4, m + f4, u + f2)) == ARG    # a gradient in a momentum
+    assert at((g, None, None, u), (g, None, None, u + f2)) == NULL
+    assert at((g, None, None, u), (u, None, None, u + f2)) == ARG
+
+
 def test_ns_empty(L):
     assert _ns(L, count=0, ws=None) == 0
     assert _ns(L, rows=0, ws=None) == 0 and _ns(L, cols=0, ws=None) == 0
