@@ -46,23 +46,22 @@ constexpr int kChunk = 64;             // reduction elements of a chunk
 constexpr int kRowBytes = 2 * kChunk;  // bytes of a staged row
 
 template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool kTransA_, bool kTransB_, bool kHalf_,
-          int kStages_ = 2, int kGroups_ = 1>
+          int kStages_ = 2>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_;
   static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
   static constexpr bool kTransA = kTransA_, kTransB = kTransB_;
   static constexpr bool kHalf = kHalf_;  // fp16 operands, else bf16
   static constexpr int kWaves = WAVES_M * WAVES_N;
-  static constexpr int kGroups = kGroups_;  // groups of kWaves waves that share the reduction
-  static constexpr int kThreads = 64 * kWaves * kGroups;
+  static constexpr int kThreads = 64 * kWaves;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int MI = WM / 16, NJ = WN / 16;
   static constexpr int kBOff = BM * kRowBytes;
   static constexpr int kStageBytes = (BM + BN) * kRowBytes;
   static constexpr int kStages = kStages_;
   // the two LDS arrays of a block: a stage each, or the whole ring and nothing
-  static constexpr bool kRing = kStages > 2 || kGroups > 1;
-  static constexpr int kLds0 = kRing ? kGroups * kStages * kStageBytes : kStageBytes;
+  static constexpr bool kRing = kStages > 2;
+  static constexpr int kLds0 = kRing ? kStages * kStageBytes : kStageBytes;
   static constexpr int kLds1 = kRing ? 16 : kStageBytes;
   static_assert(WN == 64 && WM % 16 == 0 && BM % 64 == 0 && BN % 64 == 0, "tile shape");
 };
@@ -186,29 +185,31 @@ struct RingStager : Stager<kTrans, BX, kIssuers> {
     if constexpr (!kTrans)
       words = rsrc_words(o.p + x0 * Base::ld2, (o.rows - x0 - 1) * Base::ld2 + 2 * o.cols);
   }
-  // chunk c of nk; from nk on zeros are written, so that every wave always has the same number of
-  // loads under way
-  __device__ __forceinline__ void send(uint32_t dst, int64_t c, int64_t nk) const {
-    v4u r = words;
-    uint32_t v;
+  // The chunk to send next, c of nk, and its stage; from nk on zeros are written, so that every wave
+  // always has the same number of loads under way.
+  v4u aimed;
+  uint32_t v, dst;
+  __device__ __forceinline__ void aim(uint32_t dst_, int64_t c, int64_t nk) {
+    dst = dst_;
     if constexpr (kTrans) {
-      r = rsrc_words(Base::p + c * kChunk * Base::ld2,
-                     c < nk ? (Base::rows - c * kChunk - 1) * Base::ld2 + Base::x_bytes : 0);
+      aimed = rsrc_words(Base::p + c * kChunk * Base::ld2,
+                         c < nk ? (Base::rows - c * kChunk - 1) * Base::ld2 + Base::x_bytes : 0);
       v = Base::voff;
     } else {
+      aimed = words;
       v = c < nk ? (c == nk - 1 ? Base::voff_tail : Base::voff) +
                        static_cast<uint32_t>(c * kRowBytes)
                  : kOutside;
       asm volatile("" : "+v"(v));
     }
-#pragma unroll
-    for (int n = 0; n < Base::kLoads; ++n) {
-      const int q = Base::w + kIssuers * n;
-      const uint32_t off =
-          kTrans ? static_cast<uint32_t>((q & 7) * 8 * Base::ld2) + (q >> 3) * kRowBytes
-                 : static_cast<uint32_t>(8 * q * Base::ld2);
-      load_lds16(r, v + off, dst + 8 * q * kRowBytes);
-    }
+  }
+  // load n of it
+  __device__ __forceinline__ void send(int n) const {
+    const int q = Base::w + kIssuers * n;
+    const uint32_t off =
+        kTrans ? static_cast<uint32_t>((q & 7) * 8 * Base::ld2) + (q >> 3) * kRowBytes
+               : static_cast<uint32_t>(8 * q * Base::ld2);
+    load_lds16(aimed, v + off, dst + 8 * q * kRowBytes);
   }
 };
 
@@ -220,9 +221,9 @@ struct Frag {
     const int G = lane >> 4, r = lane & 15;
     if constexpr (kTrans) {
       const int row = 16 * G + (r >> 2);
-      for (int b = 0; b < 4; ++b)
+      for (int b = 0; b < 4; ++b)  // 16 columns b of the slab from x on (x is 0 or 32 of its 64)
         o[b] = base + (x >> 6) * 64 * kRowBytes + row * kRowBytes + 8 * (r & 1) +
-               (((2 * b + ((r & 3) >> 1)) ^ swz_slab16(row)) << 4);
+               (((2 * ((b + (x >> 4)) & 3) + ((r & 3) >> 1)) ^ swz_slab16(row)) << 4);
     } else {
       for (int e = 0; e < 2; ++e)
         o[e] = base + (x + r) * kRowBytes + (((2 * G + e) ^ swz_rows(r)) << 4);
@@ -290,21 +291,56 @@ __device__ __forceinline__ void chunk_step(const lds_u8* stage, Fragments<C>& f,
   }
 }
 
-// multiply below with a ring of kStages stages: chunk c lies in stage c % kStages, and chunk
-// c + kStages - 1 is sent while c is multiplied. For tiles too few to share a CU: their loads come
-// from far (another XCD wrote them) and nothing else hides the way. With two groups of waves each
-// has a ring and every second chunk (one block of four waves spends half of a chunk's time sending the
-// next), and the second hands its sums to the first, which alone has the result in acc.
+// The fragments of a half chunk: one matrix instruction per 16x16 tile.
+template <class C>
+struct HalfChunk {
+  v4i a[C::MI], b[C::NJ];
+};
+
+// Step k of a half chunk's MI NJ: a fragment of the next half (e) is read from its stage, `send` may send
+// loads, and one instruction runs on this half's fragments.
+template <class C, int k, int e, class Send>
+__device__ __forceinline__ void half_step(const Fragments<C>& f, const lds_u8* stage,
+                                          HalfChunk<C>& next, const HalfChunk<C>& now,
+                                          v4f (&acc)[C::MI][C::NJ], const Send& send) {
+  if constexpr (k < C::MI * C::NJ) {
+    static_assert(C::MI + C::NJ <= C::MI * C::NJ, "a fragment a step");
+    // in the order of their use: the first row block, all columns, the other row blocks
+    if constexpr (k == 0)
+      next.a[0] = f.fa.template read<0, e>(stage);
+    else if constexpr (k <= C::NJ)
+      next.b[k - 1] = f.fb.template read<k - 1, e>(stage);
+    else if constexpr (k < C::MI + C::NJ)
+      next.a[k - C::NJ] = f.fa.template read<k - C::NJ, e>(stage);
+    send(k);
+    constexpr int mi = k / C::NJ, nj = k % C::NJ;
+    acc[mi][nj] = mfma<C::kHalf>(now.b[nj], now.a[mi], acc[mi][nj]);
+    __builtin_amdgcn_sched_barrier(0);
+    half_step<C, k + 1, e>(f, stage, next, now, acc, send);
+  }
+}
+
+// the first half of the first chunk
+template <class C, int k>
+__device__ __forceinline__ void read_half(const Fragments<C>& f, const lds_u8* stage,
+                                          HalfChunk<C>& h) {
+  if constexpr (k < C::MI) h.a[k] = f.fa.template read<k, 0>(stage);
+  if constexpr (k < C::NJ) h.b[k] = f.fb.template read<k, 0>(stage);
+  if constexpr (k + 1 < C::MI || k + 1 < C::NJ) read_half<C, k + 1>(f, stage, h);
+}
+
+// multiply below with a ring of kStages stages, chunk c in stage c % kStages, for tiles too few to share
+// a CU: their loads come from far (another XCD wrote them) and a SIMD has one wave, so nothing else
+// hides a wait. A half chunk's fragments are read while the half before it is multiplied, across
+// the barrier too; behind the barrier in a chunk's middle every wave has read the chunk and its
+// stage is sent the one kStages later, a load every few instructions.
 template <class C, bool kMore>
 __device__ __forceinline__ void multiply_ring(const Operand& A, const Operand& B, int64_t i0,
                                               int64_t j0, int64_t c0, int64_t c1, int64_t nk,
-                                              lds_u8* rings, v4f (&acc)[C::MI][C::NJ]) {
-  static_assert(C::kGroups == 1 || (C::kGroups == 2 && !kMore), "one or two groups");
+                                              lds_u8* ring, v4f (&acc)[C::MI][C::NJ]) {
   const int lane = threadIdx.x & 63;
-  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = all / C::kWaves, wave = all % C::kWaves;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  lds_u8* ring = rings + group * C::kStages * C::kStageBytes;
   RingStager<C::kTransA, C::BM, C::kWaves> sa;
   RingStager<C::kTransB, C::BN, C::kWaves> sb;
   sa.init(A, i0, wave, lane);
@@ -318,63 +354,56 @@ __device__ __forceinline__ void multiply_ring(const Operand& A, const Operand& B
 #pragma unroll
       for (int nj = 0; nj < C::NJ; ++nj) acc[mi][nj] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
+  constexpr int kSteps = C::MI * C::NJ;
   constexpr int kLoads = decltype(sa)::kLoads + decltype(sb)::kLoads;
   const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ring));
-  auto send = [&](int64_t n, int stage) {  // the group's n-th chunk
-    const int64_t c = c0 + group + C::kGroups * n;
+  auto aim = [&](int64_t c, int stage) {
     const int64_t end = c < c1 ? nk : 0;
-    sa.send(base + stage * C::kStageBytes, c, end);
-    sb.send(base + stage * C::kStageBytes + C::kBOff, c, end);
+    sa.aim(base + stage * C::kStageBytes, c, end);
+    sb.aim(base + stage * C::kStageBytes + C::kBOff, c, end);
+  };
+  auto send = [&](int n) {
+    if (n < decltype(sa)::kLoads)
+      sa.send(n);
+    else
+      sb.send(n - decltype(sa)::kLoads);
   };
 #pragma unroll
-  for (int k = 0; k < C::kStages - 1; ++k) send(k, k);
+  for (int k = 0; k < C::kStages; ++k) {
+    aim(c0 + k, k);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) send(n);
+  }
+  // The next chunk has landed when at most the later chunks' loads are under way, here and, behind the
+  // barrier, in every wave.
+  wait_loads<(C::kStages - 1) * kLoads>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  HalfChunk<C> first, second;
+  read_half<C, 0>(f, ring, first);
   int stage = 0;
-  const int64_t count = (c1 - c0 + C::kGroups - 1) / C::kGroups;  // the same for both groups
-  for (int64_t n = 0; n < count; ++n) {
-    // the chunk has landed when at most the later chunks' loads are under way, here and, behind the
-    // barrier, in every wave; and every wave has read the stage that is written next
+  for (int64_t c = c0; c < c1; ++c) {
+    half_step<C, 0, 1>(f, ring + stage * C::kStageBytes, second, first, acc, [](int) {});
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave has read the chunk
     wait_loads<(C::kStages - 2) * kLoads>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    send(n + C::kStages - 1, stage == 0 ? C::kStages - 1 : stage - 1);
-    const lds_u8* cur = ring + stage * C::kStageBytes;
-    f.a[0][0] = f.fa.template read<0, 0>(cur);
-    f.a[0][1] = f.fa.template read<0, 1>(cur);
-    __builtin_amdgcn_sched_barrier(0);
-    load_b<C, 0>(cur, f);
-    chunk_step<C, 0>(cur, f, acc, []() {});
-#pragma unroll
-    for (int mi = 0; mi < C::MI; ++mi)
-#pragma unroll
-      for (int nj = 0; nj < C::NJ; ++nj) asm volatile("" : "+v"(acc[mi][nj]));
+    aim(c + C::kStages, stage);
     stage = stage + 1 == C::kStages ? 0 : stage + 1;
+    half_step<C, 0, 0>(f, ring + stage * C::kStageBytes, first, second, acc, [&](int k) {
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n)
+        if (n * kSteps / kLoads == k) send(n);
+    });
   }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   wait_loads<0>();
-  if constexpr (C::kGroups == 2) {
-    static_assert(C::kWaves * C::MI * C::NJ * 64 * 16 <= C::kLds0, "the sums fit the rings");
-    __syncthreads();
-    // lane's sums 16 bytes at a time, neighbouring lanes adjacent
-    lds_v4f* sums = (lds_v4f*)rings + wave * C::MI * C::NJ * 64 + lane;
-    if (group == 1) {
-#pragma unroll
-      for (int mi = 0; mi < C::MI; ++mi)
-#pragma unroll
-        for (int nj = 0; nj < C::NJ; ++nj) sums[(mi * C::NJ + nj) * 64] = acc[mi][nj];
-    }
-    __syncthreads();
-    if (group == 0) {
-#pragma unroll
-      for (int mi = 0; mi < C::MI; ++mi)
-#pragma unroll
-        for (int nj = 0; nj < C::NJ; ++nj) acc[mi][nj] += sums[(mi * C::NJ + nj) * 64];
-    }
-  }
 }
 
 // The products of one tile over chunks [c0, c1) of the reduction, which has `nk` chunks in all.
 // Each instruction takes the B fragment as its row operand, so lane (G, r) receives row r, columns
 // 4 G .. 4 G + 3 of every 16x16 tile. On return other waves may still read the stages. kMore adds to
-// what acc holds instead of starting from zero. With kGroups = 2 the first group's waves have the result.
+// what acc holds instead of starting from zero.
 template <class C, bool kMore = false>
 __device__ __forceinline__ void multiply(const Operand& A, const Operand& B, int64_t i0,
                                          int64_t j0, int64_t c0, int64_t c1, int64_t nk,

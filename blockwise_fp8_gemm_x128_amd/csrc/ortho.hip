@@ -224,16 +224,17 @@ __global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Symmetric a, 
   __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kLds1];
   const Symmetric& p = blockIdx.y == 0 ? a : b;
   const int64_t id = regroup(blockIdx.x, gridDim.x);
-  const int64_t item = uniform64(id / tiles);
+  constexpr int kParts = C::BM / C::BN;  // blocks of BM x BM, by BN columns
+  const int64_t block = id / kParts, item = uniform64(block / tiles);
   int ti, tj;
-  triangle_at(static_cast<int>(id - item * tiles), rows, ti, tj);
-  const int64_t i0 = uniform64(int64_t(ti) * C::BM), j0 = uniform64(int64_t(tj) * C::BN);
+  triangle_at(static_cast<int>(block - item * tiles), rows, ti, tj);
+  const int64_t i0 = uniform64(int64_t(ti) * C::BM);
+  const int64_t j0 = uniform64(int64_t(tj) * C::BM + (id - block * kParts) * C::BN);
   const Operand L = p.l.at(item), R = p.r.at(item);
   const int64_t nk = ((C::kTransA ? L.rows : L.cols) + kChunk - 1) / kChunk;
   v4f acc[C::MI][C::NJ];
   multiply<C>(L, R, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
   __syncthreads();
-  if (C::kGroups > 1 && threadIdx.x >= 64 * C::kWaves) return;  // no barrier follows
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(C::kThreads) void ns_symmetric_kernel(Symmetric a, 
 }
 
 // ------------------------------------------------------------------ long reductions of few tiles
-// Split s of `splits` of A = X X' (kTransA: X' X): fp32 tiles [item][split][tile][BM][BN] of kX^2 A.
+// Split s of `splits` of A = X X' (kTransA: X' X): fp32 tiles [item][split][tile][BM][BM] of kX^2 A.
 // kBoth: from both halves of X (three products).
 template <class C, bool kBoth>
 __global__ __launch_bounds__(C::kThreads) void ns_gram_part_kernel(Batch hi, Batch lo, int tiles,
@@ -291,12 +292,14 @@ __global__ __launch_bounds__(C::kThreads) void ns_gram_part_kernel(Batch hi, Bat
                                                                    float* __restrict__ parts) {
   __shared__ __attribute__((aligned(1024))) uint8_t s0[C::kLds0];
   __shared__ __attribute__((aligned(1024))) uint8_t s1[C::kLds1];
-  const int64_t item = blockIdx.x / (tiles * splits);
-  const int rest = static_cast<int>(blockIdx.x - item * tiles * splits);
+  constexpr int kParts = C::BM / C::BN;  // tiles of BM x BM, by BN columns
+  const int block = blockIdx.x / kParts, part = blockIdx.x % kParts;
+  const int64_t item = block / (tiles * splits);
+  const int rest = static_cast<int>(block - item * tiles * splits);
   const int split = rest / tiles;
   int ti, tj;
   triangle_at(rest - split * tiles, rows, ti, tj);
-  const int64_t i0 = int64_t(ti) * C::BM, j0 = int64_t(tj) * C::BN;
+  const int64_t i0 = int64_t(ti) * C::BM, j0 = int64_t(tj) * C::BM + part * C::BN;
   const Operand X = hi.at(item);
   const int64_t nk = ((C::kTransA ? X.rows : X.cols) + kChunk - 1) / kChunk;
   const int64_t c0 = nk * split / splits, c1 = nk * (split + 1) / splits;
@@ -318,12 +321,12 @@ __global__ __launch_bounds__(C::kThreads) void ns_gram_part_kernel(Batch hi, Bat
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   const int G = lane >> 4, r = lane & 15;
-  float* out = parts + int64_t(blockIdx.x) * C::BM * C::BN;
+  float* out = parts + int64_t(block) * C::BM * C::BM + part * C::BN;
 #pragma unroll
   for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
     for (int nj = 0; nj < C::NJ; ++nj)
-      *reinterpret_cast<v4f*>(out + (wm * C::WM + 16 * mi + r) * C::BN + wn * C::WN + 16 * nj +
+      *reinterpret_cast<v4f*>(out + (wm * C::WM + 16 * mi + r) * C::BM + wn * C::WN + 16 * nj +
                               4 * G) = acc[mi][nj];
 }
 
@@ -606,7 +609,6 @@ __global__ __launch_bounds__(C::kThreads) void ns_apply_kernel(Batch A, Batch B,
   }
   multiply<C, kBoth>(a, b, i0, j0, 0, nk, nk, (lds_u8*)s0, (lds_u8*)s1, acc);
   __syncthreads();
-  if (C::kGroups > 1 && threadIdx.x >= 64 * C::kWaves) return;  // no barrier follows
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
@@ -742,18 +744,21 @@ using BigTile = Tile<256, 256, 2, 4, kTransA, kTransB, true>;
 template <bool kTransA, bool kTransB>
 using SmallTile = Tile<128, 128, 2, 2, kTransA, kTransB, true>;
 template <bool kTransA, bool kTransB>
-using DeepTile = Tile<128, 128, 2, 2, kTransA, kTransB, true, 4>;
+using DeepTile = Tile<128, 128, 4, 2, kTransA, kTransB, true, 4>;
 template <bool kTransA, bool kTransB>
-using SplitTile = Tile<128, 128, 2, 2, kTransA, kTransB, true, 2, 2>;
+using NarrowTile = Tile<128, 64, 4, 1, kTransA, kTransB, true, 4>;
 
-// Tile shape by the tiles of all matrices: 256x256 where they fill half of the chip, else 128x128, where
-// no CU gets a second block with a ring of four stages, or two groups of waves from eight chunks on.
-enum Shape { kBig, kSmall, kDeep, kSplit };
-inline Shape pick(int64_t tiles256, int64_t tiles128, int64_t k) {
-  return tiles256 >= kFill / 2 ? kBig
-         : tiles128 > kFill    ? kSmall
-         : k < 8 * kChunk      ? kDeep
-                               : kSplit;
+// Tile shape by the tiles of all matrices: 256x256 where they fill half of the chip, else 128x128, with a
+// ring of four stages where no CU gets a second block, and 128x64 where twice as many still have a
+// CU each. Measured, one symmetric product: side 2048 (136 tiles) 22.0 us with the ring, 25.4 as 272
+// of 128x64; side 1000 (36) 13.4 and 10.0, three of side 333 (18) 9.5 and 7.1. Two of side 2048 at once
+// (272 tiles) 38 us with two blocks a CU, 43 with the ring.
+enum Shape { kBig, kSmall, kDeep, kNarrow };
+inline Shape pick(int64_t tiles256, int64_t tiles128) {
+  return tiles256 >= kFill / 2   ? kBig
+         : tiles128 > kFill      ? kSmall
+         : 2 * tiles128 > kFill  ? kDeep
+                                 : kNarrow;
 }
 
 template <class C, bool kMore>
@@ -761,8 +766,8 @@ void launch_symmetric(const Symmetric& a, const Symmetric* b, int64_t count, hip
   const int64_t t = tiles_of(a.n, C::BM);
   const int tiles = static_cast<int>(t * (t + 1) / 2);
   hipLaunchKernelGGL((ns_symmetric_kernel<C, kMore>),
-                     dim3(static_cast<uint32_t>(count * tiles), b ? 2 : 1), dim3(C::kThreads), 0, s,
-                     a, b ? *b : a, tiles, static_cast<int>(t));
+                     dim3(static_cast<uint32_t>(count * tiles * (C::BM / C::BN)), b ? 2 : 1),
+                     dim3(C::kThreads), 0, s, a, b ? *b : a, tiles, static_cast<int>(t));
 }
 
 template <class C, bool kBoth>
@@ -849,7 +854,7 @@ struct Run {
   const puro_newton_schulz_params& h;
   int64_t count, rows, cols;
   hipStream_t s;
-  Shape shape_s, shape_x;
+  Shape shape_s, shape_two, shape_x;  // of one and two symmetric products, of X's
 
   Batch square(const _Float16* m) const { return {m, p.s_stride, p.side, p.lds, p.lds}; }
   Batch whole(const _Float16* x) const { return {x, p.x_stride, rows, p.ldx, p.ldx}; }
@@ -864,34 +869,45 @@ struct Run {
   }
   template <bool kTrans, bool kMore>
   void launch(const Symmetric& a, const Symmetric* b) const {
-    if (shape_s == kBig)
+    const Shape shape = b ? shape_two : shape_s;
+    if (shape == kBig)
       launch_symmetric<BigTile<kTrans, kTrans>, kMore>(a, b, count, s);
-    else if (shape_s == kSmall)
+    else if (shape == kSmall)
       launch_symmetric<SmallTile<kTrans, kTrans>, kMore>(a, b, count, s);
-    else if (shape_s == kDeep)
+    else if (shape == kDeep)
       launch_symmetric<DeepTile<kTrans, kTrans>, kMore>(a, b, count, s);
     else
-      launch_symmetric<SplitTile<kTrans, kTrans>, kMore>(a, b, count, s);
+      launch_symmetric<NarrowTile<kTrans, kTrans>, kMore>(a, b, count, s);
   }
 
+  template <bool kTrans, bool kBoth>
+  void gram_parts(const Batch& X, const Batch& lo) const {
+    if (2 * count * p.splits * p.tiles > kFill)
+      launch_gram_parts<DeepTile<kTrans, kTrans>, kBoth>(X, lo);
+    else
+      launch_gram_parts<NarrowTile<kTrans, kTrans>, kBoth>(X, lo);
+  }
+  template <class C, bool kBoth>
+  void launch_gram_parts(const Batch& X, const Batch& lo) const {
+    const int64_t blocks = count * p.splits * p.tiles * (C::BM / C::BN);
+    hipLaunchKernelGGL((ns_gram_part_kernel<C, kBoth>), dim3(static_cast<uint32_t>(blocks)),
+                       dim3(C::kThreads), 0, s, X, lo, static_cast<int>(p.tiles),
+                       static_cast<int>(tiles_of(p.side, C::BM)), static_cast<int>(p.splits),
+                       p.gram);
+  }
   template <bool kTrans>
   void gram(const _Float16* x, _Float16* out) const {
     const Batch X = whole(x);
     if (p.short_side || p.splits > 1) {
-      const dim3 grid(static_cast<uint32_t>(count * p.splits * p.tiles));
-      const int tiles = static_cast<int>(p.tiles), splits = static_cast<int>(p.splits);
-      using C = DeepTile<kTrans, kTrans>;
-      const int tile_rows = static_cast<int>((p.side + C::BM - 1) / C::BM);
       if (out == nullptr) {
-        hipLaunchKernelGGL((ns_gram_part_kernel<C, true>), grid, dim3(C::kThreads), 0, s, X,
-                           whole(p.lo), tiles, tile_rows, splits, p.gram);
+        gram_parts<kTrans, true>(X, whole(p.lo));
         return;
       }
-      hipLaunchKernelGGL((ns_gram_part_kernel<C, false>), grid, dim3(C::kThreads), 0, s, X, X,
-                         tiles, tile_rows, splits, p.gram);
+      gram_parts<kTrans, false>(X, X);
       hipLaunchKernelGGL(ns_gram_sum_kernel, dim3(static_cast<uint32_t>(count * p.tiles * 16)),
-                         dim3(kThreads), 0, s, p.gram, tiles, tile_rows, splits, out, p.s_stride,
-                         p.side, p.lds);
+                         dim3(kThreads), 0, s, p.gram, static_cast<int>(p.tiles),
+                         static_cast<int>(tiles_of(p.side, 128)), static_cast<int>(p.splits), out,
+                         p.s_stride, p.side, p.lds);
       return;
     }
     const Symmetric a = {X, X, out, nullptr, nullptr, p.s_stride, p.side, p.lds, kA / kX / kX,
@@ -931,12 +947,12 @@ struct Run {
   void launch_shape(const Batch& A, const Batch& B, const Apply& ap) const {
     if (!kBoth && shape_x == kBig)
       launch_apply<BigTile<false, kTransB>, false>(A, B, it, ap, count, s);
-    else if (!kBoth && shape_x == kSplit)
-      launch_apply<SplitTile<false, kTransB>, false>(A, B, it, ap, count, s);
     else if (shape_x == kSmall)
       launch_apply<SmallTile<false, kTransB>, kBoth>(A, B, it, ap, count, s);
-    else
+    else if (shape_x == kDeep)
       launch_apply<DeepTile<false, kTransB>, kBoth>(A, B, it, ap, count, s);
+    else
+      launch_apply<NarrowTile<false, kTransB>, kBoth>(A, B, it, ap, count, s);
   }
 
   // All steps on A alone.
@@ -1059,10 +1075,11 @@ extern "C" puro_status puro_newton_schulz(const puro_ns_item* items, int count, 
                        k, p.sums, p.parts, p.hi[0], p.lo, p.x_stride);
   }
   const int64_t side_tiles = tiles_of(p.side, 256);
+  const int64_t triangle = count * (side_tiles * (side_tiles + 1) / 2);
   const Run run = {p, it, *hp, count, rows, cols, s,
-                   pick(count * (side_tiles * (side_tiles + 1) / 2), count * p.tiles, p.side),
+                   pick(triangle, count * p.tiles), pick(2 * triangle, 2 * count * p.tiles),
                    pick(count * tiles_of(rows, 256) * tiles_of(cols, 256),
-                        count * tiles_of(rows, 128) * tiles_of(cols, 128), p.side)};
+                        count * tiles_of(rows, 128) * tiles_of(cols, 128))};
   if (p.short_side) {
     // The largest power of two (up to 64) with which the product of all polynomials fits fp16. With a
     // growth above 1e5 (nine steps of the default coefficients) errors of A pass 2e-3 of u: step by step.

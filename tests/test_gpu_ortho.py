@@ -266,3 +266,15 @@ def test_offsets_past_32_bits(puro):
     check(us[0], g[0])
     check(us[63], g[1])
     assert all(torch.equal(u, us[0]) for u in us[1:63])
+
+
+# tiles of 128x128 between half of the chip's compute units and all of them, for one symmetric product, for
+# two in a launch, and for the products with X; wide and tall
+@pytest.mark.parametrize("size", [(9, 520, 520), (14, 520, 600), (14, 600, 520), (5, 520, 800),
+                                  (5, 800, 520)], ids=str)
+def test_a_tile_for_most_compute_units(puro, size):
+    g, m = draw(*size)
+    ms = [x.clone() for x in m.unbind(0)]
+    us = puro.puro_newton_schulz(g.unbind(0), ms)
+    for k in range(size[0]):
+        check(us[k], check_momentum(ms[k], g[k], m[k], 0.95, True))
