@@ -958,7 +958,7 @@ struct Run {
   void launch_shape(const Batch& A, const Batch& B, const Apply& ap) const {
     if (!kBoth && shape_x == kBig)
       launch_apply<BigTile<false, kTransB>, false>(A, B, it, ap, count, s);
-    else if (shape_x == kSmall)
+    else if (shape_x == kSmall || shape_x == kBig)  // (kBig: in two halves, a short reduction)
       launch_apply<SmallTile<false, kTransB>, kBoth>(A, B, it, ap, count, s);
     else if (shape_x == kDeep)
       launch_apply<DeepTile<false, kTransB>, kBoth>(A, B, it, ap, count, s);
