@@ -774,6 +774,9 @@ def puro_newton_schulz(gs, ms=None, us=None, ms_out=None, beta: float = 0.95,
         return []
     if ms is None and ms_out is not None:
         raise PuroError("ms_out needs ms")
+    coefficients = tuple(coefficients)
+    if len(coefficients) != 3:
+        raise PuroError(f"coefficients: {len(coefficients)}, expected 3")
     ms = None if ms is None else list(ms)
     ms_out = ms if ms_out is None else list(ms_out)
     if us is None:
@@ -781,7 +784,7 @@ def puro_newton_schulz(gs, ms=None, us=None, ms_out=None, beta: float = 0.95,
     else:
         us = list(us)
     if _done((_native or _load_native()).newton_schulz(
-            gs, ms, ms_out, us, beta, nesterov, scale, steps, tuple(coefficients), workspace)):
+            gs, ms, ms_out, us, beta, nesterov, scale, steps, coefficients, workspace)):
         return us
     if len(gs) > NS_GROUP_MAX:
         raise PuroError(f"at most {NS_GROUP_MAX} matrices per grouped call")

@@ -421,7 +421,8 @@ puro_status puro_swiglu_bwd_fp8(const void* dh, const void* gu, const void* guq,
  * shorter side at most PURO_NS_MAX_SIDE, the longer at most PURO_NS_MAX_LONG, both of any size from 0
  * (nothing is written then). Either all matrices of a call have a momentum or none. Gradients
  * may be shared; an output that overlaps another matrix's data is refused (PURO_ERR_ARG).
- * `workspace`: puro_newton_schulz_workspace bytes (0 for sizes that are refused or empty). */
+ * `workspace`: puro_newton_schulz_workspace bytes (0 for sizes that are refused or empty). Calls, or
+ * captured graphs, that may overlap in time need one each. */
 #define PURO_NS_GROUP_MAX 64
 #define PURO_NS_MAX_STEPS 16
 #define PURO_NS_MAX_SIDE 16384
@@ -459,7 +460,8 @@ puro_status puro_newton_schulz(const puro_ns_item* items, int count, int64_t row
  * tokens from 0 to PURO_XENT_MAX_TOKENS, d from 1 to PURO_XENT_MAX_D, vocab from 1 to 2^24.
  * Sums run in an order fixed by the sizes and alignment alone, so results repeat exactly.
  * `workspace`: 16-byte aligned device memory of the bytes that the call's _workspace function
- * returns for the same structure (0 for one that is refused). */
+ * returns for the same structure (0 for one that is refused). Calls, or captured graphs, that may
+ * overlap in time need one each. */
 #define PURO_XENT_MAX_TOKENS (1 << 20)
 #define PURO_XENT_MAX_D 65536
 typedef struct {

@@ -188,6 +188,14 @@ def test_binding_refuses_host_tensors():
 
 
 # ------------------------------------------------------------------ the 64-bit forms themselves
+def test_binding_takes_three_coefficients():
+    from blockwise_fp8_gemm_x128_amd import PuroError, binding
+    us = [torch.zeros((4, 8), dtype=torch.bfloat16)]
+    for k in ((), (1.0, 2.0), (1.0, 2.0, 3.0, 4.0)):
+        with pytest.raises(PuroError, match="coefficients"):
+            binding.puro_newton_schulz([torch.zeros((4, 8))], us=us, coefficients=k)
+
+
 def test_xent_gradients_against_differences():
     gen = torch.Generator().manual_seed(3)
     t, d, v = 5, 6, 9
