@@ -73,10 +73,15 @@ __device__ __forceinline__ double block_sum(double x, double* sh) {
   return (sh[0] + sh[1]) + (sh[2] + sh[3]);
 }
 
+// Four elements from any element's address: one load or store, whose addresses need 4 bytes' alignment.
+__device__ __forceinline__ v4f load4(const float* p) {
+  v4f v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+
 // Momentum, and the sum of squares of v by blocks (in fp64, in a fixed order). Bound by memory: 28
-// matrices of 2048 x 2048 250 us, 5.6 TB/s, and the conversion below the same. kVec: four elements
-// at a time (all addresses of the group are 16-byte aligned and numel a multiple of 4).
-template <bool kVec>
+// matrices of 2048 x 2048 250 us, 5.6 TB/s, and the conversion below the same.
 __global__ __launch_bounds__(kThreads) void ns_momentum_kernel(Items it, int64_t numel, Momentum k,
                                                                double* __restrict__ parts) {
   __shared__ double sh[kThreads / 64];
@@ -85,34 +90,32 @@ __global__ __launch_bounds__(kThreads) void ns_momentum_kernel(Items it, int64_t
   const float* m = it.m[n];
   float* mo = it.mo[n];
   double acc = 0.0;
-  const int64_t step = int64_t(gridDim.x) * kThreads;
-  if constexpr (kVec) {
-    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < numel / 4; i += step) {
-      const v4f gg = reinterpret_cast<const v4f*>(g)[i];
-      v4f v = gg;
-      if (k.on) {
-        v4f mm = reinterpret_cast<const v4f*>(m)[i];
+  const int64_t first = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  for (int64_t i = first; i < numel / 4; i += int64_t(gridDim.x) * kThreads) {
+    const v4f gg = load4(g + 4 * i);
+    v4f v = gg;
+    if (k.on) {
+      v4f mm = load4(m + 4 * i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          mm[e] = fmaf(k.beta, mm[e], k.rest * gg[e]);
-          v[e] = direction(gg[e], mm[e], k);
-        }
-        reinterpret_cast<v4f*>(mo)[i] = mm;
+      for (int e = 0; e < 4; ++e) {
+        mm[e] = fmaf(k.beta, mm[e], k.rest * gg[e]);
+        v[e] = direction(gg[e], mm[e], k);
       }
+      __builtin_memcpy(mo + 4 * i, &mm, 16);
+    }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc += double(v[e]) * v[e];
+    for (int e = 0; e < 4; ++e) acc += double(v[e]) * v[e];
+  }
+  if (first < numel % 4) {  // what is left
+    const int64_t i = numel / 4 * 4 + first;
+    const float gg = g[i];
+    float v = gg;
+    if (k.on) {
+      const float mm = fmaf(k.beta, m[i], k.rest * gg);
+      v = direction(gg, mm, k);
+      mo[i] = mm;
     }
-  } else {
-    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < numel; i += step) {
-      const float gg = g[i];
-      float v = gg;
-      if (k.on) {
-        const float mm = fmaf(k.beta, m[i], k.rest * gg);
-        v = direction(gg, mm, k);
-        mo[i] = mm;
-      }
-      acc += double(v) * v;
-    }
+    acc += double(v) * v;
   }
   const double s = block_sum(acc, sh);
   if (threadIdx.x == 0) parts[int64_t(n) * gridDim.x + blockIdx.x] = s;
@@ -120,7 +123,6 @@ __global__ __launch_bounds__(kThreads) void ns_momentum_kernel(Items it, int64_t
 
 // X = v / |v| (zero where |v| is), times kX, in halves: hi [rows][ldx], zeros behind the columns, and
 // lo, what hi leaves, times kLo.
-template <bool kVec>
 __global__ __launch_bounds__(kThreads) void ns_convert_kernel(Items it, int64_t rows, int64_t cols,
                                                               int64_t ldx, Momentum k,
                                                               const double* __restrict__ parts,
@@ -145,14 +147,12 @@ __global__ __launch_bounds__(kThreads) void ns_convert_kernel(Items it, int64_t 
     const int64_t row = i / groups, c = (i - row * groups) * 4;
     const int64_t at = row * cols + c;
     v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (kVec) {
-      if (c < cols) {
-        v = *reinterpret_cast<const v4f*>(g + at);
-        if (k.on) {
-          const v4f mm = *reinterpret_cast<const v4f*>(m + at);
+    if (c + 4 <= cols) {
+      v = load4(g + at);
+      if (k.on) {
+        const v4f mm = load4(m + at);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = direction(v[e], mm[e], k);
-        }
+        for (int e = 0; e < 4; ++e) v[e] = direction(v[e], mm[e], k);
       }
     } else {
 #pragma unroll
@@ -1049,7 +1049,6 @@ extern "C" puro_status puro_newton_schulz(const puro_ns_item* items, int count, 
   if (count == 0 || rows == 0 || cols == 0) return PURO_OK;
   if (items == nullptr) return PURO_ERR_NULL;
   Items it = {};
-  bool vec = cols % 4 == 0;
   const bool momentum = items[0].m != nullptr;
   for (int n = 0; n < count; ++n) {
     const puro_ns_item& i = items[n];
@@ -1059,7 +1058,6 @@ extern "C" puro_status puro_newton_schulz(const puro_ns_item* items, int count, 
     const uintptr_t f = reinterpret_cast<uintptr_t>(i.g) | reinterpret_cast<uintptr_t>(i.m) |
                         reinterpret_cast<uintptr_t>(i.m_out);
     if (f % 4 || reinterpret_cast<uintptr_t>(i.u) % 2) return PURO_ERR_ALIGN;
-    vec = vec && f % 16 == 0;
     it.g[n] = i.g;
     it.m[n] = i.m;
     it.mo[n] = i.m_out;
@@ -1074,17 +1072,9 @@ extern "C" puro_status puro_newton_schulz(const puro_ns_item* items, int count, 
   int64_t blocks = tiles_of(rows * (p.ldx / 4), kThreads * 4);
   if (blocks > 2048) blocks = 2048;
   const dim3 conv(static_cast<uint32_t>(blocks), count);
-  if (vec) {
-    hipLaunchKernelGGL(ns_momentum_kernel<true>, sums, dim3(kThreads), 0, s, it, rows * cols, k,
-                       p.sums);
-    hipLaunchKernelGGL(ns_convert_kernel<true>, conv, dim3(kThreads), 0, s, it, rows, cols, p.ldx,
-                       k, p.sums, p.parts, p.hi[0], p.lo, p.x_stride);
-  } else {
-    hipLaunchKernelGGL(ns_momentum_kernel<false>, sums, dim3(kThreads), 0, s, it, rows * cols, k,
-                       p.sums);
-    hipLaunchKernelGGL(ns_convert_kernel<false>, conv, dim3(kThreads), 0, s, it, rows, cols, p.ldx,
-                       k, p.sums, p.parts, p.hi[0], p.lo, p.x_stride);
-  }
+  hipLaunchKernelGGL(ns_momentum_kernel, sums, dim3(kThreads), 0, s, it, rows * cols, k, p.sums);
+  hipLaunchKernelGGL(ns_convert_kernel, conv, dim3(kThreads), 0, s, it, rows, cols, p.ldx, k, p.sums,
+                     p.parts, p.hi[0], p.lo, p.x_stride);
   const int64_t side_tiles = tiles_of(p.side, 256);
   const int64_t triangle = count * (side_tiles * (side_tiles + 1) / 2);
   const Run run = {p, it, *hp, count, rows, cols, s,

@@ -417,7 +417,7 @@ puro_status puro_swiglu_bwd_fp8(const void* dh, const void* gu, const void* guq,
  * singular values in [0, 1] X has to stay within 1.75 until the last step and 12 after it, and
  * |c[0]| + |c[1]| x^2 + |c[2]| x^4 within 28 for the largest such x. An infinite or NaN element makes
  * its matrix's u NaN.
- * Matrices are dense row-major fp32 [rows][cols], aligned to 4 bytes (16 is faster), u to 2; the
+ * Matrices are dense row-major fp32 [rows][cols], aligned to 4 bytes, u to 2 (16 is faster); the
  * shorter side at most PURO_NS_MAX_SIDE, the longer at most PURO_NS_MAX_LONG, both of any size from 0
  * (nothing is written then). Either all matrices of a call have a momentum or none. Gradients
  * may be shared; an output that overlaps another matrix's data is refused (PURO_ERR_ARG).
